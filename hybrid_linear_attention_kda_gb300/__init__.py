@@ -108,8 +108,9 @@ def load():
     lib.kda_snapshot_restore.argtypes = [vp, vp, i64, vp, i32, i32, i32, i32, vp]
     lib.kda_check_status.restype = ctypes.c_int
     lib.kda_check_status.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_uint32)]
-    from . import prefix_cache
+    from . import attention, prefix_cache
     prefix_cache.declare(lib)
+    attention.declare(lib)
     _lib = lib
     return lib
 
@@ -408,3 +409,17 @@ def prefill(q, k, v, alpha, beta, cu_seqlens, total_tokens=None, *, start_pos=No
         args.workspace_bytes = workspace.numel() * workspace.element_size()
     kda_prefill_chunked(args, stream)
     return o, final_state
+
+
+_ATTENTION = ("KDA_DEV_NO_BLOCKS", "KDA_DEV_BAD_GROUP", "CachePlanArgs", "AttnPrefillArgs", "AttnDecodeArgs", "CachePlan",
+              "kda_cache_plan", "kda_cache_append", "kda_attn_prefill", "kda_attn_decode",
+              "kda_attn_decode_workspace_size", "cache_plan", "attn_prefill", "attn_prefill_paged", "attn_decode")
+
+
+def __getattr__(name):
+    """The attention side's names, from ``attention`` (which imports torch) on first use."""
+    if name in _ATTENTION:
+        from . import attention
+        globals().update({n: getattr(attention, n) for n in _ATTENTION})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

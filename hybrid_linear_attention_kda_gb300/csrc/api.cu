@@ -9,6 +9,7 @@
 #include <thread>
 #include <vector>
 
+#include "attn_common.cuh"
 #include "chunk_common.cuh"
 #include "kda_prefix_cache.h"
 
@@ -191,6 +192,8 @@ std::atomic<uint64_t> g_launches{0};
 void kda::note_launch(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 kda_status_t kda::record_error(kda_status_t status, const char* message) { return fail(status, "%s", message); }
+
+kda_status_t kda::device_status_word(uint32_t** out) { return status_ptr(out); }
 
 extern "C" {
 

@@ -1,0 +1,309 @@
+// C entry points of kda_attention.h: argument checks and dispatch.
+#include <cstdarg>
+#include <cmath>
+#include <cstdio>
+
+#include "attn_common.cuh"
+
+namespace {
+
+kda_status_t fail(kda_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+kda_status_t fail(kda_status_t st, const char* fmt, ...) {
+    char text[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(text, sizeof text, fmt, ap);
+    va_end(ap);
+    return kda::record_error(st, text);
+}
+
+kda_status_t cuda_fail(cudaError_t e, const char* what) {
+    return fail(KDA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+#define KDA_TRY(call)                       \
+    do {                                    \
+        const kda_status_t st_ = (call);    \
+        if (st_ != KDA_OK) return st_;      \
+    } while (0)
+
+kda_status_t check_ptr(const void* p, const char* name) {
+    if (!p) return fail(KDA_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return fail(KDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    return KDA_OK;
+}
+
+// Single integers need only their own alignment.
+kda_status_t check_int(const void* p, const char* name) {
+    if (!p) return fail(KDA_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(KDA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+    return KDA_OK;
+}
+
+constexpr int64_t kMaxSeqs = 1 << 20;
+constexpr int64_t kMaxHeads = 4096, kMaxGroup = 128;
+
+kda_status_t check_heads(int32_t H, int32_t H_kv, int32_t d, int32_t dtype) {
+    if (H_kv <= 0 || H <= 0 || H % H_kv) return fail(KDA_ERR_INVALID_ARG, "n_heads %d must be a positive multiple of n_kv_heads %d", H, H_kv);
+    if (H > kMaxHeads || H / H_kv > kMaxGroup)
+        return fail(KDA_ERR_UNSUPPORTED, "at most %d heads and %d query heads per key/value head (got %d, %d)", (int)kMaxHeads, (int)kMaxGroup, H, H / H_kv);
+    if (d != 64 && d != 128) return fail(KDA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", d);
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return fail(KDA_ERR_UNSUPPORTED, "dtype %d", dtype);
+    return KDA_OK;
+}
+
+int esize(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }
+
+kda_status_t check_stride(int64_t stride, int64_t heads, int32_t d, int32_t dtype, const char* name) {
+    if (stride < heads * d || stride * esize(dtype) % 16 || stride > (int64_t)INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "%s %lld must be a multiple of 16 bytes, at least %lld and below 2^31", name,
+                    (long long)stride, (long long)heads * d);
+    return KDA_OK;
+}
+
+kda_status_t check_block_size(int32_t bs) {
+    if (bs != 16 && bs != 32 && bs != 64 && bs != 128 && bs != 256)
+        return fail(KDA_ERR_UNSUPPORTED, "block_size must be 16, 32, 64, 128 or 256 (got %d)", bs);
+    return KDA_OK;
+}
+
+kda_status_t check_cache_size(int64_t n_blocks, int32_t bs, int32_t H_kv) {
+    if (n_blocks <= 0 || n_blocks > (int64_t)INT32_MAX / ((int64_t)bs * H_kv))
+        return fail(KDA_ERR_INVALID_ARG, "n_blocks %lld must be positive, with n_blocks * block_size * n_kv_heads < 2^31", (long long)n_blocks);
+    return KDA_OK;
+}
+
+kda_status_t check_seqs(int32_t n, const char* name) {
+    if (n < 0 || n > kMaxSeqs) return fail(KDA_ERR_INVALID_ARG, "%s %d outside [0, %lld]", name, n, (long long)kMaxSeqs);
+    return KDA_OK;
+}
+
+kda_status_t check_table(int32_t stride, int32_t bs) {
+    if (stride < 1 || (int64_t)stride * bs > (int64_t)INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "table_stride %d must be positive, with table_stride * block_size < 2^31", stride);
+    return KDA_OK;
+}
+
+kda_status_t check_scale(float scale) {
+    if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    return KDA_OK;
+}
+
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Thread blocks of the suffix kernel: three on each of the 152 SMs.
+constexpr int kDecodeCtas = 456;
+
+// Blocks of keys that a shared prefix is cut into: enough row tiles times blocks
+// for two on each SM, at most 64.
+int prefix_splits(const kda_attn_decode_args& a) {
+    if (a.n_groups == 0) return 0;
+    const int64_t G = a.n_heads / a.n_kv_heads;
+    const int64_t items = ((int64_t)a.n_seqs * G / 64 + a.n_groups) * a.n_kv_heads;
+    const int64_t n = (304 + items - 1) / items;
+    return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
+struct DecodeSpace {
+    size_t pre_o, pre_ml, part_o, part_ml, tiles, info, bytes;
+};
+
+DecodeSpace decode_space(const kda_attn_decode_args& a) {
+    DecodeSpace s{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t r = at;
+        at += round_up(bytes);
+        return r;
+    };
+    const size_t rows = (size_t)a.n_seqs * a.n_heads * prefix_splits(a);
+    const size_t parts = (size_t)2 * kDecodeCtas * kda::attn_decode_rows(a.dtype);
+    s.pre_o = take(rows * a.d * sizeof(float));
+    s.pre_ml = take(rows * sizeof(float2));
+    s.part_o = take(parts * a.d * sizeof(float));
+    s.part_ml = take(parts * sizeof(float2));
+    s.tiles = take(((size_t)a.n_seqs + 1) * sizeof(int64_t));
+    s.info = take((size_t)a.n_seqs * sizeof(int2));
+    s.bytes = at;
+    return s;
+}
+
+kda_status_t check_decode_sizes(const kda_attn_decode_args& a) {
+    KDA_TRY(check_heads(a.n_heads, a.n_kv_heads, a.d, a.dtype));
+    KDA_TRY(check_seqs(a.n_seqs, "n_seqs"));
+    KDA_TRY(check_seqs(a.n_groups, "n_groups"));
+    if ((int64_t)a.n_seqs * a.n_heads > (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "n_seqs * n_heads too large");
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_cache_plan(const kda_cache_plan_args* args, void* stream) {
+    if (!args) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    const kda_cache_plan_args& a = *args;
+    KDA_TRY(check_seqs(a.n_seqs, "n_seqs"));
+    KDA_TRY(check_block_size(a.block_size));
+    KDA_TRY(check_table(a.table_stride, a.block_size));
+    KDA_TRY(check_cache_size(a.n_blocks, a.block_size, 1));
+    if (a.n_free < 0) return fail(KDA_ERR_INVALID_ARG, "n_free < 0");
+    if (a.max_tokens < 0 || a.max_tokens > (int64_t)INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "max_tokens %lld outside [0, 2^31)", (long long)a.max_tokens);
+    KDA_TRY(check_int(a.free_begin, "free_begin"));
+    KDA_TRY(check_int(a.free_end, "free_end"));
+    if (a.free_begin == a.free_end) return fail(KDA_ERR_INVALID_ARG, "free_begin and free_end must differ");
+    if (a.n_free > 0) KDA_TRY(check_int(a.free_blocks, "free_blocks"));
+    KDA_TRY(check_int(a.cu_seqlens, "cu_seqlens"));
+    if (a.n_seqs > 0) {
+        KDA_TRY(check_int(a.cached_lens, "cached_lens"));
+        KDA_TRY(check_int(a.new_lens, "new_lens"));
+        KDA_TRY(check_int(a.block_table, "block_table"));
+        KDA_TRY(check_int(a.kv_lens, "kv_lens"));
+    }
+    if (a.max_tokens > 0) {
+        KDA_TRY(check_int(a.slot_map, "slot_map"));
+        KDA_TRY(check_int(a.positions, "positions"));
+    }
+    kda::CachePlanLaunch p{a, nullptr};
+    KDA_TRY(kda::device_status_word(&p.status));
+    const cudaError_t e = kda::launch_cache_plan(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache plan launch");
+}
+
+kda_status_t kda_cache_append(int64_t n_tokens, int32_t n_kv_heads, int32_t d, int32_t dtype, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slot_map,
+                              void* k_cache, void* v_cache, int64_t n_blocks, int32_t block_size, void* stream) {
+    KDA_TRY(check_heads(n_kv_heads, n_kv_heads, d, dtype));
+    KDA_TRY(check_block_size(block_size));
+    KDA_TRY(check_cache_size(n_blocks, block_size, n_kv_heads));
+    KDA_TRY(check_stride(k_stride, n_kv_heads, d, dtype, "k_stride"));
+    KDA_TRY(check_stride(v_stride, n_kv_heads, d, dtype, "v_stride"));
+    if (n_tokens < 0 || n_tokens > (int64_t)INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "n_tokens %lld outside [0, 2^31)", (long long)n_tokens);
+    if (n_tokens == 0) return KDA_OK;
+    KDA_TRY(check_ptr(k, "k"));
+    KDA_TRY(check_ptr(v, "v"));
+    KDA_TRY(check_int(slot_map, "slot_map"));
+    KDA_TRY(check_ptr(k_cache, "k_cache"));
+    KDA_TRY(check_ptr(v_cache, "v_cache"));
+    const int vec = 16 / esize(dtype);
+    kda::CacheAppendLaunch p{n_tokens, n_kv_heads, n_kv_heads * (d / vec), d / vec, k, v, k_stride / vec, v_stride / vec,
+                             slot_map, k_cache, v_cache, n_blocks, block_size, nullptr};
+    if (n_tokens * 2 * p.row_vecs / 1024 >= (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "n_tokens * n_kv_heads * d too large");
+    KDA_TRY(kda::device_status_word(&p.status));
+    const cudaError_t e = kda::launch_cache_append(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache append launch");
+}
+
+kda_status_t kda_attn_prefill(const kda_attn_prefill_args* args, void* stream) {
+    if (!args) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    const kda_attn_prefill_args& a = *args;
+    KDA_TRY(check_heads(a.n_heads, a.n_kv_heads, a.d, a.dtype));
+    KDA_TRY(check_seqs(a.n_seqs, "n_seqs"));
+    KDA_TRY(check_scale(a.scale));
+    if (a.total_tokens < 0 || a.total_tokens > (int64_t)INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "total_tokens %lld outside [0, 2^31)", (long long)a.total_tokens);
+    KDA_TRY(check_stride(a.q_stride, a.n_heads, a.d, a.dtype, "q_stride"));
+    KDA_TRY(check_stride(a.o_stride, a.n_heads, a.d, a.dtype, "o_stride"));
+    if (a.block_table) {
+        KDA_TRY(check_block_size(a.block_size));
+        KDA_TRY(check_table(a.table_stride, a.block_size));
+        KDA_TRY(check_cache_size(a.n_blocks, a.block_size, a.n_kv_heads));
+    } else {
+        KDA_TRY(check_stride(a.k_stride, a.n_kv_heads, a.d, a.dtype, "k_stride"));
+        KDA_TRY(check_stride(a.v_stride, a.n_kv_heads, a.d, a.dtype, "v_stride"));
+    }
+    // one thread block for each tile of at least one token
+    if ((a.total_tokens + a.n_seqs) * 2 > (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "total_tokens + n_seqs too large");
+    if (a.n_seqs == 0 || a.total_tokens == 0) return KDA_OK;
+    KDA_TRY(check_ptr(a.q, "q"));
+    KDA_TRY(check_ptr(a.o, "o"));
+    KDA_TRY(check_int(a.cu_seqlens, "cu_seqlens"));
+    if (a.lse) KDA_TRY(check_int(a.lse, "lse"));
+    if (a.block_table) {
+        KDA_TRY(check_ptr(a.k_cache, "k_cache"));
+        KDA_TRY(check_ptr(a.v_cache, "v_cache"));
+        KDA_TRY(check_int(a.block_table, "block_table"));
+        KDA_TRY(check_int(a.kv_lens, "kv_lens"));
+    } else {
+        KDA_TRY(check_ptr(a.k, "k"));
+        KDA_TRY(check_ptr(a.v, "v"));
+    }
+    kda::AttnTileLaunch p{a, nullptr, nullptr, 0, nullptr, nullptr};
+    KDA_TRY(kda::device_status_word(&p.status));
+    const cudaError_t e = kda::launch_attn_simt(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "prompt attention launch");
+}
+
+size_t kda_attn_decode_workspace_size(const kda_attn_decode_args* args) {
+    if (!args || check_decode_sizes(*args) != KDA_OK || args->n_seqs == 0) return 0;
+    return decode_space(*args).bytes;
+}
+
+kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
+    if (!args) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
+    const kda_attn_decode_args& a = *args;
+    KDA_TRY(check_decode_sizes(a));
+    KDA_TRY(check_scale(a.scale));
+    if (a.reserved0 != 0) return fail(KDA_ERR_INVALID_ARG, "reserved0 must be 0");
+    KDA_TRY(check_block_size(a.block_size));
+    KDA_TRY(check_table(a.table_stride, a.block_size));
+    KDA_TRY(check_cache_size(a.n_blocks, a.block_size, a.n_kv_heads));
+    KDA_TRY(check_stride(a.q_stride, a.n_heads, a.d, a.dtype, "q_stride"));
+    KDA_TRY(check_stride(a.o_stride, a.n_heads, a.d, a.dtype, "o_stride"));
+    if (a.n_seqs == 0) return KDA_OK;
+    KDA_TRY(check_ptr(a.q, "q"));
+    KDA_TRY(check_ptr(a.o, "o"));
+    KDA_TRY(check_ptr(a.k_cache, "k_cache"));
+    KDA_TRY(check_ptr(a.v_cache, "v_cache"));
+    KDA_TRY(check_int(a.block_table, "block_table"));
+    KDA_TRY(check_int(a.kv_lens, "kv_lens"));
+    if (a.lse) KDA_TRY(check_int(a.lse, "lse"));
+    if (a.n_groups > 0) {
+        KDA_TRY(check_int(a.group_start, "group_start"));
+        KDA_TRY(check_int(a.prefix_lens, "prefix_lens"));
+    }
+    const DecodeSpace sp = decode_space(a);
+    if (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u))
+        return fail(KDA_ERR_INVALID_ARG, "workspace is NULL or not 256-byte aligned");
+    if (a.workspace_bytes < sp.bytes)
+        return fail(KDA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", a.workspace_bytes, sp.bytes);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    kda::AttnDecodeLaunch p{};
+    p.a = a;
+    p.n_ctas = kDecodeCtas;
+    p.n_split = prefix_splits(a);
+    p.pre_o = reinterpret_cast<float*>(ws + sp.pre_o);
+    p.pre_ml = reinterpret_cast<float2*>(ws + sp.pre_ml);
+    p.part_o = reinterpret_cast<float*>(ws + sp.part_o);
+    p.part_ml = reinterpret_cast<float2*>(ws + sp.part_ml);
+    p.tiles = reinterpret_cast<int64_t*>(ws + sp.tiles);
+    p.info = reinterpret_cast<int2*>(ws + sp.info);
+    KDA_TRY(kda::device_status_word(&p.status));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.n_groups > 0) {
+        kda::AttnTileLaunch t{};
+        t.a.n_seqs = a.n_groups;
+        t.a.n_heads = a.n_heads, t.a.n_kv_heads = a.n_kv_heads, t.a.d = a.d, t.a.dtype = a.dtype;
+        t.a.scale = a.scale;
+        t.a.total_tokens = a.n_seqs;
+        t.a.q_stride = a.q_stride;
+        t.a.q = a.q;
+        t.a.cu_seqlens = a.group_start;
+        t.a.k_cache = a.k_cache, t.a.v_cache = a.v_cache;
+        t.a.block_table = a.block_table;
+        t.a.n_blocks = a.n_blocks, t.a.block_size = a.block_size, t.a.table_stride = a.table_stride;
+        t.status = p.status;
+        t.prefix_lens = a.prefix_lens;
+        t.n_split = p.n_split;
+        t.part_o = p.pre_o;
+        t.part_ml = p.pre_ml;
+        const cudaError_t e = kda::launch_attn_simt(t, s);
+        if (e != cudaSuccess) return cuda_fail(e, "shared-prefix attention launch");
+    }
+    const cudaError_t e = kda::launch_attn_decode(p, s);
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "decode attention launch");
+}
+
+}  // extern "C"

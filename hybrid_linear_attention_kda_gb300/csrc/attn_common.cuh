@@ -1,0 +1,147 @@
+// Shared by the softmax-attention and paged-cache kernels (not part of the C ABI).
+#pragma once
+
+#include "kda_attention.h"
+#include "kda_common.cuh"
+
+namespace kda {
+
+// Address of the current device's status word (api.cu).
+kda_status_t device_status_word(uint32_t** out);
+
+// ------------------------------------------------------------------ block scan
+
+// Inclusive scan of one value per thread over a block of NT threads; every thread
+// gets its prefix sum and the block's total.  `buf` holds NT / 32 values.
+template <int NT, typename V>
+__device__ __forceinline__ V block_scan(V x, V* buf, V* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const V y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    __syncthreads();                        // the previous scan's readers are done with buf
+    if (lane == 31) buf[warp] = x;
+    __syncthreads();
+    V before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const V t = buf[w];
+        before += w < warp ? t : 0;
+        all += t;
+    }
+    *total = all;
+    return x + before;
+}
+
+// ------------------------------------------------------------------ row tiles
+
+// Attention rows.  The query heads of one key/value head see the same keys, so a
+// tile of rows takes whole tokens with all G of those heads: row r of a tile is
+// (token r / G, head r % G).  A tile of R rows therefore covers R / G tokens, and
+// a tile of keys is loaded once for all of its rows.  Works the same for a prompt
+// (tokens of one sequence) and for a shared prefix (the members of one group, one
+// query each).
+struct RowTile {
+    int32_t seq;      // sequence (or group); -1: no such tile
+    int32_t t0;       // first token (or member) within it
+    int32_t n;        // its tokens
+    int64_t row0;     // packed row of its first token
+};
+
+// The idx-th tile of `tile_tokens` tokens over the sequences cu[0] .. cu[n_seqs].
+// Tiles of one sequence come last first: the later ones see more keys.  Called by
+// a whole block of NT threads; bad sequences have no tiles and are flagged by the
+// caller that passes report.
+template <int NT>
+__device__ RowTile find_tile(const int32_t* cu, int32_t n_seqs, int64_t total_tokens, int32_t tile_tokens,
+                             int64_t idx, bool report, uint32_t bit, uint32_t* status) {
+    __shared__ int64_t scan_buf[NT / 32];
+    __shared__ RowTile found;
+    if (threadIdx.x == 0) found.seq = -1;
+    int64_t base = 0;
+    for (int32_t s0 = 0; s0 < n_seqs; s0 += NT) {
+        const int32_t s = s0 + (int32_t)threadIdx.x;
+        int64_t a = 0, b = 0;
+        if (s < n_seqs) {
+            a = cu[s];
+            b = cu[s + 1];
+            if (a < 0 || b < a || b > total_tokens) {
+                if (report) flag(status, bit);
+                b = a;
+            }
+        }
+        const int64_t tiles = (b - a + tile_tokens - 1) / tile_tokens;
+        int64_t total;
+        const int64_t incl = block_scan<NT>(tiles, scan_buf, &total) + base;
+        if (idx < incl && idx >= incl - tiles) {
+            found.seq = s;
+            found.t0 = (int32_t)(incl - 1 - idx) * tile_tokens;
+            found.n = (int32_t)(b - a);
+            found.row0 = a;
+        }
+        base += total;
+        if (base > idx && !report) break;
+    }
+    __syncthreads();
+    return found;
+}
+
+// ------------------------------------------------------------------ launches
+
+struct AttnTileLaunch {
+    kda_attn_prefill_args a;      // q, strides, caches, ...; cu_seqlens = group_start for a shared prefix
+    uint32_t* status;
+    // shared prefixes only: keys 0 .. prefix_lens[g] of the group's first row, split over n_split blocks of keys,
+    // partial results to part_o [n_split, total_tokens, H, d] and part_ml [n_split, total_tokens, H] (m, l)
+    const int32_t* prefix_lens;
+    int32_t n_split;
+    float* part_o;
+    float2* part_ml;
+};
+
+// Prompt attention, and the shared-prefix part of decode attention (prefix_lens set).
+cudaError_t launch_attn_simt(const AttnTileLaunch& p, cudaStream_t s);
+
+// Decode attention.  The keys that a sequence does not share (its suffix) are cut
+// into tiles; all tiles of all units (sequence, key/value head, block of query
+// heads) form one line in that order, and thread block c of n_ctas takes an equal
+// piece of it.  A unit whose tiles fall into several pieces, or that has a shared
+// prefix, leaves partial results (m, l, unnormalised o) and the join adds them up
+// in a fixed order: the prefix's blocks of keys, then the pieces from first to last.
+struct AttnDecodeLaunch {
+    kda_attn_decode_args a;
+    uint32_t* status;
+    int32_t n_ctas;               // thread blocks of the suffix kernel
+    int32_t n_split;              // key blocks of the prefix (0: no groups)
+    float* pre_o;                 // [n_split, n_seqs, H, d] the prefix's partial results
+    float2* pre_ml;               // [n_split, n_seqs, H]
+    float* part_o;                // [2 * n_ctas, rows, d]: a piece's first unit, its last unit
+    float2* part_ml;              // [2 * n_ctas, rows]
+    int64_t* tiles;               // [n_seqs + 1] suffix tiles of one unit, summed over the earlier sequences
+    int2* info;                   // [n_seqs] (shared positions, all positions)
+};
+cudaError_t launch_attn_decode(const AttnDecodeLaunch& p, cudaStream_t s);
+int attn_decode_rows(int dtype);  // query heads of one unit
+
+struct CachePlanLaunch {
+    kda_cache_plan_args a;
+    uint32_t* status;
+};
+cudaError_t launch_cache_plan(const CachePlanLaunch& p, cudaStream_t s);
+
+struct CacheAppendLaunch {
+    int64_t n_tokens;
+    int32_t n_kv_heads, row_vecs, head_vecs;   // 16-byte pieces of one token's heads, of one head
+    const void *k, *v;
+    int64_t k_stride, v_stride;                // 16-byte pieces
+    const int32_t* slot_map;
+    void *k_cache, *v_cache;
+    int64_t n_blocks;
+    int32_t block_size;
+    uint32_t* status;
+};
+cudaError_t launch_cache_append(const CacheAppendLaunch& p, cudaStream_t s);
+
+}  // namespace kda

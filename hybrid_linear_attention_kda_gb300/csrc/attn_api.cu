@@ -94,13 +94,15 @@ size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 // Thread blocks of the suffix kernel: three on each of the 152 SMs.
 constexpr int kDecodeCtas = 456;
 
-// Blocks of keys that a shared prefix is cut into: enough row tiles times blocks
-// for two on each SM, at most 64.
+// Blocks of keys that a shared prefix is cut into: enough row tiles (256 rows in
+// bf16, 64 in fp32) times blocks for the thread blocks that run at once (one on
+// each of 152 SMs, two), at most 64.
 int prefix_splits(const kda_attn_decode_args& a) {
     if (a.n_groups == 0) return 0;
+    const bool bf16 = a.dtype == KDA_BF16;
     const int64_t G = a.n_heads / a.n_kv_heads;
-    const int64_t items = ((int64_t)a.n_seqs * G / 64 + a.n_groups) * a.n_kv_heads;
-    const int64_t n = (304 + items - 1) / items;
+    const int64_t items = ((int64_t)a.n_seqs * G / (bf16 ? 256 : 64) + a.n_groups) * a.n_kv_heads;
+    const int64_t n = ((bf16 ? 152 : 304) + items - 1) / items;
     return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 
@@ -232,7 +234,7 @@ kda_status_t kda_attn_prefill(const kda_attn_prefill_args* args, void* stream) {
     }
     kda::AttnTileLaunch p{a, nullptr, nullptr, 0, nullptr, nullptr};
     KDA_TRY(kda::device_status_word(&p.status));
-    const cudaError_t e = kda::launch_attn_simt(p, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = kda::launch_attn_tile(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "prompt attention launch");
 }
 
@@ -299,7 +301,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
         t.n_split = p.n_split;
         t.part_o = p.pre_o;
         t.part_ml = p.pre_ml;
-        const cudaError_t e = kda::launch_attn_simt(t, s);
+        const cudaError_t e = kda::launch_attn_tile(t, s);
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix attention launch");
     }
     const cudaError_t e = kda::launch_attn_decode(p, s);

@@ -102,7 +102,11 @@ struct AttnTileLaunch {
 };
 
 // Prompt attention, and the shared-prefix part of decode attention (prefix_lens set).
-cudaError_t launch_attn_simt(const AttnTileLaunch& p, cudaStream_t s);
+cudaError_t launch_attn_simt(const AttnTileLaunch& p, cudaStream_t s);   // fp32
+cudaError_t launch_attn_tc(const AttnTileLaunch& p, cudaStream_t s);     // bf16
+inline cudaError_t launch_attn_tile(const AttnTileLaunch& p, cudaStream_t s) {
+    return p.a.dtype == KDA_BF16 ? launch_attn_tc(p, s) : launch_attn_simt(p, s);
+}
 
 // Decode attention.  The keys that a sequence does not share (its suffix) are cut
 // into tiles; all tiles of all units (sequence, key/value head, block of query

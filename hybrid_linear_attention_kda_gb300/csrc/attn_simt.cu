@@ -1,5 +1,5 @@
-// Softmax attention of row tiles in fp32 SIMT arithmetic: prompts (causal) and the
-// shared prefixes of decode attention.
+// Softmax attention of row tiles for fp32 tensors, in SIMT arithmetic: prompts (causal)
+// and the shared prefixes of decode attention.
 //
 // For the rows i of a tile and the keys j that row i sees (x_ij = scale q_i . k_j):
 //     m = max_j x_ij,  l = sum_j exp(x_ij - m),  o_i = sum_j exp(x_ij - m) v_j / l
@@ -30,19 +30,9 @@ template <int D> constexpr size_t smem_bytes() {
 }
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
-template <typename T, int D, int MODE>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, int32_t Gp, int32_t chunks) {
     extern __shared__ __align__(16) float smem[];
     float* Qs = smem;
@@ -91,10 +81,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
         k_hi = min(K, k_lo + per);
     }
 
-    auto key_row = [&](int64_t j, const T*& kr, const T*& vr) -> bool {
+    auto key_row = [&](int64_t j, const float*& kr, const float*& vr) -> bool {
         if (MODE == kPacked) {
-            kr = static_cast<const T*>(a.k) + (rt.row0 + j) * a.k_stride + hk * D;
-            vr = static_cast<const T*>(a.v) + (rt.row0 + j) * a.v_stride + hk * D;
+            kr = static_cast<const float*>(a.k) + (rt.row0 + j) * a.k_stride + hk * D;
+            vr = static_cast<const float*>(a.v) + (rt.row0 + j) * a.v_stride + hk * D;
             return true;
         }
         const int32_t block = table[j / a.block_size];
@@ -103,8 +93,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
             return false;
         }
         const int64_t e = (((int64_t)block * a.n_kv_heads + hk) * a.block_size + j % a.block_size) * D;
-        kr = static_cast<const T*>(a.k_cache) + e;
-        vr = static_cast<const T*>(a.v_cache) + e;
+        kr = static_cast<const float*>(a.k_cache) + e;
+        vr = static_cast<const float*>(a.v_cache) + e;
         return true;
     };
 
@@ -114,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
         const int t = r / Gp, g = r % Gp;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t < nt && g < gn)
-            x = load4(static_cast<const T*>(a.q) + (rt.row0 + rt.t0 + t) * a.q_stride + (head0 + g) * D + c);
+            x = load4(static_cast<const float*>(a.q) + (rt.row0 + rt.t0 + t) * a.q_stride + (head0 + g) * D + c);
         store4(Qs + r * kPad<D> + c, x);
     }
 
@@ -137,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
         for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
             const int j = i / (D / 4), c = i % (D / 4) * 4;
             float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-            const T *kr, *vr;
+            const float *kr, *vr;
             if (k0 + j < k_hi && key_row(k0 + j, kr, vr)) {
                 kx = load4(kr + c);
                 vx = load4(vr + c);
@@ -235,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
             if (tx == 0) p.part_ml[at] = make_float2(m[r], l[r]);
         } else {
             const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-            T* out = static_cast<T*>(a.o) + row * a.o_stride + (int64_t)head * D;
+            float* out = static_cast<float*>(a.o) + row * a.o_stride + (int64_t)head * D;
 #pragma unroll
             for (int c = 0; c < OC; ++c)
                 store4(out + 4 * tx + 64 * c, make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv));
@@ -244,33 +234,31 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
     }
 }
 
-template <typename T, int D, int MODE>
+template <int D, int MODE>
 cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
     const kda_attn_prefill_args& a = p.a;
     const int G = a.n_heads / a.n_kv_heads, Gp = G < kRows ? G : kRows, chunks = (G + Gp - 1) / Gp;
     int64_t tiles = a.total_tokens / (kRows / Gp) + a.n_seqs;
     if (MODE == kPrefix) tiles *= p.n_split;
-    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
     note_launch();
-    attn_simt_kernel<T, D, MODE><<<dim3((unsigned)tiles, (unsigned)(a.n_kv_heads * chunks)), kThreads, smem_bytes<D>(), s>>>(
+    attn_simt_kernel<D, MODE><<<dim3((unsigned)tiles, (unsigned)(a.n_kv_heads * chunks)), kThreads, smem_bytes<D>(), s>>>(
         p, Gp, chunks);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_d(const AttnTileLaunch& p, cudaStream_t s) {
-    if (p.prefix_lens) return launch_t<T, D, kPrefix>(p, s);
-    return p.a.block_table ? launch_t<T, D, kPaged>(p, s) : launch_t<T, D, kPacked>(p, s);
+    if (p.prefix_lens) return launch_t<D, kPrefix>(p, s);
+    return p.a.block_table ? launch_t<D, kPaged>(p, s) : launch_t<D, kPacked>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_simt(const AttnTileLaunch& p, cudaStream_t s) {
-    if (p.a.dtype == KDA_BF16)
-        return p.a.d == 128 ? launch_d<__nv_bfloat16, 128>(p, s) : launch_d<__nv_bfloat16, 64>(p, s);
-    return p.a.d == 128 ? launch_d<float, 128>(p, s) : launch_d<float, 64>(p, s);
+    return p.a.d == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
 }
 
 }  // namespace kda

@@ -6,10 +6,11 @@ errors.  q, k and v may be views of a fused projection's output: the heads of on
 dense, the tokens evenly spaced.
 """
 import collections
-import contextlib
 import ctypes
 
 import torch
+
+import hybrid_linear_attention_kda_gb300 as _kda
 
 KDA_DEV_NO_BLOCKS, KDA_DEV_BAD_GROUP = 0x40, 0x80
 
@@ -73,62 +74,89 @@ def declare(lib):
     lib.kda_attn_decode.argtypes = [P(AttnDecodeArgs), vp]
 
 
-def _base():
-    import hybrid_linear_attention_kda_gb300 as kda
-    return kda
-
-
 _FLOATS = (torch.bfloat16, torch.float32)
+_I32, _F32, _Tensor = torch.int32, torch.float32, torch.Tensor
 
 
-def _tokens(x, name, dtype, heads, d, device, rows=None):
+def _shape(x, name, ndim):
+    """``_kda._dims``, without a copy where the rank is right."""
+    if type(x) is _Tensor and x.dim() == ndim:
+        return x.shape
+    return _kda._dims(x, name, ndim)
+
+
+def _dev(x, name, dtype, shape, dev, index):
+    """``_kda._dev`` of a tensor that must have this dtype, shape and device (of index
+    ``index``).  A serving step makes these calls for every layer, so what passes is
+    settled in one expression; what does not goes through the checks that name the fault."""
+    if type(x) is _Tensor and x.dtype is dtype and x.shape == shape and x.get_device() == index and x.is_contiguous():
+        return x.data_ptr()
+    return _kda._dev(x, name, dtype, shape, dev)
+
+
+def _tokens(x, name, dtype, shape, dev=None):
     """(address, elements between tokens) of a [T, heads, d] tensor whose tokens are
     evenly spaced and whose heads are dense."""
+    T, heads, d = shape
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor (got {type(x).__name__})")
-    allowed = dtype if isinstance(dtype, tuple) else (dtype,)
-    if x.dtype not in allowed:
-        raise TypeError(f"{name} must be {' or '.join(str(t) for t in allowed)} (got {x.dtype})")
-    want = (x.shape[0] if rows is None and x.dim() else rows, heads, d)
-    if tuple(x.shape) != want:
-        raise ValueError(f"{name} must have shape {want} (got {tuple(x.shape)})")
+    if x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {x.dtype})")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(x.shape)})")
     stride, inner, last = x.stride()
     if (last != 1 and d > 1) or (inner != d and heads > 1):
         raise ValueError(f"{name}'s heads must be dense within a token (strides {x.stride()})")
-    if x.shape[0] <= 1:
+    if T <= 1:
         stride = heads * d
-    if stride < heads * d:
+    elif stride < heads * d:
         raise ValueError(f"{name}'s tokens overlap (strides {x.stride()})")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (got {x.device})")
-    if device is not None and x.device != device:
-        raise ValueError(f"{name} is on {x.device}, the other operands on {device}")
+    if dev is not None and x.device != dev:
+        raise ValueError(f"{name} is on {x.device}, the other operands on {dev}")
     return x.data_ptr(), stride
 
 
-@contextlib.contextmanager
-def _on(stream, device):
-    """Make ``stream`` current, so that what is allocated inside belongs to it."""
+def _first(x, name):
+    """(shape, address, stride, device, device index, dtype code) of the tensor that the others
+    have to match."""
+    shape = _shape(x, name, 3)
+    if x.dtype not in _FLOATS:
+        raise TypeError(f"{name} must be {_FLOATS[0]} or {_FLOATS[1]} (got {x.dtype})")
+    ptr, stride = _tokens(x, name, x.dtype, shape)
+    return shape, ptr, stride, x.device, x.get_device(), _kda._dtype_code(x)
+
+
+def _on_stream(stream, dev, call):
+    """``call(handle)`` with ``stream`` current, so that what is allocated inside belongs to it."""
     if stream is None:
-        yield
-        return
+        return call(_current_stream(dev))
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = torch.cuda.ExternalStream(stream, device=dev)
     with torch.cuda.stream(stream):
-        yield
+        return call(stream.cuda_stream)
 
 
-def _cache(kda, k_cache, v_cache, dtype, heads, d, dev):
+def _current_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):          # the handle without a Stream object around it
+    def _current_stream(dev):                                # noqa: F811
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _cache(k_cache, v_cache, dtype, heads, d, dev, index):
     """(addresses, n_blocks, block_size) of the paged cache."""
-    n_blocks, _, bs, _ = kda._dims(k_cache, "k_cache", 4)
+    n_blocks, _, bs, _ = _shape(k_cache, "k_cache", 4)
     shape = (n_blocks, heads, bs, d)
-    return (kda._dev(k_cache, "k_cache", dtype, shape, dev), kda._dev(v_cache, "v_cache", dtype, shape, dev),
+    return (_dev(k_cache, "k_cache", dtype, shape, dev, index), _dev(v_cache, "v_cache", dtype, shape, dev, index),
             n_blocks, bs)
 
 
 def kda_cache_plan(args: CachePlanArgs, stream=None):
-    kda = _base()
-    kda._check(kda.load().kda_cache_plan(ctypes.byref(args), kda._stream_handle(stream)))
+    _kda._check(_kda.load().kda_cache_plan(ctypes.byref(args), _kda._stream_handle(stream)))
 
 
 def cache_plan(cached_lens, new_lens, block_table, free_blocks, free_begin, free_end, *, block_size, n_blocks,
@@ -138,124 +166,124 @@ def cache_plan(cached_lens, new_lens, block_table, free_blocks, free_begin, free
     free_end int32 [1], two different tensors.  The outputs are allocated unless given.
     Returns a ``CachePlan`` of cu_seqlens [n + 1], kv_lens [n], slot_map and positions
     [max_tokens]."""
-    kda = _base()
-    n = kda._dims(cached_lens, "cached_lens", 1)[0]
-    rows, stride = kda._dims(block_table, "block_table", 2)
-    n_free = kda._dims(free_blocks, "free_blocks", 1)[0]
-    i32, T = torch.int32, int(max_tokens)
+    n, = _shape(cached_lens, "cached_lens", 1)
+    _, stride = _shape(block_table, "block_table", 2)
+    n_free, = _shape(free_blocks, "free_blocks", 1)
+    T = int(max_tokens)
     if T < 0:
         raise ValueError(f"max_tokens must be >= 0 (got {T})")
-    a = CachePlanArgs()
-    a.cached_lens = kda._dev(cached_lens, "cached_lens", i32, (n,))
-    dev = cached_lens.device
-    a.new_lens = kda._dev(new_lens, "new_lens", i32, (n,), dev)
-    a.block_table = kda._dev(block_table, "block_table", i32, (n, stride), dev)
-    a.free_blocks = kda._dev(free_blocks, "free_blocks", i32, (n_free,), dev)
-    a.free_begin = kda._dev(free_begin, "free_begin", i32, (1,), dev)
-    a.free_end = kda._dev(free_end, "free_end", i32, (1,), dev)
-    with _on(stream, dev):
-        def out(x, size):
-            return torch.empty(size, dtype=i32, device=dev) if x is None else x
-        plan = CachePlan(out(cu_seqlens, n + 1), out(kv_lens, n), out(slot_map, T), out(positions, T))
-        a.cu_seqlens = kda._dev(plan.cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
-        a.kv_lens = kda._dev(plan.kv_lens, "kv_lens", i32, (n,), dev)
-        a.slot_map = kda._dev(plan.slot_map, "slot_map", i32, (T,), dev)
-        a.positions = kda._dev(plan.positions, "positions", i32, (T,), dev)
-        a.n_seqs, a.block_size, a.table_stride, a.n_free = n, int(block_size), stride, n_free
-        a.n_blocks, a.max_tokens = int(n_blocks), T
-        kda_cache_plan(a, stream)
-    return plan
+    dev, ix = cached_lens.device, cached_lens.get_device()
+    ptrs = (_dev(cached_lens, "cached_lens", _I32, (n,), None, ix if ix >= 0 else None),
+            _dev(new_lens, "new_lens", _I32, (n,), dev, ix),
+            _dev(free_blocks, "free_blocks", _I32, (n_free,), dev, ix),
+            _dev(free_begin, "free_begin", _I32, (1,), dev, ix), _dev(free_end, "free_end", _I32, (1,), dev, ix),
+            _dev(block_table, "block_table", _I32, (n, stride), dev, ix))
+
+    def call(handle):
+        def out(x, name, size):
+            if x is None:
+                x = torch.empty(size, dtype=_I32, device=dev)
+                return x, x.data_ptr()
+            return x, _dev(x, name, _I32, (size,), dev, ix)
+        kv, kv_p = out(kv_lens, "kv_lens", n)
+        cu, cu_p = out(cu_seqlens, "cu_seqlens", n + 1)
+        slots, slots_p = out(slot_map, "slot_map", T)
+        pos, pos_p = out(positions, "positions", T)
+        a = CachePlanArgs(n, int(block_size), stride, n_free, int(n_blocks), T, *ptrs, kv_p, cu_p, slots_p, pos_p)
+        _kda._check(_kda.load().kda_cache_plan(ctypes.byref(a), handle))
+        return CachePlan(cu, kv, slots, pos)
+    return _on_stream(stream, dev, call)
 
 
 def kda_cache_append(k, v, slot_map, k_cache, v_cache, stream=None):
     """k_cache[slot] = k[t], v_cache[slot] = v[t] with slot = slot_map[t] (-1 skips the token).
     k, v [T, H_kv, d]; slot_map int32 [T]; caches [n_blocks, H_kv, block_size, d]."""
-    kda = _base()
-    T, H, d = kda._dims(k, "k", 3)
-    kp, ks = _tokens(k, "k", _FLOATS, H, d, None)
-    dev = k.device
-    vp, vs = _tokens(v, "v", k.dtype, H, d, dev, T)
-    sp = kda._dev(slot_map, "slot_map", torch.int32, (T,), dev)
-    kc, vc, n_blocks, bs = _cache(kda, k_cache, v_cache, k.dtype, H, d, dev)
-    kda._check(kda.load().kda_cache_append(T, H, d, kda._dtype_code(k), kp, ks, vp, vs, sp, kc, vc, n_blocks, bs,
-                                           kda._stream_handle(stream)))
+    shape, kp, ks, dev, ix, code = _first(k, "k")
+    T, H, d = shape
+    vp, vs = _tokens(v, "v", k.dtype, shape, dev)
+    sp = _dev(slot_map, "slot_map", _I32, (T,), dev, ix)
+    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, k.dtype, H, d, dev, ix)
+    handle = _current_stream(dev) if stream is None else _kda._stream_handle(stream)
+    _kda._check(_kda.load().kda_cache_append(T, H, d, code, kp, ks, vp, vs, sp, kc, vc, n_blocks, bs, handle))
 
 
 def kda_attn_prefill(args: AttnPrefillArgs, stream=None):
-    kda = _base()
-    kda._check(kda.load().kda_attn_prefill(ctypes.byref(args), kda._stream_handle(stream)))
+    _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(args), _kda._stream_handle(stream)))
 
 
-def _outputs(kda, a, q, o, lse, want_lse, dev):
-    T, H, d = q.shape
+def _outputs(q, shape, dev, ix, o, lse, want_lse):
+    """(o, its address and stride, lse, its address), allocated where they are not given."""
+    T, H, d = shape
     if o is None:
-        o = torch.empty((T, H, d), dtype=q.dtype, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    a.o, a.o_stride = _tokens(o, "o", q.dtype, H, d, dev, T)
-    a.lse = kda._opt_dev(lse, "lse", dtype=torch.float32, shape=(T, H), device=dev)
-    return o, lse
+        o = torch.empty(shape, dtype=q.dtype, device=dev)
+        op, os_ = o.data_ptr(), H * d
+    else:
+        op, os_ = _tokens(o, "o", q.dtype, shape, dev)
+    if lse is not None:
+        return o, op, os_, lse, _dev(lse, "lse", _F32, (T, H), dev, ix)
+    if not want_lse:
+        return o, op, os_, None, None
+    lse = torch.empty((T, H), dtype=_F32, device=dev)
+    return o, op, os_, lse, lse.data_ptr()
 
 
-def _prefill(kda, a, q, cu_seqlens, H_kv, scale, o, lse, want_lse, stream, dev):
-    T, H, d = q.shape
-    n = kda._dims(cu_seqlens, "cu_seqlens", 1)[0] - 1
-    a.cu_seqlens = kda._dev(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
-    a.n_seqs, a.n_heads, a.n_kv_heads, a.d = n, H, H_kv, d
-    a.dtype, a.total_tokens = kda._dtype_code(q), T
-    a.scale = float(d ** -0.5 if scale is None else scale)
-    with _on(stream, dev):
-        o, lse = _outputs(kda, a, q, o, lse, want_lse, dev)
-        kda_attn_prefill(a, stream)
-    return o, lse
+def _scale(scale, d):
+    return d ** -0.5 if scale is None else float(scale)
 
 
 def attn_prefill(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse=False, stream=None):
     """Causal attention over packed prompts (``kda_attn_prefill``): q [T, H, d]; k, v
     [T, H_kv, d]; cu_seqlens int32 [n + 1].  scale defaults to d^-0.5; o and lse are allocated
     unless given (tokens past cu_seqlens[n] are left unwritten).  Returns (o, lse or None)."""
-    kda = _base()
-    T, H, d = kda._dims(q, "q", 3)
-    H_kv = kda._dims(k, "k", 3)[1]
-    a = AttnPrefillArgs()
-    a.q, a.q_stride = _tokens(q, "q", _FLOATS, H, d, None)
-    dev = q.device
-    a.k, a.k_stride = _tokens(k, "k", q.dtype, H_kv, d, dev, T)
-    a.v, a.v_stride = _tokens(v, "v", q.dtype, H_kv, d, dev, T)
-    return _prefill(kda, a, q, cu_seqlens, H_kv, scale, o, lse, want_lse, stream, dev)
+    shape, qp, qs, dev, ix, code = _first(q, "q")
+    T, H, d = shape
+    H_kv = _shape(k, "k", 3)[1]
+    kp, ks = _tokens(k, "k", q.dtype, (T, H_kv, d), dev)
+    vp, vs = _tokens(v, "v", q.dtype, (T, H_kv, d), dev)
+    entries, = _shape(cu_seqlens, "cu_seqlens", 1)
+    cu = _dev(cu_seqlens, "cu_seqlens", _I32, (entries,), dev, ix)
+
+    def call(handle):
+        out, op, os_, z, zp = _outputs(q, shape, dev, ix, o, lse, want_lse)
+        a = AttnPrefillArgs(entries - 1, H, H_kv, d, code, _scale(scale, d), T, qs, ks, vs, os_, qp, kp, vp, op, zp, cu)
+        _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(a), handle))
+        return out, z
+    return _on_stream(stream, dev, call)
 
 
 def attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *, scale=None, o=None, lse=None,
                        want_lse=False, stream=None):
     """``attn_prefill`` with all keys and values in the paged cache: sequence s holds kv_lens[s]
     positions, the last of which are its queries.  caches [n_blocks, H_kv, block_size, d];
-    block_table int32 [n, stride]; kv_lens int32 [n].  Returns (o, lse or None)."""
-    kda = _base()
-    T, H, d = kda._dims(q, "q", 3)
-    H_kv = kda._dims(k_cache, "k_cache", 4)[1]
-    n, stride = kda._dims(block_table, "block_table", 2)
-    a = AttnPrefillArgs()
-    a.q, a.q_stride = _tokens(q, "q", _FLOATS, H, d, None)
-    dev = q.device
-    a.k_cache, a.v_cache, a.n_blocks, a.block_size = _cache(kda, k_cache, v_cache, q.dtype, H_kv, d, dev)
-    a.block_table = kda._dev(block_table, "block_table", torch.int32, (n, stride), dev)
-    a.kv_lens = kda._dev(kv_lens, "kv_lens", torch.int32, (n,), dev)
-    if kda._dims(cu_seqlens, "cu_seqlens", 1)[0] != n + 1:
-        raise ValueError(f"cu_seqlens must have {n + 1} entries (got {cu_seqlens.shape[0]})")
-    a.table_stride = stride
-    if n == 0:
-        a.block_table = a.kv_lens = None
-        a.k_stride = a.v_stride = H_kv * d
-    return _prefill(kda, a, q, cu_seqlens, H_kv, scale, o, lse, want_lse, stream, dev)
+    block_table int32 [n, stride]; kv_lens int32 [n]; cu_seqlens int32 [n + 1].  Returns (o, lse
+    or None)."""
+    shape, qp, qs, dev, ix, code = _first(q, "q")
+    T, H, d = shape
+    H_kv = _shape(k_cache, "k_cache", 4)[1]
+    n, stride = _shape(block_table, "block_table", 2)
+    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, q.dtype, H_kv, d, dev, ix)
+    table = _dev(block_table, "block_table", _I32, (n, stride), dev, ix)
+    kv = _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix)
+    cu = _dev(cu_seqlens, "cu_seqlens", _I32, (n + 1,), dev, ix)
+    if n and not stride:
+        raise ValueError("block_table must have at least one column")
+
+    def call(handle):
+        out, op, os_, z, zp = _outputs(q, shape, dev, ix, o, lse, want_lse)
+        if n and T:
+            a = AttnPrefillArgs(n, H, H_kv, d, code, _scale(scale, d), T, qs, 0, 0, os_, qp, None, None, op, zp, cu, kc, vc,
+                                table, kv, n_blocks, bs, stride)
+            _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(a), handle))
+        return out, z
+    return _on_stream(stream, dev, call)
 
 
 def kda_attn_decode_workspace_size(args: AttnDecodeArgs) -> int:
-    return int(_base().load().kda_attn_decode_workspace_size(ctypes.byref(args)))
+    return int(_kda.load().kda_attn_decode_workspace_size(ctypes.byref(args)))
 
 
 def kda_attn_decode(args: AttnDecodeArgs, stream=None):
-    kda = _base()
-    kda._check(kda.load().kda_attn_decode(ctypes.byref(args), kda._stream_handle(stream)))
+    _kda._check(_kda.load().kda_attn_decode(ctypes.byref(args), _kda._stream_handle(stream)))
 
 
 def attn_decode(q, k_cache, v_cache, block_table, kv_lens, *, group_start=None, prefix_lens=None, scale=None, o=None,
@@ -265,33 +293,32 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_lens, *, group_start=None, 
     int32 [g] name the groups of consecutive sequences that share their first blocks; those
     are read once per group.  workspace: uint8, allocated unless a large enough one is given.
     Returns (o, lse or None)."""
-    kda = _base()
-    n, H, d = kda._dims(q, "q", 3)
-    H_kv = kda._dims(k_cache, "k_cache", 4)[1]
-    stride = kda._dims(block_table, "block_table", 2)[1]
     if (group_start is None) != (prefix_lens is None):
         raise ValueError("group_start and prefix_lens come together")
-    a = AttnDecodeArgs()
-    a.q, a.q_stride = _tokens(q, "q", _FLOATS, H, d, None)
-    dev = q.device
-    a.k_cache, a.v_cache, a.n_blocks, a.block_size = _cache(kda, k_cache, v_cache, q.dtype, H_kv, d, dev)
-    a.block_table = kda._dev(block_table, "block_table", torch.int32, (n, stride), dev)
-    a.kv_lens = kda._dev(kv_lens, "kv_lens", torch.int32, (n,), dev)
-    a.n_groups = 0
+    shape, qp, qs, dev, ix, code = _first(q, "q")
+    n, H, d = shape
+    H_kv = _shape(k_cache, "k_cache", 4)[1]
+    stride = _shape(block_table, "block_table", 2)[1]
+    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, q.dtype, H_kv, d, dev, ix)
+    table = _dev(block_table, "block_table", _I32, (n, stride), dev, ix)
+    kv = _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix)
+    groups, start, prefix = 0, None, None
     if group_start is not None:
-        a.n_groups = kda._dims(prefix_lens, "prefix_lens", 1)[0]
-        a.group_start = kda._dev(group_start, "group_start", torch.int32, (a.n_groups + 1,), dev)
-        a.prefix_lens = kda._dev(prefix_lens, "prefix_lens", torch.int32, (a.n_groups,), dev)
-    a.n_seqs, a.n_heads, a.n_kv_heads, a.d = n, H, H_kv, d
-    a.dtype, a.table_stride = kda._dtype_code(q), stride
-    a.scale = float(d ** -0.5 if scale is None else scale)
-    with _on(stream, dev):
-        o, lse = _outputs(kda, a, q, o, lse, want_lse, dev)
-        need = kda_attn_decode_workspace_size(a)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            a.workspace = kda._dev(workspace, "workspace", device=dev)
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
-        kda_attn_decode(a, stream)
-    return o, lse
+        groups, = _shape(prefix_lens, "prefix_lens", 1)
+        start = _dev(group_start, "group_start", _I32, (groups + 1,), dev, ix)
+        prefix = _dev(prefix_lens, "prefix_lens", _I32, (groups,), dev, ix)
+
+    def call(handle):
+        out, op, os_, z, zp = _outputs(q, shape, dev, ix, o, lse, want_lse)
+        a = AttnDecodeArgs(n, H, H_kv, d, code, _scale(scale, d), qs, os_, qp, op, zp, kc, vc, table, kv, n_blocks, bs,
+                           stride, groups, 0, start, prefix)
+        lib = _kda.load()
+        need, ws = lib.kda_attn_decode_workspace_size(ctypes.byref(a)), workspace
+        if need:
+            if ws is None or ws.numel() * ws.element_size() < need:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            a.workspace = _kda._dev(ws, "workspace", device=dev)
+            a.workspace_bytes = ws.numel() * ws.element_size()
+        _kda._check(lib.kda_attn_decode(ctypes.byref(a), handle))
+        return out, z
+    return _on_stream(stream, dev, call)

@@ -91,8 +91,8 @@ kda_status_t check_scale(float scale) {
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Thread blocks of the suffix kernel: three on each of the 152 SMs.
-constexpr int kDecodeCtas = 456;
+int decode_ctas(int32_t dtype) { return dtype == KDA_BF16 ? kda::kDecodeCtasBf16 : kda::kDecodeCtasF32; }
+int decode_rows(int32_t dtype) { return dtype == KDA_BF16 ? kda::kDecodeRowsBf16 : kda::kDecodeRowsF32; }
 
 // Blocks of keys that a shared prefix is cut into: enough row tiles (256 rows in
 // bf16, 64 in fp32) times blocks for the thread blocks that run at once (one on
@@ -119,7 +119,7 @@ DecodeSpace decode_space(const kda_attn_decode_args& a) {
         return r;
     };
     const size_t rows = (size_t)a.n_seqs * a.n_heads * prefix_splits(a);
-    const size_t parts = (size_t)2 * kDecodeCtas * kda::attn_decode_rows(a.dtype);
+    const size_t parts = (size_t)2 * decode_ctas(a.dtype) * decode_rows(a.dtype);
     s.pre_o = take(rows * a.d * sizeof(float));
     s.pre_ml = take(rows * sizeof(float2));
     s.part_o = take(parts * a.d * sizeof(float));
@@ -274,7 +274,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     kda::AttnDecodeLaunch p{};
     p.a = a;
-    p.n_ctas = kDecodeCtas;
+    p.n_ctas = decode_ctas(a.dtype);
     p.n_split = prefix_splits(a);
     p.pre_o = reinterpret_cast<float*>(ws + sp.pre_o);
     p.pre_ml = reinterpret_cast<float2*>(ws + sp.pre_ml);
@@ -285,6 +285,8 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     KDA_TRY(kda::device_status_word(&p.status));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.n_groups > 0) {
+        cudaError_t e = kda::launch_decode_info(p, s);
+        if (e != cudaSuccess) return cuda_fail(e, "decode plan launch");
         kda::AttnTileLaunch t{};
         t.a.n_seqs = a.n_groups;
         t.a.n_heads = a.n_heads, t.a.n_kv_heads = a.n_kv_heads, t.a.d = a.d, t.a.dtype = a.dtype;
@@ -301,10 +303,10 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
         t.n_split = p.n_split;
         t.part_o = p.pre_o;
         t.part_ml = p.pre_ml;
-        const cudaError_t e = kda::launch_attn_tile(t, s);
+        e = kda::launch_attn_tile(t, s);
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix attention launch");
     }
-    const cudaError_t e = kda::launch_attn_decode(p, s);
+    const cudaError_t e = a.dtype == KDA_BF16 ? kda::launch_decode_mma(p, s) : kda::launch_decode_simt(p, s);
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "decode attention launch");
 }
 

@@ -9,6 +9,10 @@ namespace kda {
 // Address of the current device's status word (api.cu).
 kda_status_t device_status_word(uint32_t** out);
 
+// Lets the next kernel of the stream be scheduled beside this one; it still waits
+// in griddep_wait() for this grid to complete.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ------------------------------------------------------------------ block scan
 
 // Inclusive scan of one value per thread over a block of NT threads; every thread
@@ -108,12 +112,7 @@ inline cudaError_t launch_attn_tile(const AttnTileLaunch& p, cudaStream_t s) {
     return p.a.dtype == KDA_BF16 ? launch_attn_tc(p, s) : launch_attn_simt(p, s);
 }
 
-// Decode attention.  The keys that a sequence does not share (its suffix) are cut
-// into tiles; all tiles of all units (sequence, key/value head, block of query
-// heads) form one line in that order, and thread block c of n_ctas takes an equal
-// piece of it.  A unit whose tiles fall into several pieces, or that has a shared
-// prefix, leaves partial results (m, l, unnormalised o) and the join adds them up
-// in a fixed order: the prefix's blocks of keys, then the pieces from first to last.
+// Decode attention (attn_decode.cuh describes the division of work).
 struct AttnDecodeLaunch {
     kda_attn_decode_args a;
     uint32_t* status;
@@ -126,8 +125,11 @@ struct AttnDecodeLaunch {
     int64_t* tiles;               // [n_seqs + 1] suffix tiles of one unit, summed over the earlier sequences
     int2* info;                   // [n_seqs] (shared positions, all positions)
 };
-cudaError_t launch_attn_decode(const AttnDecodeLaunch& p, cudaStream_t s);
-int attn_decode_rows(int dtype);  // query heads of one unit
+constexpr int kDecodeRowsF32 = 8, kDecodeRowsBf16 = 16;   // query heads of one unit
+constexpr int kDecodeCtasF32 = 456, kDecodeCtasBf16 = 304;   // three and two on each of 152 SMs
+cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s);   // p.info, where there are groups
+cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s);   // fp32
+cudaError_t launch_decode_mma(const AttnDecodeLaunch& p, cudaStream_t s);    // bf16
 
 struct CachePlanLaunch {
     kda_cache_plan_args a;

@@ -116,17 +116,18 @@ inline cudaError_t launch_attn_tile(const AttnTileLaunch& p, cudaStream_t s) {
 struct AttnDecodeLaunch {
     kda_attn_decode_args a;
     uint32_t* status;
-    int32_t n_ctas;               // thread blocks of the suffix kernel
+    int32_t n_pieces;             // workers of the suffix kernel
     int32_t n_split;              // key blocks of the prefix (0: no groups)
     float* pre_o;                 // [n_split, n_seqs, H, d] the prefix's partial results
     float2* pre_ml;               // [n_split, n_seqs, H]
-    float* part_o;                // [2 * n_ctas, rows, d]: a piece's first unit, its last unit
-    float2* part_ml;              // [2 * n_ctas, rows]
-    int64_t* tiles;               // [n_seqs + 1] suffix tiles of one unit, summed over the earlier sequences
-    int2* info;                   // [n_seqs] (shared positions, all positions)
+    float* part_o;                // [2 * n_pieces, rows, d]: a piece's first unit, its last unit
+    float2* part_ml;              // [2 * n_pieces, rows]
+    int4* open;                   // [n_pieces] the unit that begins in a piece and goes on
+    int2* info;                   // [n_seqs] (shared positions, all positions), where there are groups
 };
 constexpr int kDecodeRowsF32 = 8, kDecodeRowsBf16 = 16;   // query heads of one unit
-constexpr int kDecodeCtasF32 = 456, kDecodeCtasBf16 = 304;   // three and two on each of 152 SMs
+// Workers: three thread blocks (fp32) or one of eight warps (bf16) on each of 152 SMs.
+constexpr int kDecodeWarpsBf16 = 8, kDecodePiecesF32 = 3 * 152, kDecodePiecesBf16 = kDecodeWarpsBf16 * 152;
 cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s);   // p.info, where there are groups
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s);   // fp32
 cudaError_t launch_decode_mma(const AttnDecodeLaunch& p, cudaStream_t s);    // bf16

@@ -77,9 +77,17 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
     const kda_attn_decode_args& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
-    Cursor c;
-    if (!find_piece<kThreads>(p, a.n_kv_heads * blocks, kKeys, c)) return;
+    __shared__ PieceStart at_;
+    int64_t all, pieces;
+    find_pieces<kThreads, 1>(p, a.n_kv_heads * blocks, kKeys, 1, &at_, all, pieces);
     griddep_launch();
+    const int64_t piece = blockIdx.x;
+    finish_empty<float, D>(p, (int64_t)blockIdx.x * (kThreads / 32) + warp, (int64_t)gridDim.x * (kThreads / 32), lane);
+    if (piece >= pieces) {
+        if (tid == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    Cursor c = start(p, at_, a.n_kv_heads * blocks, kKeys);
     const float sl = a.scale * kLog2e;
     while (c.left > 0) {
         const int64_t k_first = c.k, k_last = c.k + c.run();
@@ -183,8 +191,7 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
         if (part == 0) {
             const bool whole = k_first == 0 && k_last == c.T;
             const int n_pre = whole && info.x > 0 ? p.n_split : 0;
-            // a piece that starts inside a unit leaves slot 0, one that starts it slot 1
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (k_first == 0 ? 1 : 0);
+            const int64_t slot = part_slot(piece, k_first == 0);
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 if (r >= rows) break;
@@ -205,6 +212,7 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
                 }
             }
         }
+        if (tid == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, pieces, all);
         c.next_unit(p, kKeys);
     }
 }
@@ -215,7 +223,7 @@ cudaError_t launch_t(const AttnDecodeLaunch& p, cudaStream_t s) {
                                          (int)sizeof(DecodeSmem<D>));
     if (e != cudaSuccess) return e;
     note_launch();
-    e = launch_overlapped(decode_suffix_kernel<D>, dim3(p.n_ctas), dim3(kThreads), sizeof(DecodeSmem<D>), s, p);
+    e = launch_overlapped(decode_suffix_kernel<D>, dim3(p.n_pieces), dim3(kThreads), sizeof(DecodeSmem<D>), s, p);
     return e == cudaSuccess ? launch_join<float, D, kRows>(p, s) : e;
 }
 

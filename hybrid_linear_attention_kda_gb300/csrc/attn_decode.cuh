@@ -2,11 +2,13 @@
 //
 // The keys that a sequence does not share (its suffix) are cut into tiles.  All
 // tiles of all units (sequence, key/value head, block of query heads), in that
-// order, form one line; it is cut into equal pieces, one for each thread block, so
-// the blocks finish together whatever the lengths are.  A unit inside one piece is
-// finished there (with its prefix's partial results); of a unit that several pieces
-// share, each leaves (m, l, unnormalised o), and the join adds them up from the
-// first piece to the last, behind the prefix's blocks of keys.
+// order, form one line; it is cut into equal pieces, one for each worker (a warp of
+// the bf16 kernel, a thread block of the fp32 one), so that the workers finish
+// together whatever the lengths are.  A unit inside one piece is finished there
+// (with its prefix's partial results); of a unit that several pieces share, each
+// leaves (m, l, unnormalised o), the piece in which it begins notes it, and the
+// join adds the parts up from the first piece to the last, behind the prefix's
+// blocks of keys.
 //
 // Joining partial results:  m = max_p m_p,  o = sum_p 2^(m_p - m) o_p,  l alike;
 // scores are kept times log2(e).
@@ -32,9 +34,13 @@ __device__ __forceinline__ int64_t seq_tiles(int2 info, int tile_keys) {
     return info.y > info.x ? ((int64_t)info.y - info.x + tile_keys - 1) / tile_keys : 0;
 }
 
-// The line has as many pieces as there are thread blocks, but none is empty:
-// piece c holds the tiles [begin(c), begin(c + 1)).
-__device__ __forceinline__ int64_t n_pieces(int64_t all, int64_t n_ctas) { return all < n_ctas ? all : n_ctas; }
+// The line has as many pieces as there are workers, or fewer of at least `least`
+// tiles: a shorter one costs more in the join than it saves.  Piece c holds the tiles
+// [begin(c), begin(c + 1)).
+__device__ __forceinline__ int64_t n_pieces(int64_t all, int64_t most, int least) {
+    const int64_t n = (all + least - 1) / least;
+    return n < most ? n : most;
+}
 __device__ __forceinline__ int64_t piece_begin(int64_t all, int64_t c, int64_t n) {
     return all / n * c + all % n * c / n;
 }
@@ -61,58 +67,61 @@ struct Cursor {
     }
 };
 
-// Start of this thread block's piece; false when it has none.  Thread i counts the
-// tiles of its share of the sequences, one block scan gives the line's length and
-// the thread whose share holds the piece's first tile walks it again.  Block 0
-// writes the running counts that the join reads, and reports bad lengths.
-template <int NT>
-__device__ bool find_piece(const AttnDecodeLaunch& p, int units, int tile_keys, Cursor& c) {
+// The pieces of a thread block of NT threads with PIECES workers: fills at[] for
+// them (the caller's shared memory) and returns the line's length in tiles and pieces.
+// Thread i counts the tiles of its share of the sequences, one block scan gives the
+// line's length, and the thread whose share holds a piece's first tile walks it
+// again.
+struct PieceStart {
+    int32_t s;
+    int64_t rel, left;     // tiles past the first of s, tiles of the piece
+};
+template <int NT, int PIECES>
+__device__ void find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, int least, PieceStart* at, int64_t& all,
+                            int64_t& pieces) {
     __shared__ int64_t scan_buf[NT / 32];
-    __shared__ int32_t found_s;
-    __shared__ int64_t found_rel;
     const int32_t n = p.a.n_seqs;
     const int32_t share = (n + NT - 1) / NT, s0 = min(n, (int32_t)threadIdx.x * share), s1 = min(n, s0 + share);
     int64_t mine = 0;
+#pragma unroll 4
     for (int32_t s = s0; s < s1; ++s) mine += seq_tiles(seq_info(p, s), tile_keys);
     int64_t total;
-    int64_t before = block_scan<NT>(mine, scan_buf, &total) - mine;
-    if (blockIdx.x == 0) {
-        int64_t t = before;
-        for (int32_t s = s0; s < s1; ++s) {
-            const int2 info = seq_info(p, s);
-            if (p.a.n_groups == 0) {
-                const int32_t kv = p.a.kv_lens[s];
-                if (kv != info.y) flag(p.status, KDA_DEV_BAD_SEQLENS);
-                p.info[s] = info;
-            }
-            p.tiles[s] = t;
-            t += seq_tiles(info, tile_keys);
-        }
-        if (threadIdx.x == 0) p.tiles[n] = total;
-    }
-    const int64_t all = total * units, pieces = n_pieces(all, p.n_ctas);
-    if ((int64_t)blockIdx.x >= pieces) return false;
-    const int64_t at = piece_begin(all, blockIdx.x, pieces);
-    if (before * units <= at && at < (before + mine) * units) {
-        int32_t s = s0;
-        for (;; ++s) {
+    const int64_t before = block_scan<NT>(mine, scan_buf, &total) - mine;
+    all = total * units;
+    pieces = n_pieces(all, p.n_pieces, least);
+    for (int i = 0; i < PIECES; ++i) {
+        const int64_t c = (int64_t)blockIdx.x * PIECES + i;
+        if (c >= pieces) break;
+        const int64_t begin = piece_begin(all, c, pieces);
+        if (before * units > begin || begin >= (before + mine) * units) continue;
+        int64_t x = before;
+        for (int32_t s = s0;; ++s) {
             const int64_t t = seq_tiles(seq_info(p, s), tile_keys);
-            if (at < (before + t) * units) break;
-            before += t;
+            if (begin < (x + t) * units) {
+                at[i] = PieceStart{s, begin - x * units, piece_begin(all, c + 1, pieces) - begin};
+                break;
+            }
+            x += t;
         }
-        found_s = s;
-        found_rel = at - before * units;
     }
     __syncthreads();
-    c.s = found_s;
-    c.units = units;
-    c.info = seq_info(p, c.s);
-    c.T = seq_tiles(c.info, tile_keys);
-    c.u = (int32_t)(found_rel / c.T);
-    c.k = found_rel % c.T;
-    c.left = piece_begin(all, (int64_t)blockIdx.x + 1, pieces) - at;
-    return true;
 }
+
+__device__ __forceinline__ Cursor start(const AttnDecodeLaunch& p, const PieceStart& at, int units, int tile_keys) {
+    Cursor c;
+    c.s = at.s;
+    c.units = units;
+    c.info = seq_info(p, at.s);
+    c.T = seq_tiles(c.info, tile_keys);
+    c.u = (int32_t)(at.rel / c.T);
+    c.k = at.rel - c.u * c.T;
+    c.left = at.left;
+    return c;
+}
+
+// What piece c leaves of a unit that it does not hold whole: slot 1 when the unit
+// begins in it (then the join finds it noted in p.open), slot 0 otherwise.
+__device__ __forceinline__ int64_t part_slot(int64_t c, bool begins) { return 2 * c + (begins ? 1 : 0); }
 
 // Adds (m2, l2) to (m, l); the factors that the two sides' o take.
 __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, float& w, float& w2) {
@@ -129,38 +138,62 @@ __device__ __forceinline__ void write_lse(const kda_attn_decode_args& a, int32_t
     if (a.lse) a.lse[(int64_t)s * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m, kLn2, logf(l));
 }
 
-// One thread block of four warps for each unit; a warp takes every fourth row, a
-// lane D / 32 columns.
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnDecodeLaunch p) {
+// Sequences without a suffix: zeros, or the prefix's results.  Worker w of n takes
+// every n-th sequence, a lane D / 32 columns.  Also reports bad lengths.
+template <typename T, int D>
+__device__ void finish_empty(const AttnDecodeLaunch& p, int64_t w, int64_t n, int lane) {
     constexpr int kCols = D / 32;
+    const kda_attn_decode_args& a = p.a;
+    for (int64_t s = w; s < a.n_seqs; s += n) {
+        const int2 info = seq_info(p, (int32_t)s);
+        if (a.n_groups == 0 && info.y != a.kv_lens[s] && lane == 0) flag(p.status, KDA_DEV_BAD_SEQLENS);
+        if (info.y > info.x) continue;
+        const int n_pre = info.x > 0 ? p.n_split : 0;
+        for (int head = 0; head < a.n_heads; ++head) {
+            float m = -CUDART_INF_F, l = 0.f, o[kCols] = {};
+            for (int i = 0; i < n_pre; ++i) {
+                const int64_t at = prefix_row(p, i, (int32_t)s, head);
+                const float2 ml = p.pre_ml[at];
+                float w1, w2;
+                join(m, l, ml.x, ml.y, w1, w2);
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) o[e] = o[e] * w1 + p.pre_o[at * D + lane * kCols + e] * w2;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + lane * kCols;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) Elem<T>::store(out + e, o[e] * inv);
+            if (lane == 0) write_lse(a, (int32_t)s, head, m, l);
+        }
+    }
+}
+
+constexpr int kJoinWarps = 8;
+
+// Thread block c joins the unit that begins in piece c and ends in a later one, if
+// there is one.  Its warps are spread over the unit's rows, and over its parts when
+// there are fewer rows than warps; a lane takes D / 32 columns.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ AttnDecodeLaunch p) {
+    constexpr int kCols = D / 32;
+    __shared__ float s_o[kJoinWarps][D];
+    __shared__ float2 s_ml[kJoinWarps];
     griddep_wait();
     const kda_attn_decode_args& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c0 = blockIdx.x;
+    const int4 open = p.open[c0];                        // sequence (-1: none), unit, last piece
+    if (open.x < 0) return;
+    const int32_t s = open.x;
+    const int64_t parts = open.z - c0 + 1;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + ROWS - 1) / ROWS;
-    const int64_t U = (int64_t)a.n_kv_heads * blocks;
-    const int32_t s = (int32_t)(blockIdx.x / U);
-    const int u = (int)(blockIdx.x - s * U), hk = u / blocks, rb = u % blocks;
+    const int hk = open.y / blocks, rb = open.y % blocks;
     const int head0 = hk * G + rb * ROWS, rows = min(ROWS, G - rb * ROWS);
-    const int2 info = p.info[s];
-    const int64_t T_s = p.tiles[s + 1] - p.tiles[s], all = p.tiles[a.n_seqs] * U;
-    const int64_t lo = p.tiles[s] * U + u * T_s;
-    int64_t c0 = 0, c1 = -1;                             // pieces that hold the unit's tiles
-    if (T_s > 0) {
-        const int64_t n = n_pieces(all, p.n_ctas);
-        auto piece = [&](int64_t x) {                    // the piece with begin(c) <= x < begin(c + 1)
-            int64_t c = (int64_t)((double)x * n / (double)all);
-            c = c < 0 ? 0 : c >= n ? n - 1 : c;
-            while (c > 0 && piece_begin(all, c, n) > x) --c;
-            while (c + 1 < n && piece_begin(all, c + 1, n) <= x) ++c;
-            return c;
-        };
-        c0 = piece(lo);
-        c1 = piece(lo + T_s - 1);
-        if (c0 == c1) return;                            // written by its piece
-    }
-    const int n_pre = info.x > 0 ? p.n_split : 0;
-    for (int r = warp; r < rows; r += 4) {
+    const int2 info = seq_info(p, s);
+    const int row_warps = rows >= 8 ? 8 : rows >= 4 ? 4 : rows >= 2 ? 2 : 1, part_warps = kJoinWarps / row_warps;
+    const int r0 = warp % row_warps, pw = warp / row_warps;
+    const int64_t per = (parts + part_warps - 1) / part_warps;
+    for (int r = r0; r - r0 < rows; r += row_warps) {    // every warp the same number of times
         const int head = head0 + r;
         float m = -CUDART_INF_F, l = 0.f, o[kCols] = {};
         auto add = [&](const float2 ml, const float* src) {
@@ -172,18 +205,31 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnD
 #pragma unroll
             for (int e = 0; e < kCols; ++e) o[e] = o[e] * w + x[e] * w2;
         };
-#pragma unroll 4
-        for (int i = 0; i < n_pre; ++i) {
-            const int64_t at = prefix_row(p, i, s, head);
-            add(p.pre_ml[at], p.pre_o + at * D);
+        if (r < rows) {
+            if (pw == 0 && info.x > 0)
+                for (int i = 0; i < p.n_split; ++i) {
+                    const int64_t at = prefix_row(p, i, s, head);
+                    add(p.pre_ml[at], p.pre_o + at * D);
+                }
+            const int64_t last = min(parts, (pw + 1) * per);
+#pragma unroll 8
+            for (int64_t i = pw * per; i < last; ++i) {
+                const int64_t at = part_slot(c0 + i, i == 0) * ROWS + r;
+                add(p.part_ml[at], p.part_o + at * D);
+            }
         }
-#pragma unroll 4
-        for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t at = (2 * c + (c == c0 ? 1 : 0)) * ROWS + r;
-            add(p.part_ml[at], p.part_o + at * D);
+        if (part_warps > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) s_o[warp][lane * kCols + e] = o[e];
+            if (lane == 0) s_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (pw == 0)
+                for (int i = 1; i < part_warps; ++i) add(s_ml[warp + i * row_warps], s_o[warp + i * row_warps]);
         }
-        T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + lane * kCols;
+        if (pw != 0 || r >= rows) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + lane * kCols;
 #pragma unroll
         for (int e = 0; e < kCols; ++e) Elem<T>::store(out + e, o[e] * inv);
         if (lane == 0) write_lse(a, s, head, m, l);
@@ -192,10 +238,21 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnD
 
 template <typename T, int D, int ROWS>
 cudaError_t launch_join(const AttnDecodeLaunch& p, cudaStream_t s) {
-    const int G = p.a.n_heads / p.a.n_kv_heads;
-    const int64_t units = (int64_t)p.a.n_seqs * p.a.n_kv_heads * ((G + ROWS - 1) / ROWS);
     note_launch();
-    return launch_overlapped(join_kernel<T, D, ROWS>, dim3((unsigned)units), dim3(128), 0, s, p);
+    return launch_overlapped(join_kernel<T, D, ROWS>, dim3((unsigned)p.n_pieces), dim3(32 * kJoinWarps), 0, s, p);
+}
+
+// Notes for the join whether the unit of the piece that ends at cursor c's run
+// begins there and goes on: `done` tiles of the unit lie in the piece.
+__device__ __forceinline__ int4 open_unit(const Cursor& c, int64_t piece, int64_t pieces, int64_t all) {
+    const int64_t rest = c.T - (c.k + c.run());          // its tiles in later pieces
+    if (c.k != 0 || rest == 0) return make_int4(-1, 0, 0, 0);
+    const int64_t x = piece_begin(all, piece + 1, pieces) + rest - 1;    // its last tile
+    int64_t last = (int64_t)((double)x * pieces / (double)all);
+    last = last < piece ? piece : last >= pieces ? pieces - 1 : last;
+    while (last > piece && piece_begin(all, last, pieces) > x) --last;
+    while (last + 1 < pieces && piece_begin(all, last + 1, pieces) <= x) ++last;
+    return make_int4(c.s, c.u, (int)last, 0);
 }
 
 }  // namespace decode

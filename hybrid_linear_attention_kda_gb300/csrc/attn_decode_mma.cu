@@ -4,30 +4,26 @@
 // A unit has up to 16 query heads, the rows of one m16n8k16 product, so the cache is
 // read once for all of them: 16 rows x 4 d flops for the 4 d bytes of a key, which
 // keeps the warp-level tensor instructions well below their rate (the wider tcgen05
-// tiles would be seven eighths padding).  Each of a block's four warps works on its
-// own 16 keys of a 64-key tile with its own (m, l, o), and its own ring of
-// asynchronous copies, so that the loop has no barrier; the copies run ahead across
-// the ends of units.  At the end of a unit the warps' results are added up through
-// shared memory.  A page holds at least 16 keys, so that a warp's keys lie in one.
+// tiles would be seven eighths padding).  Each warp is a worker of its own: it walks
+// its piece in tiles of 16 keys with its (m, l, o) in registers and its own ring of
+// asynchronous copies, which run ahead across the ends of units, so that nothing in
+// the kernel waits for another warp.  A page holds at least 16 keys, so that a tile
+// lies in one.
 //
-// Bound by reading the cache once.  Measured: one sequence of 2^20 tokens, 8 heads,
-// d = 128: 0.62 ms, 6.9 TB/s (the SIMT form took 2.08 ms); 512 sequences of 32 query
-// and 8 key/value heads behind 8 shared prefixes of 4096: 0.52 ms in all (1.24 ms).
+// Bound by reading the cache once.
 #include "attn_decode.cuh"
 
 namespace kda {
 namespace {
 using namespace decode;
 
-constexpr int kThreads = 128, kWarps = 4, kRows = kDecodeRowsBf16, kWarpKeys = 16, kKeys = kWarps * kWarpKeys;
-constexpr int kStages = 3;
+constexpr int kWarps = kDecodeWarpsBf16, kThreads = 32 * kWarps, kRows = kDecodeRowsBf16, kKeys = 16;
+constexpr int kLeastTiles = 4;           // of a piece
 constexpr float kMaxGrowth = 8.f;        // log2 of how far weights may exceed 1 before their maximum moves
 
 template <int D> struct DecodeSmem {
-    static constexpr int kTileBytes = kWarpKeys * D * 2;
+    static constexpr int kTileBytes = kKeys * D * 2, kStages = 384 / D;      // 24 KB of keys and values a warp
     uint8_t ring[kWarps][kStages][2][kTileBytes];
-    float o[2][kRows * D];
-    float m[kWarps][kRows], l[kWarps][kRows];
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -68,33 +64,41 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_constant__ AttnDecodeLaunch p) {
+__global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid_constant__ AttnDecodeLaunch p) {
     using S = DecodeSmem<D>;
-    constexpr int kChunks = D / 8;                       // 16-byte pieces of a key
+    constexpr int kChunks = D / 8, kStages = S::kStages;  // 16-byte pieces of a key
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>(smem_raw);
     griddep_wait();
     const kda_attn_decode_args& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
-    Cursor c;
-    if (!find_piece<kThreads>(p, a.n_kv_heads * blocks, kKeys, c)) return;
+    __shared__ PieceStart at_[kWarps];
+    int64_t all, pieces;
+    find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_, all, pieces);
     griddep_launch();
+    const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
+    finish_empty<__nv_bfloat16, D>(p, piece, p.n_pieces, lane);
+    if (piece >= pieces) {
+        if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    Cursor c = start(p, at_[warp], a.n_kv_heads * blocks, kKeys);
 
     // ------------------------------------------------------------------ copies
     // The copies' own place on the line, kStages - 1 tiles ahead.  Chunk y of key j
     // lies at chunk y ^ (j % 8) of its row: eight keys' equal chunks in eight banks.
     Cursor f = c;
     const uint32_t ring = smem_u32(sm.ring[warp]);
-    int32_t next_block = 0;                              // table entry of the place f (this warp's keys)
+    int32_t next_block = 0;                              // table entry of the place f
     auto look_up = [&]() {
-        const int64_t key = f.info.x + f.k * kKeys + warp * kWarpKeys;
+        const int64_t key = f.info.x + f.k * kKeys;
         next_block = f.left > 0 && key < f.info.y ? a.block_table[(int64_t)f.s * a.table_stride + key / a.block_size] : -2;
     };
     auto fetch = [&](int stage) {
         if (f.left > 0) {
-            const int64_t key = f.info.x + f.k * kKeys + warp * kWarpKeys;
-            int live = (int)max((int64_t)0, min((int64_t)kWarpKeys, f.info.y - key));     // keys that exist
+            const int64_t key = f.info.x + f.k * kKeys;
+            int live = (int)max((int64_t)0, min((int64_t)kKeys, f.info.y - key));     // keys that exist
             if (live > 0 && (next_block < 0 || next_block >= a.n_blocks)) {
                 flag(p.status, KDA_DEV_BAD_SLOT);
                 live = 0;
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
             const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(a.v_cache) + row * D;
             const uint32_t kd = ring + stage * 2 * S::kTileBytes, vd = kd + S::kTileBytes;
 #pragma unroll
-            for (int i = 0; i < kWarpKeys * kChunks / 32; ++i) {
+            for (int i = 0; i < kKeys * kChunks / 32; ++i) {
                 const int j = (i * 32 + lane) / kChunks, y = (i * 32 + lane) % kChunks;
                 const uint32_t to = (uint32_t)(j * kChunks + (y ^ (j & 7))) * 16u;
                 const int from = j < live ? j * D + y * 8 : 0;
@@ -166,8 +170,8 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
             fetch(stage == 0 ? kStages - 1 : stage - 1);
             const uint32_t kb = ring + stage * 2 * S::kTileBytes, vb = kb + S::kTileBytes;
             stage = stage == kStages - 1 ? 0 : stage + 1;
-            const int64_t key0 = info.x + kt * kKeys + warp * kWarpKeys;
-            const int live = (int)max((int64_t)0, min((int64_t)kWarpKeys, info.y - key0));
+            const int64_t key0 = info.x + kt * kKeys;
+            const int live = (int)max((int64_t)0, min((int64_t)kKeys, info.y - key0));
             float x[2][4] = {};
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
                 mma(x[1], q[d], b[2], b[3]);
             }
             // x[h][2 r + e]: row `row + 8 r`, key 8 h + pair + e
-            if (live < kWarpKeys) {
+            if (live < kKeys) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float w0 = ex2(fmaf(x[h][2 * r], sc, off)), w1 = ex2(fmaf(x[h][2 * r + 1], sc, off));
-                    if (live < kWarpKeys) {
+                    if (live < kKeys) {
                         w0 = 8 * h + pair < live ? w0 : 0.f;
                         w1 = 8 * h + pair + 1 < live ? w1 : 0.f;
                     }
@@ -232,94 +236,44 @@ __global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_co
             __syncwarp();                                // all lanes have read the stage
         }
 
-        // ------------------------------------------------------------------ the warps' sum
+        const bool whole = k_first == 0 && k_last == c.T;
+        const int n_pre = whole && info.x > 0 ? p.n_split : 0;
+        const int64_t slot = part_slot(piece, k_first == 0);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            m[r] = m[r] == -CUDART_INF_F ? m[r] : m[r] * sc;
-            if ((lane & 3) == 0) {
-                sm.m[warp][row + 8 * r] = m[r];
-                sm.l[warp][row + 8 * r] = l[r];
-            }
-        }
-        __syncthreads();
-        float mt[2], lt[2];
+            float lt = l[r], mt = m[r] == -CUDART_INF_F ? m[r] : m[r] * sc;
+            lt += __shfl_xor_sync(0xffffffffu, lt, 1);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 2);
+            const int rr = row + 8 * r, head = head0 + rr;
+            if (rr >= rows) continue;
+            for (int i = 0; i < n_pre; ++i) {
+                const int64_t pr = prefix_row(p, i, s, head);
+                const float2 ml = p.pre_ml[pr];
+                float w, w2;
+                join(mt, lt, ml.x, ml.y, w, w2);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int at = row + 8 * r;
-            mt[r] = fmaxf(fmaxf(sm.m[0][at], sm.m[1][at]), fmaxf(sm.m[2][at], sm.m[3][at]));
-            const float ms = mt[r] == -CUDART_INF_F ? 0.f : mt[r];
-            lt[r] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) lt[r] += sm.l[w][at] * ex2(sm.m[w][at] - ms);
-            const float w = ex2(m[r] - ms);
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-                o[y][2 * r] *= w;
-                o[y][2 * r + 1] *= w;
-            }
-        }
-        auto at = [&](int y, int r) { return (row + 8 * r) * D + 8 * y + pair; };
-        auto give = [&](float* to) {
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) *reinterpret_cast<float2*>(to + at(y, r)) = make_float2(o[y][2 * r], o[y][2 * r + 1]);
-        };
-        auto take = [&](const float* from) {
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float2 v = *reinterpret_cast<const float2*>(from + at(y, r));
-                    o[y][2 * r] += v.x;
-                    o[y][2 * r + 1] += v.y;
-                }
-        };
-        if (warp >= 2) give(sm.o[warp - 2]);
-        __syncthreads();
-        if (warp < 2) take(sm.o[warp]);
-        __syncthreads();
-        if (warp == 1) give(sm.o[0]);
-        __syncthreads();
-        if (warp == 0) {
-            take(sm.o[0]);
-            const bool whole = k_first == 0 && k_last == c.T;
-            const int n_pre = whole && info.x > 0 ? p.n_split : 0;
-            // a piece that starts inside a unit leaves slot 0, one that starts it slot 1
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (k_first == 0 ? 1 : 0);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int rr = row + 8 * r, head = head0 + rr;
-                if (rr >= rows) continue;
-                for (int i = 0; i < n_pre; ++i) {
-                    const int64_t pr = prefix_row(p, i, s, head);
-                    const float2 ml = p.pre_ml[pr];
-                    float w, w2;
-                    join(mt[r], lt[r], ml.x, ml.y, w, w2);
-#pragma unroll
-                    for (int y = 0; y < D / 8; ++y) {
-                        const float2 v = *reinterpret_cast<const float2*>(p.pre_o + pr * D + 8 * y + pair);
-                        o[y][2 * r] = o[y][2 * r] * w + v.x * w2;
-                        o[y][2 * r + 1] = o[y][2 * r + 1] * w + v.y * w2;
-                    }
-                }
-                if (whole) {
-                    const float inv = lt[r] == 0.f ? 0.f : 1.f / lt[r];
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + s * a.o_stride + (int64_t)head * D + pair;
-#pragma unroll
-                    for (int y = 0; y < D / 8; ++y)
-                        *reinterpret_cast<uint32_t*>(out + 8 * y) = pack(o[y][2 * r] * inv, o[y][2 * r + 1] * inv);
-                    if (pair == 0) write_lse(a, s, head, mt[r], lt[r]);
-                } else {
-                    float* out = p.part_o + (slot * kRows + rr) * D + pair;
-#pragma unroll
-                    for (int y = 0; y < D / 8; ++y) *reinterpret_cast<float2*>(out + 8 * y) = make_float2(o[y][2 * r], o[y][2 * r + 1]);
-                    if (pair == 0) p.part_ml[slot * kRows + rr] = make_float2(mt[r], lt[r]);
+                for (int y = 0; y < D / 8; ++y) {
+                    const float2 v = *reinterpret_cast<const float2*>(p.pre_o + pr * D + 8 * y + pair);
+                    o[y][2 * r] = o[y][2 * r] * w + v.x * w2;
+                    o[y][2 * r + 1] = o[y][2 * r + 1] * w + v.y * w2;
                 }
             }
+            if (whole) {
+                const float inv = lt == 0.f ? 0.f : 1.f / lt;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + s * a.o_stride + (int64_t)head * D + pair;
+#pragma unroll
+                for (int y = 0; y < D / 8; ++y)
+                    *reinterpret_cast<uint32_t*>(out + 8 * y) = pack(o[y][2 * r] * inv, o[y][2 * r + 1] * inv);
+                if (pair == 0) write_lse(a, s, head, mt, lt);
+            } else {
+                float* out = p.part_o + (slot * kRows + rr) * D + pair;
+#pragma unroll
+                for (int y = 0; y < D / 8; ++y) *reinterpret_cast<float2*>(out + 8 * y) = make_float2(o[y][2 * r], o[y][2 * r + 1]);
+                if (pair == 0) p.part_ml[slot * kRows + rr] = make_float2(mt, lt);
+            }
         }
+        __syncwarp();
+        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, pieces, all);
         c.next_unit(p, kKeys);
     }
     copy_wait<0>();
@@ -331,7 +285,7 @@ cudaError_t launch_t(const AttnDecodeLaunch& p, cudaStream_t s) {
                                          (int)sizeof(DecodeSmem<D>));
     if (e != cudaSuccess) return e;
     note_launch();
-    e = launch_overlapped(decode_suffix_kernel<D>, dim3(p.n_ctas), dim3(kThreads), sizeof(DecodeSmem<D>), s, p);
+    e = launch_overlapped(decode_suffix_kernel<D>, dim3(p.n_pieces / kWarps), dim3(kThreads), sizeof(DecodeSmem<D>), s, p);
     return e == cudaSuccess ? launch_join<__nv_bfloat16, D, kRows>(p, s) : e;
 }
 

@@ -42,6 +42,9 @@ using namespace tc;
 constexpr int kTile = 128;                    // rows of a tile, keys of a tile
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kGuardWarp = 10, kGuardWarps = 2;
 constexpr int kThreads = 384;
+// Registers a thread: 168 at launch; the softmax warps hold a whole row of scores.
+// 256 * 208 + 128 * 88 <= 384 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMaxGrowth = 8.f;             // log2 of how far weights may exceed 1
 constexpr uint32_t kTmemCols = 512;           // S0 0, S1 128, O0 256, O1 384
@@ -116,6 +119,31 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// Pairs of fp32 values in one 64-bit register, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t x) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t pair2(float x) { return pair2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // ------------------------------------------------------------------ the block's work
 
@@ -233,190 +261,201 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     // some row sees only a part of tile j
     auto edge = [&](int j) { return w.k_lo + (int64_t)(j + 1) * kTile > w.all_see; };
 
-    if (warp == kMmaWarp) {
-        if (lane == 0 && n_tiles > 0) {
-            const uint32_t id_s = idesc_bf16(kTile, kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
-            const uint32_t id_o = idesc_bf16(kTile, D, false, true);
-            const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
-            auto at = [](uint64_t desc, uint32_t byte) { return desc + (uint64_t)(byte >> 4); };
-            auto scores = [&](int q, int stage) {
-                const uint32_t qb = s_base + Sh::kQ + q * Sh::kTileBytes, kb = s_base + Sh::kRing + stage * Sh::kTileBytes;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
-                    mma_bf16(tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
-                }
-                mma_commit(&ms.s_full[q]);
-            };
-            auto values = [&](int q, int stage, bool first) {
-                const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
-#pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                    mma_bf16_ts(tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
-            };
-            bool ok = waitb(&ms.q_full, 0) && waitb(&ms.full[0], 0);
-            if (ok) {
-                fence_after_sync();
-                for (int q = 0; q < 2; ++q)
-                    if (w.n_keys[q] > 0) scores(q, 0);
-                mma_commit(&ms.empty[0]);
-            }
-            uint32_t guard_phase = 0;                             // a bit for each stage
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
-                if (!(ok = waitb(&ms.full[stage_of(iv)], phase_of(iv)))) break;
-                if (edge(j)) {
-                    if (!(ok = waitb(&ms.guarded[stage_of(iv)], guard_phase >> stage_of(iv) & 1))) break;
-                    guard_phase ^= 1u << stage_of(iv);
-                }
-                const bool more = j + 1 < n_tiles;
-                if (more && !(ok = waitb(&ms.full[stage_of(ik)], phase_of(ik)))) break;
-                for (int q = 0; q < 2 && ok; ++q) {
-                    if (j < w.n_keys[q]) {
-                        if (!(ok = waitb(&ms.p_ready[q], j & 1))) break;
-                        fence_after_sync();
-                        values(q, stage_of(iv), j == 0);
-                        if (j + 1 == w.n_keys[q]) mma_commit(&ms.o_done[q]);
+    // the register split is made inside the branches: after a merge of the two the
+    // compiler would hold everything to the smaller share
+    if (warp >= kMmaWarp) {
+        fewer_registers<kOtherRegs>();
+        if (warp == kMmaWarp) {
+            if (lane == 0 && n_tiles > 0) {
+                const uint32_t id_s = idesc_bf16(kTile, kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
+                const uint32_t id_o = idesc_bf16(kTile, D, false, true);
+                const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
+                auto at = [](uint64_t desc, uint32_t byte) { return desc + (uint64_t)(byte >> 4); };
+                auto scores = [&](int q, int stage) {
+                    const uint32_t qb = s_base + Sh::kQ + q * Sh::kTileBytes, kb = s_base + Sh::kRing + stage * Sh::kTileBytes;
+    #pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
+                        mma_bf16(tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
                     }
-                    if (q == 1) mma_commit(&ms.empty[stage_of(iv)]);
-                    if (j + 1 < w.n_keys[q]) scores(q, stage_of(ik));
+                    mma_commit(&ms.s_full[q]);
+                };
+                auto values = [&](int q, int stage, bool first) {
+                    const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
+    #pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        mma_bf16_ts(tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
+                };
+                bool ok = waitb(&ms.q_full, 0) && waitb(&ms.full[0], 0);
+                if (ok) {
+                    fence_after_sync();
+                    for (int q = 0; q < 2; ++q)
+                        if (w.n_keys[q] > 0) scores(q, 0);
+                    mma_commit(&ms.empty[0]);
                 }
-                if (ok && more) mma_commit(&ms.empty[stage_of(ik)]);
+                uint32_t guard_phase = 0;                             // a bit for each stage
+                for (int j = 0; j < n_tiles && ok; ++j) {
+                    const int iv = 2 * j + 1, ik = 2 * j + 2;
+                    if (!(ok = waitb(&ms.full[stage_of(iv)], phase_of(iv)))) break;
+                    if (edge(j)) {
+                        if (!(ok = waitb(&ms.guarded[stage_of(iv)], guard_phase >> stage_of(iv) & 1))) break;
+                        guard_phase ^= 1u << stage_of(iv);
+                    }
+                    const bool more = j + 1 < n_tiles;
+                    if (more && !(ok = waitb(&ms.full[stage_of(ik)], phase_of(ik)))) break;
+                    for (int q = 0; q < 2 && ok; ++q) {
+                        if (j < w.n_keys[q]) {
+                            if (!(ok = waitb(&ms.p_ready[q], j & 1))) break;
+                            fence_after_sync();
+                            values(q, stage_of(iv), j == 0);
+                            if (j + 1 == w.n_keys[q]) mma_commit(&ms.o_done[q]);
+                        }
+                        if (q == 1) mma_commit(&ms.empty[stage_of(iv)]);
+                        if (j + 1 < w.n_keys[q]) scores(q, stage_of(ik));
+                    }
+                    if (ok && more) mma_commit(&ms.empty[stage_of(ik)]);
+                }
+                if (!ok) {
+                    // let the MMAs in flight finish before shared and tensor memory go
+                    mma_commit(&ms.q_full);
+                    mbar_wait(&ms.q_full, 1);
+                }
             }
-            if (!ok) {
-                // let the MMAs in flight finish before shared and tensor memory go
-                mma_commit(&ms.q_full);
-                mbar_wait(&ms.q_full, 1);
-            }
-        }
-    } else if (warp == kLoadWarp) {
-        if (n_tiles > 0) {
-            if (lane == 0) {
-                const int tiles = w.n_keys[1] > 0 ? 2 : 1;
-                mbar_expect_tx(&ms.q_full, (uint32_t)tiles * kRegions * (uint32_t)(w.tokens * G) * 128u);
-                for (int q = 0; q < tiles; ++q)
-                    for (int c = 0; c < kRegions; ++c)
-                        tma_load_3d(sm + Sh::kQ + q * Sh::kTileBytes + c * Sh::kRegion, &maps.q, 64 * c, w.hk * G,
-                                    (int32_t)(w.rt.row0 + w.rt.t0 + q * w.tokens), &ms.q_full);
-            }
-            const int box = MODE == kPacked ? kTile : min(a.block_size, kTile);       // rows of one copy
-            const int boxes = kTile / box;
-            const int mine = lane / kRegions, region = lane % kRegions;               // this lane's copy
-            int issued = 0;
-            bool ok = true;
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const int64_t k0 = w.k_lo + (int64_t)j * kTile;
-                // copies that begin beyond the last key that a row sees are left out
-                const int live = MODE == kPacked ? 1 : (int)min((int64_t)boxes, (w.k_hi - k0 + box - 1) / box);
-                int32_t row = 0;
-                if (MODE != kPacked && mine < live) {
-                    const int64_t key = k0 + mine * box;
-                    const int32_t block = w.table[key / a.block_size];
-                    if (block < 0 || block >= a.n_blocks) {
-                        flag(p.status, KDA_DEV_BAD_SLOT);
-                        row = (int32_t)(a.n_blocks * a.n_kv_heads * a.block_size);     // past the end: reads zeros
-                    } else {
-                        row = (int32_t)((block * (int64_t)a.n_kv_heads + w.hk) * a.block_size + key % a.block_size);
+        } else if (warp == kLoadWarp) {
+            if (n_tiles > 0) {
+                if (lane == 0) {
+                    const int tiles = w.n_keys[1] > 0 ? 2 : 1;
+                    mbar_expect_tx(&ms.q_full, (uint32_t)tiles * kRegions * (uint32_t)(w.tokens * G) * 128u);
+                    for (int q = 0; q < tiles; ++q)
+                        for (int c = 0; c < kRegions; ++c)
+                            tma_load_3d(sm + Sh::kQ + q * Sh::kTileBytes + c * Sh::kRegion, &maps.q, 64 * c, w.hk * G,
+                                        (int32_t)(w.rt.row0 + w.rt.t0 + q * w.tokens), &ms.q_full);
+                }
+                const int box = MODE == kPacked ? kTile : min(a.block_size, kTile);       // rows of one copy
+                const int boxes = kTile / box;
+                const int mine = lane / kRegions, region = lane % kRegions;               // this lane's copy
+                int issued = 0;
+                bool ok = true;
+                for (int j = 0; j < n_tiles && ok; ++j) {
+                    const int64_t k0 = w.k_lo + (int64_t)j * kTile;
+                    // copies that begin beyond the last key that a row sees are left out
+                    const int live = MODE == kPacked ? 1 : (int)min((int64_t)boxes, (w.k_hi - k0 + box - 1) / box);
+                    int32_t row = 0;
+                    if (MODE != kPacked && mine < live) {
+                        const int64_t key = k0 + mine * box;
+                        const int32_t block = w.table[key / a.block_size];
+                        if (block < 0 || block >= a.n_blocks) {
+                            flag(p.status, KDA_DEV_BAD_SLOT);
+                            row = (int32_t)(a.n_blocks * a.n_kv_heads * a.block_size);     // past the end: reads zeros
+                        } else {
+                            row = (int32_t)((block * (int64_t)a.n_kv_heads + w.hk) * a.block_size + key % a.block_size);
+                        }
+                    }
+                    for (int kv = 0; kv < 2 && ok; ++kv) {
+                        const int i = 2 * j + kv, st = stage_of(i);
+                        if (i >= Sh::kStages && !(ok = __all_sync(0xffffffffu, waitb(&ms.empty[st], phase_of(i) ^ 1u)))) break;
+                        uint8_t* dst = sm + Sh::kRing + st * Sh::kTileBytes;
+                        const void* map = kv ? &maps.v : &maps.k;
+                        if (lane == 0) mbar_expect_tx(&ms.full[st], (uint32_t)(live * box) * 128u * kRegions);
+                        __syncwarp();
+                        if (mine < live) {
+                            uint8_t* to = dst + region * Sh::kRegion + mine * box * 128;
+                            if (MODE == kPacked) tma_load_3d(to, map, 64 * region, w.hk, (int32_t)(w.rt.row0 + k0), &ms.full[st]);
+                            else tma_load_2d(to, map, 64 * region, row, &ms.full[st]);
+                        }
+                        issued = i + 1;
                     }
                 }
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    const int i = 2 * j + kv, st = stage_of(i);
-                    if (i >= Sh::kStages && !(ok = __all_sync(0xffffffffu, waitb(&ms.empty[st], phase_of(i) ^ 1u)))) break;
-                    uint8_t* dst = sm + Sh::kRing + st * Sh::kTileBytes;
-                    const void* map = kv ? &maps.v : &maps.k;
-                    if (lane == 0) mbar_expect_tx(&ms.full[st], (uint32_t)(live * box) * 128u * kRegions);
-                    __syncwarp();
-                    if (mine < live) {
-                        uint8_t* to = dst + region * Sh::kRegion + mine * box * 128;
-                        if (MODE == kPacked) tma_load_3d(to, map, 64 * region, w.hk, (int32_t)(w.rt.row0 + k0), &ms.full[st]);
-                        else tma_load_2d(to, map, 64 * region, row, &ms.full[st]);
-                    }
-                    issued = i + 1;
+                if (!ok) {
+                    // copies in flight land before the block's shared memory goes
+                    mbar_wait(&ms.q_full, 0);
+                    for (int i = max(0, issued - Sh::kStages); i < issued; ++i) mbar_wait(&ms.full[stage_of(i)], phase_of(i));
                 }
             }
-            if (!ok) {
-                // copies in flight land before the block's shared memory goes
-                mbar_wait(&ms.q_full, 0);
-                for (int i = max(0, issued - Sh::kStages); i < issued; ++i) mbar_wait(&ms.full[stage_of(i)], phase_of(i));
-            }
-        }
-    } else if (warp >= kGuardWarp) {
-        const int gt = tid - 32 * kGuardWarp;
-        // These warps follow every load and release its stage with the MMAs, so that
-        // no barrier gets two phases ahead of their waits.
-        for (int i = 0; i < 2 * n_tiles; ++i) {
-            const int j = i >> 1;
-            if (!__all_sync(0xffffffffu, waitb(&ms.full[stage_of(i)], phase_of(i)))) break;
-            if (!(i & 1) || !edge(j)) {
-                if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
-                continue;
-            }
-            const int64_t k0 = w.k_lo + (int64_t)j * kTile;
-            uint8_t* v = sm + Sh::kRing + stage_of(i) * Sh::kTileBytes;
-            const int from = (int)max((int64_t)0, min((int64_t)kTile, w.all_see - k0));   // rows that not every row sees
-            const int none = (int)max((int64_t)0, min((int64_t)kTile, w.k_hi - k0));      // rows that no row sees
-            for (int x = gt; x < (kTile - from) * kRegions * 8; x += 32 * kGuardWarps) {
-                const int r = from + x / (kRegions * 8), y = x % (kRegions * 8), region = y >> 3, c = y & 7;
-                uint4* at = reinterpret_cast<uint4*>(v + region * Sh::kRegion + row64_chunk_off(r, c));
-                if (r >= none) {
-                    *at = make_uint4(0, 0, 0, 0);
+        } else {
+            const int gt = tid - 32 * kGuardWarp;
+            // These warps follow every load and release its stage with the MMAs, so that
+            // no barrier gets two phases ahead of their waits.
+            for (int i = 0; i < 2 * n_tiles; ++i) {
+                const int j = i >> 1;
+                if (!__all_sync(0xffffffffu, waitb(&ms.full[stage_of(i)], phase_of(i)))) break;
+                if (!(i & 1) || !edge(j)) {
+                    if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
                     continue;
                 }
-                uint4 u = *at;
-                uint32_t* e = &u.x;
-                uint32_t hit = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) hit |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
-                if (hit) {
-                    ms.poison = 1;
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t b = e[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
-                        if ((b & 0x7F80u) != 0x7F80u) continue;
-                        int32_t* first = b & 0x7Fu ? ms.first_nan : b & 0x8000u ? ms.first_neg : ms.first_pos;
-                        atomicMin(&first[region * 64 + c * 8 + k], (int32_t)(k0 + r));
-                        e[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                const int64_t k0 = w.k_lo + (int64_t)j * kTile;
+                uint8_t* v = sm + Sh::kRing + stage_of(i) * Sh::kTileBytes;
+                const int from = (int)max((int64_t)0, min((int64_t)kTile, w.all_see - k0));   // rows that not every row sees
+                const int none = (int)max((int64_t)0, min((int64_t)kTile, w.k_hi - k0));      // rows that no row sees
+                for (int x = gt; x < (kTile - from) * kRegions * 8; x += 32 * kGuardWarps) {
+                    const int r = from + x / (kRegions * 8), y = x % (kRegions * 8), region = y >> 3, c = y & 7;
+                    uint4* at = reinterpret_cast<uint4*>(v + region * Sh::kRegion + row64_chunk_off(r, c));
+                    if (r >= none) {
+                        *at = make_uint4(0, 0, 0, 0);
+                        continue;
                     }
-                    *at = u;
+                    uint4 u = *at;
+                    uint32_t* e = &u.x;
+                    uint32_t hit = 0;
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k) hit |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
+                    if (hit) {
+                        ms.poison = 1;
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t b = e[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
+                            if ((b & 0x7F80u) != 0x7F80u) continue;
+                            int32_t* first = b & 0x7Fu ? ms.first_nan : b & 0x8000u ? ms.first_neg : ms.first_pos;
+                            atomicMin(&first[region * 64 + c * 8 + k], (int32_t)(k0 + r));
+                            e[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+                        *at = u;
+                    }
                 }
+                __threadfence_block();
+                fence_async_smem();
+                mbar_arrive(&ms.guarded[stage_of(i)]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
             }
-            __threadfence_block();
-            fence_async_smem();
-            mbar_arrive(&ms.guarded[stage_of(i)]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
         }
     } else {
         // ------------------------------------------------------------------ softmax
+        more_registers<kSoftmaxRegs>();
         const int q = warp >> 2;
         const int r = 32 * (warp & 3) + lane;                     // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int t = w.rt.t0 + q * w.tokens + r / G, g = r % G;
         const bool live = r < w.tokens * G && t < w.rt.n;
-        // keys that this row sees, and keys that all rows of the tile see
+        // keys that this row sees, and keys that all rows of the tile see, from k_lo on
         const int64_t seen = MODE == kPrefix ? w.k_hi : min(w.k_hi, w.first + t + 1);
-        const int64_t tile_sees = MODE == kPrefix ? w.k_hi : min(w.k_hi, w.first + w.rt.t0 + q * w.tokens + 1);
-        const float c = fabsf(a.scale) * kLog2e;
+        const int row_sees = (int)max((int64_t)0, seen - w.k_lo);
+        const int tile_sees =
+            (int)max((int64_t)0, (MODE == kPrefix ? w.k_hi : min(w.k_hi, w.first + w.rt.t0 + q * w.tokens + 1)) - w.k_lo);
+        // a scale of 0 becomes the least normal number, so that a hidden score of -inf stays one
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
         const int n = w.n_keys[q];
-        float m = -CUDART_INF_F, l = 0.f;
+        float m = -CUDART_INF_F;
+        uint64_t l2 = pair2(0.f);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             if (!(ok = __all_sync(0xffffffffu, waitb(&ms.s_full[q], j & 1)))) break;
             fence_after_sync();
-            const int64_t k0 = w.k_lo + (int64_t)j * kTile;
-            const bool masked = k0 + kTile > tile_sees;
-            const int visible = (int)max((int64_t)0, min((int64_t)kTile, seen - k0));
             uint32_t s[kTile];
 #pragma unroll
             for (int x = 0; x < kTile; x += 32) tmem_ld32(tS(q) + lanes + x, s + x);
             tmem_wait_ld();
-            if (masked) {
+            if ((j + 1) * kTile > tile_sees) {
+                const int visible = row_sees - j * kTile;
 #pragma unroll
                 for (int x = 0; x < kTile; ++x) s[x] = x < visible ? s[x] : 0xFF800000u;
             }
-            float mx = -CUDART_INF_F;
+            float mx[4] = {m, m, m, m};
 #pragma unroll
-            for (int x = 0; x < kTile; x += 2) mx = fmaxf(fmaxf(mx, __uint_as_float(s[x])), __uint_as_float(s[x + 1]));
-            const float mn = fmaxf(m, mx);
+            for (int x = 0; x < kTile; x += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
+            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (j == 0) {
                 m = mn;
             } else {
@@ -424,7 +463,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2((m - mn) * c) : 1.f;
                     m = grow ? mn : m;
-                    l *= f;
+                    const float2 lf = unpair2(l2);
+                    l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
 #pragma unroll
                     for (int x = 0; x < D; x += 16) {
                         uint32_t o[16];
@@ -436,27 +476,26 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                 }
             }
-            const float off = m == -CUDART_INF_F ? 0.f : -m * c;
-            float sum[2] = {0.f, 0.f};
-            uint32_t w2[kTile / 2];
+            const uint64_t off2 = pair2(m == -CUDART_INF_F ? 0.f : -m * c), c2 = pair2(c);
+            uint64_t sum[2] = {pair2(0.f), pair2(0.f)};
 #pragma unroll
-            for (int x = 0; x < kTile; x += 2) {
-                float p0 = ex2(fmaf(__uint_as_float(s[x]), c, off)), p1 = ex2(fmaf(__uint_as_float(s[x + 1]), c, off));
-                if (masked) {
-                    p0 = x < visible ? p0 : 0.f;
-                    p1 = x + 1 < visible ? p1 : 0.f;
+            for (int h = 0; h < 2; ++h) {                          // 64 keys each
+                uint32_t w2[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float2 y = unpair2(fma2(pair2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, off2));
+                    const float p0 = ex2(y.x), p1 = ex2(y.y);
+                    sum[x & 1] = add2(sum[x & 1], pair2(__float_as_uint(p0), __float_as_uint(p1)));
+                    w2[x] = pack_bf16(p0, p1);
                 }
-                sum[0] += p0;
-                sum[1] += p1;
-                w2[x / 2] = pack_bf16(p0, p1);
+                tmem_st32(tS(q) + lanes + 32 * h, w2);
             }
-            tmem_st32(tS(q) + lanes, w2);
-            tmem_st32(tS(q) + lanes + 32, w2 + 32);
-            l += sum[0] + sum[1];
+            l2 = add2(l2, add2(sum[0], sum[1]));
             tmem_wait_st();
             fence_before_sync();
             mbar_arrive(&ms.p_ready[q]);
         }
+        const float l = unpair2(l2).x + unpair2(l2).y;
         if (ok && n > 0) ok = __all_sync(0xffffffffu, waitb(&ms.o_done[q], 0));
         fence_after_sync();
         if (ok) {

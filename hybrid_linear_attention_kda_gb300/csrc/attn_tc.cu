@@ -82,14 +82,42 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int32_t
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-// D[tmem] (+)= A[tmem, bf16 pairs] x B[smem desc]^T.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The MMA warp runs its loop as a whole and lets one lane issue, so that the
+// descriptors stay in uniform registers: issued from inside a one-lane branch, each
+// MMA took 90 cycles of register moves, against 64 of the tensor pipe.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+// D[tmem] (+)= A[smem desc] x B[smem desc]^T, issued where `leader` is set.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(leader),
+        "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem, bf16 pairs] x B[smem desc]^T.
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(leader),
+        "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+        "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -245,15 +273,17 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tbase = ms.tslot;
-    auto tS = [&](int q) { return tbase + 128u * q; };
-    auto tO = [&](int q) { return tbase + 256u + 128u * q; };
+    constexpr uint32_t tbase = 0;                 // all of tensor memory is this block's
+    auto tS = [](int q) { return tbase + 128u * q; };
+    auto tO = [](int q) { return tbase + 256u + 128u * q; };
     auto waitb = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (mbar_wait(bar, parity)) return true;
         atomicExch(&ms.failed, 1);
         flag(p.status, KDA_DEV_WAIT_TIMEOUT);
         return false;
     };
+    // the same for a whole warp, whose lanes then agree
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, waitb(bar, parity)); };
     const int n_tiles = max(w.n_keys[0], w.n_keys[1]);
     // ring stage of the i-th load (K of tile j: 2 j, V of tile j: 2 j + 1) and the parity of its phase
     auto stage_of = [&](int i) { return i % Sh::kStages; };
@@ -266,7 +296,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     if (warp >= kMmaWarp) {
         fewer_registers<kOtherRegs>();
         if (warp == kMmaWarp) {
-            if (lane == 0 && n_tiles > 0) {
+            if (n_tiles > 0) {
+                const uint32_t leader = elect_one();
                 const uint32_t id_s = idesc_bf16(kTile, kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
                 const uint32_t id_o = idesc_bf16(kTile, D, false, true);
                 const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
@@ -276,48 +307,48 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
-                        mma_bf16(tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
+                        mma_ss(leader, tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
                     }
-                    mma_commit(&ms.s_full[q]);
+                    commit(leader, &ms.s_full[q]);
                 };
                 auto values = [&](int q, int stage, bool first) {
                     const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
     #pragma unroll
                     for (int ks = 0; ks < kTile / 16; ++ks)
-                        mma_bf16_ts(tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
+                        mma_ts(leader, tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
                 };
-                bool ok = waitb(&ms.q_full, 0) && waitb(&ms.full[0], 0);
+                bool ok = wait_all(&ms.q_full, 0) && wait_all(&ms.full[0], 0);
                 if (ok) {
                     fence_after_sync();
                     for (int q = 0; q < 2; ++q)
                         if (w.n_keys[q] > 0) scores(q, 0);
-                    mma_commit(&ms.empty[0]);
+                    commit(leader, &ms.empty[0]);
                 }
                 uint32_t guard_phase = 0;                             // a bit for each stage
                 for (int j = 0; j < n_tiles && ok; ++j) {
                     const int iv = 2 * j + 1, ik = 2 * j + 2;
-                    if (!(ok = waitb(&ms.full[stage_of(iv)], phase_of(iv)))) break;
+                    if (!(ok = wait_all(&ms.full[stage_of(iv)], phase_of(iv)))) break;
                     if (edge(j)) {
-                        if (!(ok = waitb(&ms.guarded[stage_of(iv)], guard_phase >> stage_of(iv) & 1))) break;
+                        if (!(ok = wait_all(&ms.guarded[stage_of(iv)], guard_phase >> stage_of(iv) & 1))) break;
                         guard_phase ^= 1u << stage_of(iv);
                     }
                     const bool more = j + 1 < n_tiles;
-                    if (more && !(ok = waitb(&ms.full[stage_of(ik)], phase_of(ik)))) break;
+                    if (more && !(ok = wait_all(&ms.full[stage_of(ik)], phase_of(ik)))) break;
                     for (int q = 0; q < 2 && ok; ++q) {
                         if (j < w.n_keys[q]) {
-                            if (!(ok = waitb(&ms.p_ready[q], j & 1))) break;
+                            if (!(ok = wait_all(&ms.p_ready[q], j & 1))) break;
                             fence_after_sync();
                             values(q, stage_of(iv), j == 0);
-                            if (j + 1 == w.n_keys[q]) mma_commit(&ms.o_done[q]);
+                            if (j + 1 == w.n_keys[q]) commit(leader, &ms.o_done[q]);
                         }
-                        if (q == 1) mma_commit(&ms.empty[stage_of(iv)]);
+                        if (q == 1) commit(leader, &ms.empty[stage_of(iv)]);
                         if (j + 1 < w.n_keys[q]) scores(q, stage_of(ik));
                     }
-                    if (ok && more) mma_commit(&ms.empty[stage_of(ik)]);
+                    if (ok && more) commit(leader, &ms.empty[stage_of(ik)]);
                 }
                 if (!ok) {
                     // let the MMAs in flight finish before shared and tensor memory go
-                    mma_commit(&ms.q_full);
+                    commit(leader, &ms.q_full);
                     mbar_wait(&ms.q_full, 1);
                 }
             }
@@ -353,7 +384,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                     for (int kv = 0; kv < 2 && ok; ++kv) {
                         const int i = 2 * j + kv, st = stage_of(i);
-                        if (i >= Sh::kStages && !(ok = __all_sync(0xffffffffu, waitb(&ms.empty[st], phase_of(i) ^ 1u)))) break;
+                        if (i >= Sh::kStages && !(ok = wait_all(&ms.empty[st], phase_of(i) ^ 1u))) break;
                         uint8_t* dst = sm + Sh::kRing + st * Sh::kTileBytes;
                         const void* map = kv ? &maps.v : &maps.k;
                         if (lane == 0) mbar_expect_tx(&ms.full[st], (uint32_t)(live * box) * 128u * kRegions);
@@ -378,7 +409,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             // no barrier gets two phases ahead of their waits.
             for (int i = 0; i < 2 * n_tiles; ++i) {
                 const int j = i >> 1;
-                if (!__all_sync(0xffffffffu, waitb(&ms.full[stage_of(i)], phase_of(i)))) break;
+                if (!wait_all(&ms.full[stage_of(i)], phase_of(i))) break;
                 if (!(i & 1) || !edge(j)) {
                     if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
                     continue;
@@ -438,7 +469,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         uint64_t l2 = pair2(0.f);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            if (!(ok = __all_sync(0xffffffffu, waitb(&ms.s_full[q], j & 1)))) break;
+            if (!(ok = wait_all(&ms.s_full[q], j & 1))) break;
             fence_after_sync();
             uint32_t s[kTile];
 #pragma unroll
@@ -496,7 +527,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             mbar_arrive(&ms.p_ready[q]);
         }
         const float l = unpair2(l2).x + unpair2(l2).y;
-        if (ok && n > 0) ok = __all_sync(0xffffffffu, waitb(&ms.o_done[q], 0));
+        if (ok && n > 0) ok = wait_all(&ms.o_done[q], 0);
         fence_after_sync();
         if (ok) {
             const int64_t row = w.rt.row0 + t;
@@ -555,7 +586,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     __syncthreads();
     if (warp == kMmaWarp) {
         fence_after_sync();
-        tmem_dealloc(tbase, kTmemCols);
+        tmem_dealloc(ms.tslot, kTmemCols);
     }
 }
 

@@ -14,10 +14,13 @@
 // and of K and V into a ring of stages, warps 10-11 make the values at the edge of
 // what the rows see safe (below).
 //
-// The maximum that weights refer to is only moved when it has grown by more than a
-// factor of 2^8: until then the weights stay below 2^8, l and o are sums of the
-// same weights whatever they refer to, and O needs no rescaling.  A rescale is
-// done by the rows' own threads: S's commit came after the last product into O.
+// The maximum that weights refer to is the first tile's, and is only moved when a
+// half tile's weights add up to more than 2^10: until then no weight is larger, l
+// and o are sums of the same weights whatever they refer to (their rounding is
+// relative), and neither a maximum nor a rescaled O is needed.  A move is done by
+// the rows' own threads, while no product into O is under way: for the first half of
+// a tile because its scores' commit came after the last one, for the second half
+// after a commit that follows the first half's product.
 //
 // Hidden values.  A product with P has 0 * v for hidden keys, which is NaN for an
 // infinite or NaN v.  In the tiles that some row sees only a part of, warps 10-11
@@ -26,7 +29,7 @@
 // NaN, +inf or -inf; at the end, rows that see such a key get it added.
 //
 // Bound by the tensor pipe: 4 d flops per (row, key) pair.  Measured on 4 x 8192
-// tokens, 32 query and 8 key/value heads, d = 128: 2.23 ms, 986 TFLOP/s.
+// tokens, 32 query and 8 key/value heads, d = 128: 1.48 ms, 1485 TFLOP/s.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -46,7 +49,7 @@ constexpr int kThreads = 384;
 // 256 * 208 + 128 * 88 <= 384 * 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMaxGrowth = 8.f;             // log2 of how far weights may exceed 1
+constexpr float kMostWeight = 1024.f;         // of a half tile, before the maximum moves
 constexpr uint32_t kTmemCols = 512;           // S0 0, S1 128, O0 256, O1 384
 
 enum Mode { kPacked, kPaged, kPrefix };
@@ -61,7 +64,7 @@ template <int D> struct Shape {
 template <int D> struct Misc {
     uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages];
     uint64_t guarded[Shape<D>::kStages];
-    uint64_t q_full, s_full[2], p_ready[2], o_done[2];
+    uint64_t q_full, s_full[2], p_ready[2][2], half_done[2], o_done[2];   // p_ready: [row tile][half of the keys]
     uint32_t tslot;
     int32_t failed, poison;
     int32_t first_nan[D], first_pos[D], first_neg[D];            // first key of a column that holds such a value
@@ -173,6 +176,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// A place in the ring of stages, as it moves from load to load: one warp's scalar
+// arithmetic between two MMAs is time that the tensor pipe waits.
+struct Ring {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t stages) {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 // ------------------------------------------------------------------ the block's work
 
 struct Work {
@@ -262,7 +277,9 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         mbar_init(&ms.q_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.s_full[i], 1);
-            mbar_init(&ms.p_ready[i], 128);
+            mbar_init(&ms.p_ready[i][0], 4);
+            mbar_init(&ms.p_ready[i][1], 4);
+            mbar_init(&ms.half_done[i], 1);
             mbar_init(&ms.o_done[i], 1);
         }
         ms.failed = 0;
@@ -288,8 +305,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     // ring stage of the i-th load (K of tile j: 2 j, V of tile j: 2 j + 1) and the parity of its phase
     auto stage_of = [&](int i) { return i % Sh::kStages; };
     auto phase_of = [&](int i) { return (uint32_t)(i / Sh::kStages) & 1u; };
-    // some row sees only a part of tile j
-    auto edge = [&](int j) { return w.k_lo + (int64_t)(j + 1) * kTile > w.all_see; };
+    // from this tile on some row sees only a part of the keys
+    const int first_edge = (int)(max((int64_t)0, w.all_see - w.k_lo) / kTile);
 
     // the register split is made inside the branches: after a merge of the two the
     // compiler would hold everything to the smaller share
@@ -311,10 +328,10 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                     commit(leader, &ms.s_full[q]);
                 };
-                auto values = [&](int q, int stage, bool first) {
+                auto values = [&](int q, int half, int stage, bool first) {
                     const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
     #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
+                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
                         mma_ts(leader, tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
                 };
                 bool ok = wait_all(&ms.q_full, 0) && wait_all(&ms.full[0], 0);
@@ -324,27 +341,44 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         if (w.n_keys[q] > 0) scores(q, 0);
                     commit(leader, &ms.empty[0]);
                 }
-                uint32_t guard_phase = 0;                             // a bit for each stage
-                for (int j = 0; j < n_tiles && ok; ++j) {
-                    const int iv = 2 * j + 1, ik = 2 * j + 2;
-                    if (!(ok = wait_all(&ms.full[stage_of(iv)], phase_of(iv)))) break;
-                    if (edge(j)) {
-                        if (!(ok = wait_all(&ms.guarded[stage_of(iv)], guard_phase >> stage_of(iv) & 1))) break;
-                        guard_phase ^= 1u << stage_of(iv);
+                uint32_t guard_phase = 0;                         // a bit for each stage
+                Ring v;
+                v.next(Sh::kStages);
+                // Waits for the copies stand between the MMAs of one row tile, where the
+                // tensor pipe still has work.
+                auto v_ready = [&](int j) -> bool {
+                    if (!wait_all(&ms.full[v.stage], v.phase)) return false;
+                    if (j >= first_edge) {
+                        if (!wait_all(&ms.guarded[v.stage], guard_phase >> v.stage & 1)) return false;
+                        guard_phase ^= 1u << v.stage;
                     }
+                    return true;
+                };
+                ok = ok && v_ready(0);
+                for (int j = 0; j < n_tiles && ok; ++j) {
+                    const uint32_t vs = v.stage;
+                    v.next(Sh::kStages);
+                    const Ring k = v;
+                    v.next(Sh::kStages);
                     const bool more = j + 1 < n_tiles;
-                    if (more && !(ok = wait_all(&ms.full[stage_of(ik)], phase_of(ik)))) break;
-                    for (int q = 0; q < 2 && ok; ++q) {
+                    if (more && !(ok = wait_all(&ms.full[k.stage], k.phase))) break;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
                         if (j < w.n_keys[q]) {
-                            if (!(ok = wait_all(&ms.p_ready[q], j & 1))) break;
+                            if (!(ok = wait_all(&ms.p_ready[q][0], j & 1))) break;
                             fence_after_sync();
-                            values(q, stage_of(iv), j == 0);
+                            values(q, 0, vs, j == 0);
+                            commit(leader, &ms.half_done[q]);
+                            if (!(ok = wait_all(&ms.p_ready[q][1], j & 1))) break;
+                            fence_after_sync();
+                            values(q, 1, vs, false);
                             if (j + 1 == w.n_keys[q]) commit(leader, &ms.o_done[q]);
                         }
-                        if (q == 1) commit(leader, &ms.empty[stage_of(iv)]);
-                        if (j + 1 < w.n_keys[q]) scores(q, stage_of(ik));
+                        if (q == 1) commit(leader, &ms.empty[vs]);
+                        if (j + 1 < w.n_keys[q]) scores(q, k.stage);
                     }
-                    if (ok && more) commit(leader, &ms.empty[stage_of(ik)]);
+                    if (ok && more) commit(leader, &ms.empty[k.stage]);
+                    if (ok && more && !(ok = v_ready(j + 1))) break;
                 }
                 if (!ok) {
                     // let the MMAs in flight finish before shared and tensor memory go
@@ -367,6 +401,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 const int mine = lane / kRegions, region = lane % kRegions;               // this lane's copy
                 int issued = 0;
                 bool ok = true;
+                Ring ring;
                 for (int j = 0; j < n_tiles && ok; ++j) {
                     const int64_t k0 = w.k_lo + (int64_t)j * kTile;
                     // copies that begin beyond the last key that a row sees are left out
@@ -383,8 +418,9 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         }
                     }
                     for (int kv = 0; kv < 2 && ok; ++kv) {
-                        const int i = 2 * j + kv, st = stage_of(i);
-                        if (i >= Sh::kStages && !(ok = wait_all(&ms.empty[st], phase_of(i) ^ 1u))) break;
+                        const int i = 2 * j + kv, st = (int)ring.stage;
+                        if (i >= Sh::kStages && !(ok = wait_all(&ms.empty[st], ring.phase ^ 1u))) break;
+                        ring.next(Sh::kStages);
                         uint8_t* dst = sm + Sh::kRing + st * Sh::kTileBytes;
                         const void* map = kv ? &maps.v : &maps.k;
                         if (lane == 0) mbar_expect_tx(&ms.full[st], (uint32_t)(live * box) * 128u * kRegions);
@@ -407,15 +443,18 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             const int gt = tid - 32 * kGuardWarp;
             // These warps follow every load and release its stage with the MMAs, so that
             // no barrier gets two phases ahead of their waits.
+            Ring ring;
             for (int i = 0; i < 2 * n_tiles; ++i) {
                 const int j = i >> 1;
-                if (!wait_all(&ms.full[stage_of(i)], phase_of(i))) break;
-                if (!(i & 1) || !edge(j)) {
-                    if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
+                const uint32_t st = ring.stage;
+                if (!wait_all(&ms.full[st], ring.phase)) break;
+                ring.next(Sh::kStages);
+                if (!(i & 1) || j < first_edge) {
+                    if (lane == 0) mbar_arrive(&ms.empty[st]);
                     continue;
                 }
                 const int64_t k0 = w.k_lo + (int64_t)j * kTile;
-                uint8_t* v = sm + Sh::kRing + stage_of(i) * Sh::kTileBytes;
+                uint8_t* v = sm + Sh::kRing + st * Sh::kTileBytes;
                 const int from = (int)max((int64_t)0, min((int64_t)kTile, w.all_see - k0));   // rows that not every row sees
                 const int none = (int)max((int64_t)0, min((int64_t)kTile, w.k_hi - k0));      // rows that no row sees
                 for (int x = gt; x < (kTile - from) * kRegions * 8; x += 32 * kGuardWarps) {
@@ -444,9 +483,9 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 }
                 __threadfence_block();
                 fence_async_smem();
-                mbar_arrive(&ms.guarded[stage_of(i)]);
+                mbar_arrive(&ms.guarded[st]);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.empty[stage_of(i)]);
+                if (lane == 0) mbar_arrive(&ms.empty[st]);
             }
         }
     } else {
@@ -480,51 +519,65 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
 #pragma unroll
                 for (int x = 0; x < kTile; ++x) s[x] = x < visible ? s[x] : 0xFF800000u;
             }
-            float mx[4] = {m, m, m, m};
+            auto maximum = [&]() {                                 // of the tile's scores, and m
+                float top[4] = {m, m, m, m};
 #pragma unroll
-            for (int x = 0; x < kTile; x += 8)
+                for (int x = 0; x < kTile; x += 8)
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
-            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (j == 0) {
-                m = mn;
-            } else {
-                const bool grow = (mn - m) * c > kMaxGrowth;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? ex2((m - mn) * c) : 1.f;
-                    m = grow ? mn : m;
-                    const float2 lf = unpair2(l2);
-                    l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
-#pragma unroll
-                    for (int x = 0; x < D; x += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(tO(q) + lanes + x, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        tmem_st16(tO(q) + lanes + x, o);
-                    }
-                }
-            }
-            const uint64_t off2 = pair2(m == -CUDART_INF_F ? 0.f : -m * c), c2 = pair2(c);
-            uint64_t sum[2] = {pair2(0.f), pair2(0.f)};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {                          // 64 keys each
+                    for (int y = 0; y < 4; ++y)
+                        top[y] = fmaxf(fmaxf(top[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
+                return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            };
+            // the weights of one half of the keys, for the maximum as it stands, to P; returns their sum
+            auto weights = [&](int h) -> uint64_t {
+                const uint64_t off2 = pair2(m == -CUDART_INF_F ? 0.f : -m * c), c2 = pair2(c);
+                uint64_t sums[2] = {pair2(0.f), pair2(0.f)};
                 uint32_t w2[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
                     const float2 y = unpair2(fma2(pair2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, off2));
                     const float p0 = ex2(y.x), p1 = ex2(y.y);
-                    sum[x & 1] = add2(sum[x & 1], pair2(__float_as_uint(p0), __float_as_uint(p1)));
+                    sums[x & 1] = add2(sums[x & 1], pair2(__float_as_uint(p0), __float_as_uint(p1)));
                     w2[x] = pack_bf16(p0, p1);
                 }
                 tmem_st32(tS(q) + lanes + 32 * h, w2);
+                return add2(sums[0], sums[1]);
+            };
+            if (j == 0) m = maximum();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint64_t sum = weights(h);
+                const float2 both = unpair2(sum);
+                const bool grow = !(both.x + both.y <= kMostWeight);
+                if (__any_sync(0xffffffffu, grow)) {
+                    // rare: move the maximum, rescale what was summed so far, weigh again
+                    if (h == 1) ok = ok && wait_all(&ms.half_done[q], j & 1);
+                    fence_after_sync();
+                    const float mx = grow ? maximum() : m;         // a row's result depends on no other row
+                    const float f = mx > m ? ex2((m - mx) * c) : 1.f;
+                    m = mx;
+                    const float2 lf = unpair2(l2);
+                    l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
+                    if (j > 0 || h == 1) {
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO(q) + lanes + x, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                            tmem_st16(tO(q) + lanes + x, o);
+                        }
+                    }
+                    tmem_wait_st();
+                    sum = weights(h);
+                }
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.p_ready[q][h]);
+                l2 = add2(l2, sum);
             }
-            l2 = add2(l2, add2(sum[0], sum[1]));
-            tmem_wait_st();
-            fence_before_sync();
-            mbar_arrive(&ms.p_ready[q]);
         }
         const float l = unpair2(l2).x + unpair2(l2).y;
         if (ok && n > 0) ok = wait_all(&ms.o_done[q], 0);

@@ -11,21 +11,25 @@
 //     O_q += P_q V       128 x d x 128, P (bf16) in TMEM in S's place, O in TMEM
 // Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1 (a thread owns a row: no
 // reductions between threads), warp 8 issues the MMAs, warp 9 the TMA copies of Q
-// and of K and V into a ring of stages, warps 10-11 make the values at the edge of
-// what the rows see safe (below).
+// and of K and V into a ring of stages, warp 10 makes the values at the edge of what
+// the rows see safe (below), warp 11 finds the block's next item of work.
+//
+// Items.  The grid has a block for each item (two row tiles of one key/value head),
+// but a running block takes over the items of blocks that have not started
+// (clusterlaunchcontrol), so that loads, scores and products of the next item run
+// while the last one's output is written, and short and long items even out.  Every
+// role walks the same items with its own running barrier phases.
 //
 // The maximum that weights refer to is the first tile's, and is only moved when a
-// half tile's weights add up to more than 2^10: until then no weight is larger, l
+// row's weights of a tile add up to more than 2^10: until then no weight is larger, l
 // and o are sums of the same weights whatever they refer to (their rounding is
-// relative), and neither a maximum nor a rescaled O is needed.  A move is done by
-// the rows' own threads, while no product into O is under way: for the first half of
-// a tile because its scores' commit came after the last one, for the second half
-// after a commit that follows the first half's product.
+// relative), and neither a maximum nor a rescaled O is needed.  A move is done by the
+// row's own thread: a tile's scores are committed after the last product into O.
 //
 // Hidden values.  A product with P has 0 * v for hidden keys, which is NaN for an
-// infinite or NaN v.  In the tiles that some row sees only a part of, warps 10-11
-// therefore zero the values of keys that no row sees, and replace the non-finite
-// values of the others by zero and note the first key of each column that held a
+// infinite or NaN v.  In the tiles that some row sees only a part of, warp 10
+// therefore zeroes the values of keys that no row sees, and replaces the non-finite
+// values of the others by zero and notes the first key of each column that held a
 // NaN, +inf or -inf; at the end, rows that see such a key get it added.
 //
 // Bound by the tensor pipe: 4 d flops per (row, key) pair.  Measured on 4 x 8192
@@ -43,13 +47,17 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;                    // rows of a tile, keys of a tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kGuardWarp = 10, kGuardWarps = 2;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kGuardWarp = 10;   // 11: the items
+constexpr int kItemReaders = 11;              // warps that read an item: all but its own
 constexpr int kThreads = 384;
 // Registers a thread: 168 at launch; the softmax warps hold a whole row of scores.
-// 256 * 208 + 128 * 88 <= 384 * 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// 256 * 216 + 128 * 72 <= 384 * 168.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kMostWeight = 1024.f;         // of a half tile, before the maximum moves
+constexpr float kMostWeight = 1024.f;         // of a row's tile, before the maximum moves
+// The maximum of a row that has seen only scores of -inf: the first score above it
+// gives an infinite weight, which moves it.
+constexpr float kLeastMaximum = -1e30f;
 constexpr uint32_t kTmemCols = 512;           // S0 0, S1 128, O0 256, O1 384
 
 enum Mode { kPacked, kPaged, kPrefix };
@@ -61,13 +69,29 @@ template <int D> struct Shape {
     static constexpr uint32_t kQ = 0, kRing = 2 * kTileBytes, kMisc = kRing + kStages * kTileBytes;
 };
 
+// One item of work; positions fit 32 bits (a table row has fewer than 2^31).
+struct Item {
+    int64_t row0;                 // packed row of the first token (or member)
+    int32_t live;                 // 0: no further items
+    int32_t t0, n;                // first token of the item, tokens of the sequence
+    int32_t hk, split;
+    int32_t table_row;
+    int32_t first;                // token t sees the keys j <= first + t
+    int32_t k_lo, k_hi;           // keys that some row of the item sees
+    int32_t all_see;              // every row sees the keys below this one
+    int32_t n_keys[2];            // key tiles of each row tile
+};
+
 template <int D> struct Misc {
     uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages];
     uint64_t guarded[Shape<D>::kStages];
-    uint64_t q_full, s_full[2], p_ready[2][2], half_done[2], o_done[2];   // p_ready: [row tile][half of the keys]
+    uint64_t item_full[2], item_empty[2], next, q_full, q_free, drained;
+    uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
+    alignas(16) uint4 next_block;                                 // clusterlaunchcontrol's answer
+    Item item[2];
     uint32_t tslot;
-    int32_t failed, poison;
-    int32_t first_nan[D], first_pos[D], first_neg[D];            // first key of a column that holds such a value
+    int32_t poison;                                               // the item that the notes below belong to
+    int32_t first_nan[D], first_pos[D], first_neg[D];             // first key of a column that holds such a value
 };
 
 template <int D> constexpr size_t smem_bytes() { return Shape<D>::kMisc + sizeof(Misc<D>) + 1024; }
@@ -151,6 +175,28 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Asks for the work of a block that has not started; the answer arrives at `to` with 16 bytes on `bar`.
+__device__ __forceinline__ void ask_next_block(uint4* to, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(to)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The answer: the block's index, or -1.
+__device__ __forceinline__ int64_t next_block(const uint4* from) {
+    uint32_t taken, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(taken), "=r"(x)
+        : "r"(smem_u32(from))
+        : "memory");
+    return taken ? (int64_t)x : -1;
+}
+
 // Pairs of fp32 values in one 64-bit register, for the two-wide fp32 instructions.
 __device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) {
     uint64_t r;
@@ -188,65 +234,90 @@ struct Ring {
     }
 };
 
-// ------------------------------------------------------------------ the block's work
+// ------------------------------------------------------------------ items
 
-struct Work {
-    RowTile rt;
-    int hk, split;
-    int64_t K, first;             // keys of the sequence; row of token t sees the keys j <= first + t
-    int64_t k_lo, k_hi;           // keys that some row of the block sees
-    int64_t all_see;              // every row sees the keys below this one
-    int n_keys[2];                // key tiles of each row tile
-    int tokens;                   // of a row tile
-    const int32_t* table;
+// The finder's place among the sequences: tiles of the ones before `s`.
+struct Place {
+    int32_t s = 0;
+    int64_t tiles = 0;
 };
 
+// Fills `it` for grid index `block`; false when that block has nothing to do.  One
+// warp; later indexes mostly lie further on, so the search goes on where the last one
+// ended.  Tiles of one sequence come last first: the later ones see more keys.
 template <int MODE>
-__device__ bool find_work(const AttnTileLaunch& p, Work& w) {
+__device__ bool find_item(const AttnTileLaunch& p, int64_t block, Place& place, Item& it) {
     const kda_attn_prefill_args& a = p.a;
-    const int G = a.n_heads / a.n_kv_heads;
-    const int64_t idx = blockIdx.x / a.n_kv_heads;
-    w.hk = (int)(blockIdx.x - idx * a.n_kv_heads);
-    w.tokens = kTile / G;
-    w.split = MODE == kPrefix ? (int)(idx % p.n_split) : 0;
-    w.rt = find_tile<kThreads>(a.cu_seqlens, a.n_seqs, a.total_tokens, 2 * w.tokens, MODE == kPrefix ? idx / p.n_split : idx,
-                               MODE != kPrefix && blockIdx.x == 0, KDA_DEV_BAD_SEQLENS, p.status);
-    if (w.rt.seq < 0) return false;
+    const int lane = threadIdx.x & 31;
+    const int tokens = kTile / (a.n_heads / a.n_kv_heads);
+    int64_t idx = block / a.n_kv_heads;
+    it.hk = (int32_t)(block - idx * a.n_kv_heads);
+    it.split = 0;
+    if (MODE == kPrefix) {
+        it.split = (int32_t)(idx % p.n_split);
+        idx /= p.n_split;
+    }
+    if (idx < place.tiles) place = Place{};
+    int32_t seq = 0;
+    for (; place.s < a.n_seqs; place.s += 32) {
+        const int32_t s = place.s + lane;
+        int64_t lo = 0, hi = 0;
+        if (s < a.n_seqs) {
+            lo = a.cu_seqlens[s];
+            hi = a.cu_seqlens[s + 1];
+            if (lo < 0 || hi < lo || hi > a.total_tokens) hi = lo;
+        }
+        const int64_t mine = (hi - lo + 2 * tokens - 1) / (2 * tokens);
+        int64_t upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        upto += place.tiles;
+        const uint32_t here = __ballot_sync(0xffffffffu, idx < upto);
+        if (here) {
+            const int src = __ffs(here) - 1;
+            it.row0 = __shfl_sync(0xffffffffu, lo, src);
+            it.n = (int32_t)(__shfl_sync(0xffffffffu, hi, src) - it.row0);
+            it.t0 = (int32_t)(__shfl_sync(0xffffffffu, upto, src) - 1 - idx) * 2 * tokens;
+            seq = place.s + src;
+            it.table_row = MODE == kPrefix ? (int32_t)it.row0 : seq;
+            break;
+        }
+        place.tiles = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (place.s >= a.n_seqs) return false;
     const int64_t cap = (int64_t)a.table_stride * a.block_size;
-    w.table = nullptr;
+    int64_t K;
     if (MODE == kPacked) {
-        w.K = w.rt.n;
-        w.first = 0;
+        K = it.n;
     } else if (MODE == kPaged) {
-        w.K = a.kv_lens[w.rt.seq];
-        w.table = a.block_table + (int64_t)w.rt.seq * a.table_stride;
-        if (w.K < 0 || w.K > cap) {
-            if (threadIdx.x == 0) flag(p.status, KDA_DEV_BAD_SEQLENS);
+        K = a.kv_lens[seq];
+        if (K < 0 || K > cap) {
+            if (lane == 0) flag(p.status, KDA_DEV_BAD_SEQLENS);
             return false;
         }
-        w.first = w.K - w.rt.n;
     } else {
-        w.K = p.prefix_lens[w.rt.seq];
-        w.table = a.block_table + w.rt.row0 * a.table_stride;
-        if (w.K < 0 || w.K > cap || w.K % a.block_size) w.K = 0;           // flagged by the decode plan
-        w.first = w.K;
+        K = p.prefix_lens[seq];
+        if (K < 0 || K > cap || K % a.block_size) K = 0;                   // flagged by the decode plan
     }
-    const int left = w.rt.n - w.rt.t0;                                     // tokens from the first one on
+    it.first = (int32_t)(MODE == kPacked ? 0 : MODE == kPaged ? K - it.n : K);
+    const int left = it.n - it.t0;                                         // tokens from the first one on
     if (MODE == kPrefix) {
-        const int64_t per = ((w.K + kTile - 1) / kTile + p.n_split - 1) / p.n_split * kTile;
-        w.k_lo = min(w.K, w.split * per);
-        w.k_hi = w.all_see = min(w.K, w.k_lo + per);
-        w.n_keys[0] = w.n_keys[1] = (int)((w.k_hi - w.k_lo + kTile - 1) / kTile);
+        const int64_t per = ((K + kTile - 1) / kTile + p.n_split - 1) / p.n_split * kTile;
+        it.k_lo = (int32_t)min(K, it.split * per);
+        it.k_hi = it.all_see = (int32_t)min(K, it.k_lo + per);
+        it.n_keys[0] = it.n_keys[1] = (it.k_hi - it.k_lo + kTile - 1) / kTile;
     } else {
-        w.k_lo = 0;
-        auto seen = [&](int tokens) { return max((int64_t)0, min(w.K, w.first + w.rt.t0 + tokens)); };
-        w.all_see = seen(1);
-        const int64_t k0 = seen(min(left, w.tokens));
-        w.k_hi = seen(min(left, 2 * w.tokens));
-        w.n_keys[0] = (int)((k0 + kTile - 1) / kTile);
-        w.n_keys[1] = (int)((w.k_hi + kTile - 1) / kTile);
+        it.k_lo = 0;
+        auto seen = [&](int tokens) { return (int32_t)max((int64_t)0, min(K, (int64_t)it.first + it.t0 + tokens)); };
+        it.all_see = seen(1);
+        it.k_hi = seen(min(left, 2 * tokens));
+        it.n_keys[0] = (seen(min(left, tokens)) + kTile - 1) / kTile;
+        it.n_keys[1] = (it.k_hi + kTile - 1) / kTile;
     }
-    if (left <= w.tokens) w.n_keys[1] = 0;
+    if (left <= tokens) it.n_keys[1] = 0;
     return true;
 }
 
@@ -263,163 +334,185 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     const uint32_t s_base = smem_u32(sm);
     const kda_attn_prefill_args& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = a.n_heads / a.n_kv_heads;
-    Work w;
-    if (!find_work<MODE>(p, w)) return;
+    const int G = a.n_heads / a.n_kv_heads, tokens = kTile / G;
 
     if (warp == kMmaWarp) tmem_alloc(&ms.tslot, kTmemCols);
     if (tid == 0) {
         for (int i = 0; i < Sh::kStages; ++i) {
             mbar_init(&ms.full[i], 1);
-            mbar_init(&ms.empty[i], 1 + kGuardWarps);
-            mbar_init(&ms.guarded[i], 32 * kGuardWarps);
+            mbar_init(&ms.empty[i], 2);               // the MMAs and the guard
+            mbar_init(&ms.guarded[i], 1);
         }
-        mbar_init(&ms.q_full, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&ms.item_full[i], 1);
+            mbar_init(&ms.item_empty[i], kItemReaders);
             mbar_init(&ms.s_full[i], 1);
-            mbar_init(&ms.p_ready[i][0], 4);
-            mbar_init(&ms.p_ready[i][1], 4);
-            mbar_init(&ms.half_done[i], 1);
+            mbar_init(&ms.p_ready[i], 128);
             mbar_init(&ms.o_done[i], 1);
+            mbar_init(&ms.o_free[i], 4);
         }
-        ms.failed = 0;
-        ms.poison = 0;
+        mbar_init(&ms.next, 1);
+        mbar_init(&ms.q_full, 1);
+        mbar_init(&ms.q_free, 1);
+        mbar_init(&ms.drained, 1);
+        ms.poison = -1;
         fence_mbar_init();
     }
-    for (int i = tid; i < D; i += kThreads) ms.first_nan[i] = ms.first_pos[i] = ms.first_neg[i] = INT_MAX;
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     constexpr uint32_t tbase = 0;                 // all of tensor memory is this block's
     auto tS = [](int q) { return tbase + 128u * q; };
     auto tO = [](int q) { return tbase + 256u + 128u * q; };
-    auto waitb = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (mbar_wait(bar, parity)) return true;
-        atomicExch(&ms.failed, 1);
-        flag(p.status, KDA_DEV_WAIT_TIMEOUT);
-        return false;
+    // A bounded wait of a whole warp, whose lanes then agree.  Once one runs out, the
+    // roles that depend on it run out of theirs.  Between a tile's steps, where the
+    // vote's time counts, lanes wait with `pass`, each for itself: one that ran out goes
+    // on without waiting, to the vote at the item's end.
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+        if (!ok) flag(p.status, KDA_DEV_WAIT_TIMEOUT);
+        return ok;
     };
-    // the same for a whole warp, whose lanes then agree
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, waitb(bar, parity)); };
-    const int n_tiles = max(w.n_keys[0], w.n_keys[1]);
-    // ring stage of the i-th load (K of tile j: 2 j, V of tile j: 2 j + 1) and the parity of its phase
-    auto stage_of = [&](int i) { return i % Sh::kStages; };
-    auto phase_of = [&](int i) { return (uint32_t)(i / Sh::kStages) & 1u; };
+    auto pass = [&](bool& ok, uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity)) {
+            flag(p.status, KDA_DEV_WAIT_TIMEOUT);
+            ok = false;
+        }
+    };
+    // The i-th item of this block, copied out of its slot; false at the end.
+    auto get_item = [&](uint32_t i, Item& it) -> bool {
+        if (!wait_all(&ms.item_full[i & 1], i >> 1 & 1)) return false;
+        it = ms.item[i & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.item_empty[i & 1]);
+        return it.live != 0;
+    };
     // from this tile on some row sees only a part of the keys
-    const int first_edge = (int)(max((int64_t)0, w.all_see - w.k_lo) / kTile);
+    auto edge_of = [](const Item& it) { return max(0, it.all_see - it.k_lo) / kTile; };
 
     // the register split is made inside the branches: after a merge of the two the
     // compiler would hold everything to the smaller share
     if (warp >= kMmaWarp) {
         fewer_registers<kOtherRegs>();
         if (warp == kMmaWarp) {
-            if (n_tiles > 0) {
-                const uint32_t leader = elect_one();
-                const uint32_t id_s = idesc_bf16(kTile, kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
-                const uint32_t id_o = idesc_bf16(kTile, D, false, true);
-                const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
-                auto at = [](uint64_t desc, uint32_t byte) { return desc + (uint64_t)(byte >> 4); };
-                auto scores = [&](int q, int stage) {
-                    const uint32_t qb = s_base + Sh::kQ + q * Sh::kTileBytes, kb = s_base + Sh::kRing + stage * Sh::kTileBytes;
-    #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
-                        mma_ss(leader, tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
-                    }
-                    commit(leader, &ms.s_full[q]);
-                };
-                auto values = [&](int q, int half, int stage, bool first) {
-                    const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
-    #pragma unroll
-                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                        mma_ts(leader, tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
-                };
-                bool ok = wait_all(&ms.q_full, 0) && wait_all(&ms.full[0], 0);
-                if (ok) {
-                    fence_after_sync();
-                    for (int q = 0; q < 2; ++q)
-                        if (w.n_keys[q] > 0) scores(q, 0);
-                    commit(leader, &ms.empty[0]);
+            // -------------------------------------------------------------- MMAs
+            const uint32_t leader = elect_one();
+            const uint32_t id_s = idesc_bf16(kTile, kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
+            const uint32_t id_o = idesc_bf16(kTile, D, false, true);
+            const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
+            auto at = [](uint64_t desc, uint32_t byte) { return desc + (uint64_t)(byte >> 4); };
+            auto scores = [&](int q, uint32_t stage) {
+                const uint32_t qb = s_base + Sh::kQ + q * Sh::kTileBytes, kb = s_base + Sh::kRing + stage * Sh::kTileBytes;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
+                    mma_ss(leader, tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
                 }
-                uint32_t guard_phase = 0;                         // a bit for each stage
-                Ring v;
-                v.next(Sh::kStages);
-                // Waits for the copies stand between the MMAs of one row tile, where the
-                // tensor pipe still has work.
-                auto v_ready = [&](int j) -> bool {
-                    if (!wait_all(&ms.full[v.stage], v.phase)) return false;
+                commit(leader, &ms.s_full[q]);
+            };
+            auto values = [&](int q, uint32_t stage, bool first) {
+                const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                    mma_ts(leader, tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
+            };
+            uint32_t guard_phase = 0;                             // a bit for each stage
+            uint32_t p_phase[2] = {0, 0}, o_items[2] = {0, 0};
+            Ring r;
+            bool ok = true;
+            Item it;
+            for (uint32_t i = 0; __all_sync(0xffffffffu, ok) && get_item(i, it); ++i) {
+                const int n_tiles = max(it.n_keys[0], it.n_keys[1]), first_edge = edge_of(it);
+                pass(ok, &ms.q_full, i & 1);
+                if (n_tiles == 0) {
+                    commit(leader, &ms.q_free);
+                    continue;
+                }
+                pass(ok, &ms.full[r.stage], r.phase);
+                fence_after_sync();
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (it.n_keys[q] > 0) scores(q, r.stage);
+                commit(leader, &ms.empty[r.stage]);
+                if (n_tiles == 1) commit(leader, &ms.q_free);
+                r.next(Sh::kStages);
+                auto v_ready = [&](int j) {
+                    pass(ok, &ms.full[r.stage], r.phase);
                     if (j >= first_edge) {
-                        if (!wait_all(&ms.guarded[v.stage], guard_phase >> v.stage & 1)) return false;
-                        guard_phase ^= 1u << v.stage;
+                        pass(ok, &ms.guarded[r.stage], guard_phase >> r.stage & 1);
+                        guard_phase ^= 1u << r.stage;
                     }
-                    return true;
                 };
-                ok = ok && v_ready(0);
-                for (int j = 0; j < n_tiles && ok; ++j) {
-                    const uint32_t vs = v.stage;
-                    v.next(Sh::kStages);
-                    const Ring k = v;
-                    v.next(Sh::kStages);
+                v_ready(0);
+                for (int j = 0;; ++j) {
+                    const uint32_t vs = r.stage;
+                    r.next(Sh::kStages);
                     const bool more = j + 1 < n_tiles;
-                    if (more && !(ok = wait_all(&ms.full[k.stage], k.phase))) break;
+                    if (more) pass(ok, &ms.full[r.stage], r.phase);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        if (j < w.n_keys[q]) {
-                            if (!(ok = wait_all(&ms.p_ready[q][0], j & 1))) break;
+                        if (j < it.n_keys[q]) {
+                            if (j == 0) pass(ok, &ms.o_free[q], (o_items[q]++ & 1) ^ 1);
+                            pass(ok, &ms.p_ready[q], p_phase[q]);
+                            if (!ok) break;
+                            p_phase[q] ^= 1;
                             fence_after_sync();
-                            values(q, 0, vs, j == 0);
-                            commit(leader, &ms.half_done[q]);
-                            if (!(ok = wait_all(&ms.p_ready[q][1], j & 1))) break;
-                            fence_after_sync();
-                            values(q, 1, vs, false);
-                            if (j + 1 == w.n_keys[q]) commit(leader, &ms.o_done[q]);
+                            values(q, vs, j == 0);
+                            if (j + 1 == it.n_keys[q]) commit(leader, &ms.o_done[q]);
                         }
                         if (q == 1) commit(leader, &ms.empty[vs]);
-                        if (j + 1 < w.n_keys[q]) scores(q, k.stage);
+                        if (j + 1 < it.n_keys[q]) scores(q, r.stage);
                     }
-                    if (ok && more) commit(leader, &ms.empty[k.stage]);
-                    if (ok && more && !(ok = v_ready(j + 1))) break;
-                }
-                if (!ok) {
-                    // let the MMAs in flight finish before shared and tensor memory go
-                    commit(leader, &ms.q_full);
-                    mbar_wait(&ms.q_full, 1);
+                    if (!more || !ok) break;
+                    commit(leader, &ms.empty[r.stage]);
+                    if (j + 2 == n_tiles) commit(leader, &ms.q_free);   // after the item's last scores
+                    r.next(Sh::kStages);
+                    v_ready(j + 1);
                 }
             }
+            // the MMAs in flight finish before shared and tensor memory go
+            commit(leader, &ms.drained);
+            mbar_wait(&ms.drained, 0);
         } else if (warp == kLoadWarp) {
-            if (n_tiles > 0) {
+            // -------------------------------------------------------------- copies
+            const int box = MODE == kPacked ? kTile : min(a.block_size, kTile);           // rows of one copy
+            const int boxes = kTile / box;
+            const int mine = lane / kRegions, region = lane % kRegions;                   // this lane's copy
+            uint32_t q_loads = 0, issued = 0;
+            Ring ring;
+            bool ok = true;
+            Item it;
+            for (uint32_t i = 0; ok && get_item(i, it); ++i) {
+                const int n_tiles = max(it.n_keys[0], it.n_keys[1]);
+                if (i > 0 && !(ok = wait_all(&ms.q_free, (i - 1) & 1))) break;
                 if (lane == 0) {
-                    const int tiles = w.n_keys[1] > 0 ? 2 : 1;
-                    mbar_expect_tx(&ms.q_full, (uint32_t)tiles * kRegions * (uint32_t)(w.tokens * G) * 128u);
+                    const int tiles = it.n_keys[1] > 0 ? 2 : 1;
+                    mbar_expect_tx(&ms.q_full, (uint32_t)tiles * kRegions * (uint32_t)(tokens * G) * 128u);
                     for (int q = 0; q < tiles; ++q)
                         for (int c = 0; c < kRegions; ++c)
-                            tma_load_3d(sm + Sh::kQ + q * Sh::kTileBytes + c * Sh::kRegion, &maps.q, 64 * c, w.hk * G,
-                                        (int32_t)(w.rt.row0 + w.rt.t0 + q * w.tokens), &ms.q_full);
+                            tma_load_3d(sm + Sh::kQ + q * Sh::kTileBytes + c * Sh::kRegion, &maps.q, 64 * c, it.hk * G,
+                                        (int32_t)(it.row0 + it.t0 + q * tokens), &ms.q_full);
                 }
-                const int box = MODE == kPacked ? kTile : min(a.block_size, kTile);       // rows of one copy
-                const int boxes = kTile / box;
-                const int mine = lane / kRegions, region = lane % kRegions;               // this lane's copy
-                int issued = 0;
-                bool ok = true;
-                Ring ring;
+                q_loads = i + 1;
+                const int32_t* table = MODE == kPacked ? nullptr : a.block_table + (int64_t)it.table_row * a.table_stride;
                 for (int j = 0; j < n_tiles && ok; ++j) {
-                    const int64_t k0 = w.k_lo + (int64_t)j * kTile;
+                    const int32_t k0 = it.k_lo + j * kTile;
                     // copies that begin beyond the last key that a row sees are left out
-                    const int live = MODE == kPacked ? 1 : (int)min((int64_t)boxes, (w.k_hi - k0 + box - 1) / box);
+                    const int live = MODE == kPacked ? 1 : min(boxes, (it.k_hi - k0 + box - 1) / box);
                     int32_t row = 0;
                     if (MODE != kPacked && mine < live) {
-                        const int64_t key = k0 + mine * box;
-                        const int32_t block = w.table[key / a.block_size];
+                        const int32_t key = k0 + mine * box;
+                        const int32_t block = table[key / a.block_size];
                         if (block < 0 || block >= a.n_blocks) {
                             flag(p.status, KDA_DEV_BAD_SLOT);
                             row = (int32_t)(a.n_blocks * a.n_kv_heads * a.block_size);     // past the end: reads zeros
                         } else {
-                            row = (int32_t)((block * (int64_t)a.n_kv_heads + w.hk) * a.block_size + key % a.block_size);
+                            row = (int32_t)((block * (int64_t)a.n_kv_heads + it.hk) * a.block_size + key % a.block_size);
                         }
                     }
-                    for (int kv = 0; kv < 2 && ok; ++kv) {
-                        const int i = 2 * j + kv, st = (int)ring.stage;
-                        if (i >= Sh::kStages && !(ok = wait_all(&ms.empty[st], ring.phase ^ 1u))) break;
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t st = ring.stage;
+                        if (!(ok = wait_all(&ms.empty[st], ring.phase ^ 1u))) break;
                         ring.next(Sh::kStages);
                         uint8_t* dst = sm + Sh::kRing + st * Sh::kTileBytes;
                         const void* map = kv ? &maps.v : &maps.k;
@@ -427,138 +520,200 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         __syncwarp();
                         if (mine < live) {
                             uint8_t* to = dst + region * Sh::kRegion + mine * box * 128;
-                            if (MODE == kPacked) tma_load_3d(to, map, 64 * region, w.hk, (int32_t)(w.rt.row0 + k0), &ms.full[st]);
+                            if (MODE == kPacked) tma_load_3d(to, map, 64 * region, it.hk, (int32_t)(it.row0 + k0), &ms.full[st]);
                             else tma_load_2d(to, map, 64 * region, row, &ms.full[st]);
                         }
-                        issued = i + 1;
+                        ++issued;
                     }
-                }
-                if (!ok) {
-                    // copies in flight land before the block's shared memory goes
-                    mbar_wait(&ms.q_full, 0);
-                    for (int i = max(0, issued - Sh::kStages); i < issued; ++i) mbar_wait(&ms.full[stage_of(i)], phase_of(i));
                 }
             }
-        } else {
-            const int gt = tid - 32 * kGuardWarp;
-            // These warps follow every load and release its stage with the MMAs, so that
-            // no barrier gets two phases ahead of their waits.
+            // copies in flight land before the block's shared memory goes: the last of
+            // Q, and the last of every stage
+            if (q_loads > 0) mbar_wait(&ms.q_full, (q_loads - 1) & 1);
+            for (uint32_t i = issued < Sh::kStages ? 0 : issued - Sh::kStages; i < issued; ++i)
+                mbar_wait(&ms.full[i % Sh::kStages], i / Sh::kStages & 1);
+        } else if (warp == kGuardWarp) {
+            // -------------------------------------------------------------- hidden values
+            // This warp follows every load and releases its stage with the MMAs, so that
+            // no barrier gets two phases ahead of its waits.
             Ring ring;
-            for (int i = 0; i < 2 * n_tiles; ++i) {
-                const int j = i >> 1;
-                const uint32_t st = ring.stage;
-                if (!wait_all(&ms.full[st], ring.phase)) break;
-                ring.next(Sh::kStages);
-                if (!(i & 1) || j < first_edge) {
-                    if (lane == 0) mbar_arrive(&ms.empty[st]);
-                    continue;
-                }
-                const int64_t k0 = w.k_lo + (int64_t)j * kTile;
-                uint8_t* v = sm + Sh::kRing + st * Sh::kTileBytes;
-                const int from = (int)max((int64_t)0, min((int64_t)kTile, w.all_see - k0));   // rows that not every row sees
-                const int none = (int)max((int64_t)0, min((int64_t)kTile, w.k_hi - k0));      // rows that no row sees
-                for (int x = gt; x < (kTile - from) * kRegions * 8; x += 32 * kGuardWarps) {
-                    const int r = from + x / (kRegions * 8), y = x % (kRegions * 8), region = y >> 3, c = y & 7;
-                    uint4* at = reinterpret_cast<uint4*>(v + region * Sh::kRegion + row64_chunk_off(r, c));
-                    if (r >= none) {
-                        *at = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint4 u = *at;
-                    uint32_t* e = &u.x;
-                    uint32_t hit = 0;
-    #pragma unroll
-                    for (int k = 0; k < 4; ++k) hit |= ((e[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // exponent all ones
-                    if (hit) {
-                        ms.poison = 1;
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t b = e[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
-                            if ((b & 0x7F80u) != 0x7F80u) continue;
-                            int32_t* first = b & 0x7Fu ? ms.first_nan : b & 0x8000u ? ms.first_neg : ms.first_pos;
-                            atomicMin(&first[region * 64 + c * 8 + k], (int32_t)(k0 + r));
-                            e[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+            bool ok = true;
+            uint32_t o_items[2] = {0, 0};                         // items before this one that each row tile takes part in
+            Item it;
+            for (uint32_t i = 0; ok && get_item(i, it); ++i) {
+                const int n_tiles = max(it.n_keys[0], it.n_keys[1]), first_edge = edge_of(it);
+                bool noted = false;
+                for (int x = 0; x < 2 * n_tiles; ++x) {
+                    const int j = x >> 1;
+                    const uint32_t st = ring.stage;
+                    if (!(ok = wait_all(&ms.full[st], ring.phase))) break;
+                    ring.next(Sh::kStages);
+                    if ((x & 1) && j >= first_edge) {
+                        const int32_t k0 = it.k_lo + j * kTile;
+                        uint8_t* v = sm + Sh::kRing + st * Sh::kTileBytes;
+                        const int from = max(0, min(kTile, it.all_see - k0));             // keys that not every row sees
+                        const int none = max(0, min(kTile, it.k_hi - k0));                // keys that no row sees
+                        const int pieces = (kTile - from) * kRegions * 8;                 // of 16 bytes
+                        auto key_of = [&](int y) { return from + y / (kRegions * 8); };
+                        auto piece = [&](int y) {
+                            const int z = y % (kRegions * 8);
+                            return reinterpret_cast<uint4*>(v + (z >> 3) * Sh::kRegion + row64_chunk_off(key_of(y), z & 7));
+                        };
+                        bool hit = false;
+#pragma unroll 4
+                        for (int y = lane; y < pieces; y += 32) {
+                            uint4* at = piece(y);
+                            if (key_of(y) >= none) {
+                                *at = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            const uint4 u = *at;
+                            auto odd = [](uint32_t e) { return ((e & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+                            hit |= (odd(u.x) | odd(u.y) | odd(u.z) | odd(u.w)) != 0;      // an exponent of all ones
                         }
-                        *at = u;
+                        if (__any_sync(0xffffffffu, hit)) {
+                            if (!noted) {
+                                // the notes may still be read for the item before
+                                for (int q = 0; q < 2 && ok; ++q)
+                                    if (o_items[q] > 0) ok = wait_all(&ms.o_free[q], (o_items[q] - 1) & 1);
+                                if (!ok) break;
+                                for (int d = lane; d < D; d += 32) ms.first_nan[d] = ms.first_pos[d] = ms.first_neg[d] = INT_MAX;
+                                if (lane == 0) ms.poison = (int32_t)i;
+                                noted = true;
+                                __syncwarp();
+                            }
+                            for (int y = lane; y < pieces && key_of(y) < none; y += 32) {
+                                uint16_t* e = reinterpret_cast<uint16_t*>(piece(y));
+                                for (int k = 0; k < 8; ++k) {
+                                    const uint32_t b = e[k];
+                                    if ((b & 0x7F80u) != 0x7F80u) continue;
+                                    int32_t* first = b & 0x7Fu ? ms.first_nan : b & 0x8000u ? ms.first_neg : ms.first_pos;
+                                    atomicMin(&first[y % (kRegions * 8) * 8 + k], k0 + key_of(y));
+                                    e[k] = 0;
+                                }
+                            }
+                        }
+                        __threadfence_block();
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.guarded[st]);
                     }
+                    if (lane == 0) mbar_arrive(&ms.empty[st]);
                 }
-                __threadfence_block();
-                fence_async_smem();
-                mbar_arrive(&ms.guarded[st]);
+                for (int q = 0; q < 2; ++q) o_items[q] += it.n_keys[q] > 0;
+            }
+        } else {
+            // -------------------------------------------------------------- items
+            Place place;
+            int64_t block = blockIdx.x;
+            uint32_t i = 0;
+            bool ok = true;
+            for (uint32_t asked = 0; block >= 0; ++asked) {
+                if (lane == 0) {
+                    mbar_expect_tx(&ms.next, 16);
+                    ask_next_block(&ms.next_block, &ms.next);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.empty[st]);
+                Item it;
+                if (ok && find_item<MODE>(p, block, place, it) && (ok = wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1))) {
+                    it.live = 1;
+                    if (lane == 0) {
+                        ms.item[i & 1] = it;
+                        mbar_arrive(&ms.item_full[i & 1]);
+                    }
+                    ++i;
+                }
+                // the answer lands before the block's shared memory goes, so this wait comes in any case
+                block = wait_all(&ms.next, asked & 1) && ok ? next_block(&ms.next_block) : -1;
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (ok && wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1) && lane == 0) {
+                ms.item[i & 1].live = 0;
+                mbar_arrive(&ms.item_full[i & 1]);
             }
         }
     } else {
         // ------------------------------------------------------------------ softmax
         more_registers<kSoftmaxRegs>();
+        if (MODE != kPrefix && blockIdx.x == 0)
+            for (int32_t s = tid; s < a.n_seqs; s += 32 * kMmaWarp) {
+                const int64_t lo = a.cu_seqlens[s], hi = a.cu_seqlens[s + 1];
+                if (lo < 0 || hi < lo || hi > a.total_tokens) flag(p.status, KDA_DEV_BAD_SEQLENS);
+            }
         const int q = warp >> 2;
         const int r = 32 * (warp & 3) + lane;                     // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const int t = w.rt.t0 + q * w.tokens + r / G, g = r % G;
-        const bool live = r < w.tokens * G && t < w.rt.n;
-        // keys that this row sees, and keys that all rows of the tile see, from k_lo on
-        const int64_t seen = MODE == kPrefix ? w.k_hi : min(w.k_hi, w.first + t + 1);
-        const int row_sees = (int)max((int64_t)0, seen - w.k_lo);
-        const int tile_sees =
-            (int)max((int64_t)0, (MODE == kPrefix ? w.k_hi : min(w.k_hi, w.first + w.rt.t0 + q * w.tokens + 1)) - w.k_lo);
         // a scale of 0 becomes the least normal number, so that a hidden score of -inf stays one
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
-        const int n = w.n_keys[q];
-        float m = -CUDART_INF_F;
-        uint64_t l2 = pair2(0.f);
+        uint32_t phase = 0, o_phase = 0;                          // of the tiles, of the items with tiles
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            if (!(ok = wait_all(&ms.s_full[q], j & 1))) break;
-            fence_after_sync();
-            uint32_t s[kTile];
+        Item it;
+        for (uint32_t i = 0; __all_sync(0xffffffffu, ok) && get_item(i, it); ++i) {
+            const int t = it.t0 + q * tokens + r / G, g = r % G;
+            const bool live = r < tokens * G && t < it.n;
+            // keys that this row sees, and keys that all rows of the warp see for sure.  Rows
+            // past the end see none: what their scores hold is never looked at.
+            const int seen = !live ? 0 : MODE == kPrefix ? it.k_hi : min(it.k_hi, it.first + t + 1);
+            const int row_sees = max(0, seen - it.k_lo);
+            int tile_sees = max(0, (MODE == kPrefix ? it.k_hi : min(it.k_hi, it.first + it.t0 + q * tokens + 1)) - it.k_lo);
+            if (__any_sync(0xffffffffu, !live)) tile_sees = 0;
+            const int n = it.n_keys[q];
+            float m = kLeastMaximum;
+            uint64_t l2 = pair2(0.f);
+            for (int j = 0; j < n; ++j) {
+                pass(ok, &ms.s_full[q], phase);
+                __syncwarp();
+                phase ^= 1;
+                fence_after_sync();
+                uint32_t s[kTile];
 #pragma unroll
-            for (int x = 0; x < kTile; x += 32) tmem_ld32(tS(q) + lanes + x, s + x);
-            tmem_wait_ld();
-            if ((j + 1) * kTile > tile_sees) {
-                const int visible = row_sees - j * kTile;
+                for (int x = 0; x < kTile; x += 32) tmem_ld32(tS(q) + lanes + x, s + x);
+                tmem_wait_ld();
+                if ((j + 1) * kTile > tile_sees) {
+                    const int visible = row_sees - j * kTile;
 #pragma unroll
-                for (int x = 0; x < kTile; ++x) s[x] = x < visible ? s[x] : 0xFF800000u;
-            }
-            auto maximum = [&]() {                                 // of the tile's scores, and m
-                float top[4] = {m, m, m, m};
-#pragma unroll
-                for (int x = 0; x < kTile; x += 8)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        top[y] = fmaxf(fmaxf(top[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
-                return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            };
-            // the weights of one half of the keys, for the maximum as it stands, to P; returns their sum
-            auto weights = [&](int h) -> uint64_t {
-                const uint64_t off2 = pair2(m == -CUDART_INF_F ? 0.f : -m * c), c2 = pair2(c);
-                uint64_t sums[2] = {pair2(0.f), pair2(0.f)};
-                uint32_t w2[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const float2 y = unpair2(fma2(pair2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, off2));
-                    const float p0 = ex2(y.x), p1 = ex2(y.y);
-                    sums[x & 1] = add2(sums[x & 1], pair2(__float_as_uint(p0), __float_as_uint(p1)));
-                    w2[x] = pack_bf16(p0, p1);
+                    for (int x = 0; x < kTile; ++x) s[x] = x < visible ? s[x] : 0xFF800000u;
                 }
-                tmem_st32(tS(q) + lanes + 32 * h, w2);
-                return add2(sums[0], sums[1]);
-            };
-            if (j == 0) m = maximum();
+                auto maximum = [&]() {                             // of the tile's scores, and m
+                    float top[4] = {m, m, m, m};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint64_t sum = weights(h);
+                    for (int x = 0; x < kTile; x += 8)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            top[y] = fmaxf(fmaxf(top[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
+                    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                };
+                // the weights for the maximum as it stands, to P; returns their sum
+                auto weights = [&]() -> uint64_t {
+                    const uint64_t off2 = pair2(-m * c), c2 = pair2(c);
+                    uint64_t sums[2] = {pair2(0.f), pair2(0.f)};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w2[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            const float2 y = unpair2(fma2(pair2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, off2));
+                            const float p0 = ex2(y.x), p1 = ex2(y.y);
+                            sums[x & 1] = add2(sums[x & 1], pair2(__float_as_uint(p0), __float_as_uint(p1)));
+                            w2[x] = pack_bf16(p0, p1);
+                        }
+                        tmem_st32(tS(q) + lanes + 32 * h, w2);
+                    }
+                    return add2(sums[0], sums[1]);
+                };
+                if (j == 0) m = maximum();
+                uint64_t sum = weights();
                 const float2 both = unpair2(sum);
                 const bool grow = !(both.x + both.y <= kMostWeight);
                 if (__any_sync(0xffffffffu, grow)) {
                     // rare: move the maximum, rescale what was summed so far, weigh again
-                    if (h == 1) ok = ok && wait_all(&ms.half_done[q], j & 1);
-                    fence_after_sync();
                     const float mx = grow ? maximum() : m;         // a row's result depends on no other row
                     const float f = mx > m ? ex2((m - mx) * c) : 1.f;
                     m = mx;
                     const float2 lf = unpair2(l2);
                     l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
-                    if (j > 0 || h == 1) {
+                    if (j > 0) {
 #pragma unroll 1
                         for (int x = 0; x < D; x += 16) {
                             uint32_t o[16];
@@ -570,69 +725,74 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         }
                     }
                     tmem_wait_st();
-                    sum = weights(h);
+                    sum = weights();
                 }
+                l2 = add2(l2, sum);
                 tmem_wait_st();
                 fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_ready[q][h]);
-                l2 = add2(l2, sum);
+                mbar_arrive(&ms.p_ready[q]);
             }
-        }
-        const float l = unpair2(l2).x + unpair2(l2).y;
-        if (ok && n > 0) ok = wait_all(&ms.o_done[q], 0);
-        fence_after_sync();
-        if (ok) {
-            const int64_t row = w.rt.row0 + t;
-            const int head = w.hk * G + g;
-            const int64_t at = ((int64_t)w.split * a.total_tokens + row) * a.n_heads + head;
+            const float l = unpair2(l2).x + unpair2(l2).y;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool poison = MODE != kPrefix && *(volatile int32_t*)&ms.poison;
-#pragma unroll
-            for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(tO(q) + lanes + x, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] = 0u;
-                }
+            const int64_t row = it.row0 + t;
+            const int head = it.hk * G + g;
+            const int64_t at = ((int64_t)it.split * a.total_tokens + row) * a.n_heads + head;
+            uint32_t o[D];
+            if (n > 0) {
+                pass(ok, &ms.o_done[q], o_phase);
                 __syncwarp();
-                if (!live) {
-                } else if (MODE == kPrefix) {
-                    float4* out = reinterpret_cast<float4*>(p.part_o + at * D + x);
+                o_phase ^= 1;
+                fence_after_sync();
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4)
-                        out[y / 4] = make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
-                                                 __uint_as_float(o[y + 3]));
-                } else {
-                    if (poison) {
+                for (int x = 0; x < D; x += 32) tmem_ld32(tO(q) + lanes + x, o + x);
+                tmem_wait_ld();
+                if (MODE != kPrefix && *(volatile int32_t*)&ms.poison == (int32_t)i) {
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const bool pos = seen > ms.first_pos[x + y], neg = seen > ms.first_neg[x + y];
-                            float add = pos ? CUDART_INF_F : neg ? -CUDART_INF_F : 0.f;
-                            if (seen > ms.first_nan[x + y] || (pos && neg)) add = CUDART_NAN_F;
-                            o[y] = __float_as_uint(__uint_as_float(o[y]) + add);
-                        }
-                    }
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_stride + (int64_t)head * D + x);
-#pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
-                        uint32_t b[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            b[k] = pack_bf16(__uint_as_float(o[y + 2 * k]) * inv, __uint_as_float(o[y + 2 * k + 1]) * inv);
-                        out[y / 8] = make_uint4(b[0], b[1], b[2], b[3]);
+                    for (int x = 0; x < D; ++x) {
+                        const bool pos = seen > ms.first_pos[x], neg = seen > ms.first_neg[x];
+                        float add = pos ? CUDART_INF_F : neg ? -CUDART_INF_F : 0.f;
+                        if (seen > ms.first_nan[x] || (pos && neg)) add = CUDART_NAN_F;
+                        o[x] = __float_as_uint(__uint_as_float(o[x]) + add);
                     }
                 }
+                fence_before_sync();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.o_free[q]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < D; ++x) o[x] = 0u;
             }
             if (live) {
-                const float m2 = m == -CUDART_INF_F ? m : m * c;
-                if (MODE == kPrefix) p.part_ml[at] = make_float2(m2, l);
-                else if (a.lse) a.lse[row * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m2, kLn2, logf(l));
+                const float m2 = l == 0.f ? -CUDART_INF_F : m * c;
+                if (MODE == kPrefix) {
+                    float4* out = reinterpret_cast<float4*>(p.part_o + at * D);
+#pragma unroll
+                    for (int x = 0; x < D; x += 4)
+                        out[x / 4] = make_float4(__uint_as_float(o[x]), __uint_as_float(o[x + 1]), __uint_as_float(o[x + 2]),
+                                                 __uint_as_float(o[x + 3]));
+                    p.part_ml[at] = make_float2(m2, l);
+                } else {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + row * a.o_stride + (int64_t)head * D;
+                    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;      // whole 32-byte sectors
+#pragma unroll
+                    for (int x = 0; x < D; x += 16) {
+                        uint32_t b[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            b[k] = pack_bf16(__uint_as_float(o[x + 2 * k]) * inv, __uint_as_float(o[x + 2 * k + 1]) * inv);
+                        if (wide) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + x), "r"(b[0]),
+                                         "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7])
+                                         : "memory");
+                        } else {
+                            reinterpret_cast<uint4*>(out + x)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                            reinterpret_cast<uint4*>(out + x)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+                        }
+                    }
+                    if (a.lse) a.lse[row * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m2, kLn2, logf(l));
+                }
             }
+            __syncwarp();
         }
         fence_before_sync();
     }

@@ -85,7 +85,7 @@ struct Item {
 template <int D> struct Misc {
     uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages];
     uint64_t guarded[Shape<D>::kStages];
-    uint64_t item_full[2], item_empty[2], next, q_full, q_free, drained;
+    uint64_t item_full[2], item_empty[2], want, next, q_full, q_free, drained;
     uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
     alignas(16) uint4 next_block;                                 // clusterlaunchcontrol's answer
     Item item[2];
@@ -351,6 +351,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             mbar_init(&ms.o_done[i], 1);
             mbar_init(&ms.o_free[i], 4);
         }
+        mbar_init(&ms.want, 1);
         mbar_init(&ms.next, 1);
         mbar_init(&ms.q_full, 1);
         mbar_init(&ms.q_free, 1);
@@ -526,6 +527,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         ++issued;
                     }
                 }
+                if (lane == 0) mbar_arrive(&ms.want);             // time to claim another item
             }
             // copies in flight land before the block's shared memory goes: the last of
             // Q, and the last of every stage
@@ -604,29 +606,34 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             }
         } else {
             // -------------------------------------------------------------- items
+            // The next item is claimed when the last one's copies are under way, not before:
+            // what a block claims early, a block that gets free first cannot have.
             Place place;
             int64_t block = blockIdx.x;
             uint32_t i = 0;
             bool ok = true;
-            for (uint32_t asked = 0; block >= 0; ++asked) {
-                if (lane == 0) {
-                    mbar_expect_tx(&ms.next, 16);
-                    ask_next_block(&ms.next_block, &ms.next);
-                }
-                __syncwarp();
+            for (uint32_t asked = 0;; ++asked) {
                 Item it;
-                if (ok && find_item<MODE>(p, block, place, it) && (ok = wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1))) {
+                if (find_item<MODE>(p, block, place, it)) {
+                    if (!(ok = wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1))) break;
                     it.live = 1;
                     if (lane == 0) {
                         ms.item[i & 1] = it;
                         mbar_arrive(&ms.item_full[i & 1]);
                     }
+                    if (!(ok = wait_all(&ms.want, i & 1))) break;
                     ++i;
                 }
-                // the answer lands before the block's shared memory goes, so this wait comes in any case
-                block = wait_all(&ms.next, asked & 1) && ok ? next_block(&ms.next_block) : -1;
+                if (lane == 0) {
+                    mbar_expect_tx(&ms.next, 16);
+                    ask_next_block(&ms.next_block, &ms.next);
+                }
+                __syncwarp();
+                if (!(ok = wait_all(&ms.next, asked & 1))) break;
+                block = next_block(&ms.next_block);
                 fence_async_smem();
                 __syncwarp();
+                if (block < 0) break;
             }
             if (ok && wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1) && lane == 0) {
                 ms.item[i & 1].live = 0;

@@ -91,7 +91,6 @@ kda_status_t check_scale(float scale) {
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-int decode_pieces(int32_t dtype) { return dtype == KDA_BF16 ? kda::kDecodePiecesBf16 : kda::kDecodePiecesF32; }
 int decode_rows(int32_t dtype) { return dtype == KDA_BF16 ? kda::kDecodeRowsBf16 : kda::kDecodeRowsF32; }
 
 // Blocks of keys that a shared prefix is cut into: enough row tiles (256 rows in
@@ -119,12 +118,12 @@ DecodeSpace decode_space(const kda_attn_decode_args& a) {
         return r;
     };
     const size_t rows = (size_t)a.n_seqs * a.n_heads * prefix_splits(a);
-    const size_t parts = (size_t)2 * decode_pieces(a.dtype) * decode_rows(a.dtype);
+    const size_t parts = (size_t)2 * kda::kDecodePieces * decode_rows(a.dtype);
     s.pre_o = take(rows * a.d * sizeof(float));
     s.pre_ml = take(rows * sizeof(float2));
     s.part_o = take(parts * a.d * sizeof(float));
     s.part_ml = take(parts * sizeof(float2));
-    s.open = take((size_t)decode_pieces(a.dtype) * sizeof(int4));
+    s.open = take((size_t)kda::kDecodePieces * sizeof(int4));
     s.info = take(a.n_groups > 0 ? (size_t)a.n_seqs * sizeof(int2) : 0);
     s.bytes = at;
     return s;
@@ -274,7 +273,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     kda::AttnDecodeLaunch p{};
     p.a = a;
-    p.n_pieces = decode_pieces(a.dtype);
+    p.n_pieces = kda::kDecodePieces;
     p.n_split = prefix_splits(a);
     p.pre_o = reinterpret_cast<float*>(ws + sp.pre_o);
     p.pre_ml = reinterpret_cast<float2*>(ws + sp.pre_ml);

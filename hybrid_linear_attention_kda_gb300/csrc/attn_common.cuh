@@ -125,9 +125,8 @@ struct AttnDecodeLaunch {
     int4* open;                   // [n_pieces] the unit that begins in a piece and goes on
     int2* info;                   // [n_seqs] (shared positions, all positions), where there are groups
 };
-constexpr int kDecodeRowsF32 = 8, kDecodeRowsBf16 = 16;   // query heads of one unit
-// Workers: three thread blocks (fp32) or one of eight warps (bf16) on each of 152 SMs.
-constexpr int kDecodeWarpsBf16 = 8, kDecodePiecesF32 = 3 * 152, kDecodePiecesBf16 = kDecodeWarpsBf16 * 152;
+constexpr int kDecodeRowsF32 = 8, kDecodeRowsBf16 = 16;   // at most: query heads of one unit
+constexpr int kDecodeWarps = 8, kDecodePieces = kDecodeWarps * 152;   // workers: eight warps on each of 152 SMs
 cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s);   // p.info, where there are groups
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s);   // fp32
 cudaError_t launch_decode_mma(const AttnDecodeLaunch& p, cudaStream_t s);    // bf16

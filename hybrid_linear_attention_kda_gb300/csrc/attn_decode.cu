@@ -1,7 +1,8 @@
 // Decode attention over the paged cache for fp32 tensors, and the sequences' shared
-// positions.  The division of work is described in attn_decode.cuh; this kernel
-// works on a unit of 8 query heads and tiles of 32 keys, double-buffered in shared
-// memory.  Bound by reading the cache once.
+// positions.  The division of work is described in attn_decode.cuh.  As in the bf16
+// kernel a warp is a worker of its own, with a unit of four or eight query heads, a
+// ring of asynchronous copies and no barrier; the products are SIMT: two or four
+// lanes share a key's dot products, then every lane owns columns of the output.
 #include "async_copy.cuh"
 #include "attn_decode.cuh"
 
@@ -50,181 +51,232 @@ __global__ void __launch_bounds__(kInfoThreads) decode_info_kernel(const __grid_
 
 // ------------------------------------------------------------------ suffix, fp32
 
-constexpr int kThreads = 128, kRows = kDecodeRowsF32, kKeys = 32;
+constexpr int kWarps = kDecodeWarps, kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kLeastTiles = 4;           // of a piece
+// The maximum that weights refer to is the first tile's, and is moved when a weight
+// passes kMostWeight; kLeastMaximum until a row has seen a score above -inf.
+constexpr float kMostWeight = 1024.f, kLeastMaximum = -1e30f;
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
-template <int D>
-struct DecodeSmem {
-    static constexpr int kPad = D + 4;
-    float k[2][kKeys * kPad];
-    float v[2][kKeys * kPad];
-    float q[kRows * D];
-    float w[kKeys * kRows];              // scores, then weights, key-major
-    float corr[kRows], m[kRows], l[kRows];
-    float o[kThreads / D > 1 ? kRows * D : 1];
+// A tile holds 4 KB of keys and 4 KB of values.  The 16-byte pieces of key j lie at
+// piece ^ (j * lanes per key) of its row, so that eight lanes of a score (two or four
+// to a key) and the lanes of a value row read distinct banks.
+template <int D, int R> struct DecodeSmem {
+    static constexpr int kKeys = 1024 / D, kLanesPerKey = D / 32;
+    float ring[kWarps][kStages][2][kKeys * D];
+    float q[kWarps][R * D];
+    float w[kWarps][kKeys * R];          // weights, key-major
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) decode_suffix_kernel(const __grid_constant__ AttnDecodeLaunch p) {
-    using S = DecodeSmem<D>;
-    constexpr int kPad = S::kPad;
-    constexpr int kParts = kThreads / D;                 // threads per output column, over the keys
-    constexpr int kRowsPerThread = kRows * kKeys / kThreads;
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// 16 bytes global -> shared, zeros instead when !live.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(__cvta_generic_to_global(src)), "r"(live ? 16 : 0)
+                 : "memory");
+}
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// R query heads of a unit.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid_constant__ AttnDecodeLaunch p) {
+    using S = DecodeSmem<D, R>;
+    constexpr int kKeys = S::kKeys, kLanes = S::kLanesPerKey, kPieces = D / 4, kCols = D / 32;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>(smem_raw);
     griddep_wait();
     const kda_attn_decode_args& a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
-    __shared__ PieceStart at_;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = a.n_heads / a.n_kv_heads, blocks = (G + R - 1) / R;
+    __shared__ PieceStart at_[kWarps];
     int64_t all, pieces;
-    find_pieces<kThreads, 1>(p, a.n_kv_heads * blocks, kKeys, 1, &at_, all, pieces);
+    find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_, all, pieces);
     griddep_launch();
-    const int64_t piece = blockIdx.x;
-    finish_empty<float, D>(p, (int64_t)blockIdx.x * (kThreads / 32) + warp, (int64_t)gridDim.x * (kThreads / 32), lane);
+    const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
+    finish_empty<float, D>(p, piece, p.n_pieces, lane);
     if (piece >= pieces) {
-        if (tid == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
         return;
     }
-    Cursor c = start(p, at_, a.n_kv_heads * blocks, kKeys);
+    Cursor c = start(p, at_[warp], a.n_kv_heads * blocks, kKeys);
+
+    // ------------------------------------------------------------------ copies, kStages - 1 tiles ahead
+    Cursor f = c;
+    int32_t next_block = 0;                              // table entry of the place f
+    auto look_up = [&]() {
+        const int64_t key = f.info.x + f.k * kKeys;
+        next_block = f.left > 0 && key < f.info.y ? a.block_table[(int64_t)f.s * a.table_stride + key / a.block_size] : -2;
+    };
+    auto fetch = [&](int stage) {
+        if (f.left > 0) {
+            const int64_t key = f.info.x + f.k * kKeys;
+            int live = (int)max((int64_t)0, min((int64_t)kKeys, f.info.y - key));         // keys that exist
+            if (live > 0 && (next_block < 0 || next_block >= a.n_blocks)) {
+                flag(p.status, KDA_DEV_BAD_SLOT);
+                live = 0;
+            }
+            const int hk = f.u / blocks;
+            const int64_t row = live > 0 ? ((int64_t)next_block * a.n_kv_heads + hk) * a.block_size + key % a.block_size : 0;
+            const float* ks = static_cast<const float*>(a.k_cache) + row * D;
+            const float* vs = static_cast<const float*>(a.v_cache) + row * D;
+#pragma unroll
+            for (int i = 0; i < kKeys * kPieces / 32; ++i) {
+                const int j = (i * 32 + lane) / kPieces, y = (i * 32 + lane) % kPieces;
+                const int to = (j * kPieces + (y ^ (j * kLanes & 7))) * 4, from = j < live ? j * D + y * 4 : 0;
+                copy16(sm.ring[warp][stage][0] + to, ks + from, j < live);
+                copy16(sm.ring[warp][stage][1] + to, vs + from, j < live);
+            }
+            f.step(p, kKeys);
+            look_up();
+        }
+        cp_async_commit();
+    };
+    look_up();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+    // ------------------------------------------------------------------ units
     const float sl = a.scale * kLog2e;
+    const int my_key = lane / kLanes, my_part = lane % kLanes;
+    float* q = sm.q[warp];
+    float* w = sm.w[warp];
+    int stage = 0;
     while (c.left > 0) {
         const int64_t k_first = c.k, k_last = c.k + c.run();
         const int32_t s = c.s;
         const int hk = c.u / blocks, rb = c.u % blocks;
-        const int head0 = hk * G + rb * kRows, rows = min(kRows, G - rb * kRows);
+        const int head0 = hk * G + rb * R, rows = min(R, G - rb * R);
         const int2 info = c.info;
-        const int32_t* table = a.block_table + (int64_t)s * a.table_stride;
-
-        auto fetch = [&](int64_t tile, int buf) {
-            const int64_t base = info.x + tile * kKeys;
-            for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-                const int j = i / (D / 4), e = i % (D / 4) * 4;
-                float* kd = sm.k[buf] + j * kPad + e;
-                float* vd = sm.v[buf] + j * kPad + e;
-                int32_t block = -1;
-                if (base + j < info.y) {
-                    block = table[(base + j) / a.block_size];
-                    if (block < 0 || block >= a.n_blocks) flag(p.status, KDA_DEV_BAD_SLOT), block = -1;
-                }
-                if (block >= 0) {
-                    const int64_t at = (((int64_t)block * a.n_kv_heads + hk) * a.block_size + (base + j) % a.block_size) * D + e;
-                    cp_async16(kd, static_cast<const float*>(a.k_cache) + at);
-                    cp_async16(vd, static_cast<const float*>(a.v_cache) + at);
-                } else {
-                    *reinterpret_cast<uint4*>(kd) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(vd) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            cp_async_commit();
-        };
-        __syncthreads();                                 // the previous unit is finished
-        fetch(k_first, 0);
-        for (int i = tid; i < kRows * D; i += kThreads)
-            sm.q[i] = i / D < rows ? static_cast<const float*>(a.q)[s * a.q_stride + (int64_t)head0 * D + i] * sl : 0.f;
-        if (tid < kRows) sm.m[tid] = -CUDART_INF_F, sm.l[tid] = 0.f;
-        float o[kRows] = {};
-        const int col = tid % D, part = tid / D;
+        __syncwarp();                                    // the last unit's q is read
+#pragma unroll
+        for (int i = 4 * lane; i < R * D; i += 128) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i / D < rows) x = load4(static_cast<const float*>(a.q) + s * a.q_stride + (int64_t)head0 * D + i);
+            *reinterpret_cast<float4*>(q + i) = make_float4(x.x * sl, x.y * sl, x.z * sl, x.w * sl);
+        }
+        float o[R][kCols], m[R], l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = kLeastMaximum;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) o[r][e] = 0.f;
+        }
         for (int64_t kt = k_first; kt < k_last; ++kt) {
-            const int buf = (int)((kt - k_first) & 1);
-            cp_async_wait_all();
-            __syncthreads();
-            if (kt + 1 < k_last) fetch(kt + 1, buf ^ 1);
-            {   // scores: thread = one key, some rows
-                const int key = tid % kKeys, r0 = tid / kKeys * kRowsPerThread;
-                float acc[kRowsPerThread] = {};
-#pragma unroll 4
-                for (int e = 0; e < D; e += 4) {
-                    const float4 kx = load4(sm.k[buf] + key * kPad + e);
+            copy_wait<kStages - 2>();
+            __syncwarp();                                // the tile and q are there, and the stage before is read
+            fetch(stage == 0 ? kStages - 1 : stage - 1);
+            const float* kb = sm.ring[warp][stage][0];
+            const float* vb = sm.ring[warp][stage][1];
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+            const bool seen = info.x + kt * kKeys + my_key < info.y;
+            float x[R] = {};
 #pragma unroll
-                    for (int r = 0; r < kRowsPerThread; ++r) {
-                        const float4 qv = load4(sm.q + (r0 + r) * D + e);
-                        acc[r] = fmaf(qv.w, kx.w, fmaf(qv.z, kx.z, fmaf(qv.y, kx.y, fmaf(qv.x, kx.x, acc[r]))));
-                    }
-                }
-                const bool seen = info.x + kt * kKeys + key < info.y;
+            for (int i = 0; i < kPieces / kLanes; ++i) {
+                const int y = i * kLanes + my_part;
+                const float4 k = load4(kb + (my_key * kPieces + (y ^ (my_key * kLanes & 7))) * 4);
 #pragma unroll
-                for (int r = 0; r < kRowsPerThread; ++r) sm.w[key * kRows + r0 + r] = seen ? acc[r] : -CUDART_INF_F;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int rr = 0; rr < kRows / 4; ++rr) {     // a warp's rows
-                const int r = warp * (kRows / 4) + rr;
-                float x = sm.w[lane * kRows + r], mx = fmaxf(sm.m[r], x);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float ms = mx == -CUDART_INF_F ? 0.f : mx;
-                float sum = exp2f(x - ms);
-                sm.w[lane * kRows + r] = sum;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (lane == 0) {
-                    const float corr = exp2f(sm.m[r] - ms);
-                    sm.corr[r] = corr;
-                    sm.l[r] = fmaf(sm.l[r], corr, sum);
-                    sm.m[r] = mx;
+                for (int r = 0; r < R; ++r) {
+                    const float4 z = load4(q + r * D + 4 * y);
+                    x[r] = fmaf(z.w, k.w, fmaf(z.z, k.z, fmaf(z.y, k.y, fmaf(z.x, k.x, x[r]))));
                 }
             }
-            __syncthreads();
+            bool grow = false;
+            float weight[R];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) o[r] *= sm.corr[r];
-#pragma unroll 8
-            for (int j = part; j < kKeys; j += kParts) {
-                const float vx = sm.v[buf][j * kPad + col];
-                const float4 w0 = load4(sm.w + j * kRows), w1 = load4(sm.w + j * kRows + 4);
-                const float w[kRows] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            for (int r = 0; r < R; ++r) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) o[r] = fmaf(w[r], vx, o[r]);
+                for (int off = 1; off < kLanes; off <<= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], off);
+                x[r] = seen ? x[r] : -CUDART_INF_F;
+                weight[r] = exp2f(x[r] - m[r]);
+                grow |= !(weight[r] <= kMostWeight);
             }
-        }
-        if (kParts > 1) {
-            __syncthreads();
-            if (part == 1)
+            if (__any_sync(0xffffffffu, grow)) {         // the first tile, and rarely later
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) sm.o[r * D + col] = o[r];
-            __syncthreads();
-            if (part == 0)
+                for (int r = 0; r < R; ++r) {
+                    float mx = fmaxf(m[r], x[r]);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) o[r] += sm.o[r * D + col];
-        }
-        if (part == 0) {
-            const bool whole = k_first == 0 && k_last == c.T;
-            const int n_pre = whole && info.x > 0 ? p.n_split : 0;
-            const int64_t slot = part_slot(piece, k_first == 0);
+                    for (int off = kLanes; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float corr = exp2f(m[r] - mx);
+                    m[r] = mx;
+                    l[r] *= corr;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (r >= rows) break;
-                float l = sm.l[r], m = sm.m[r], x = o[r];
-                for (int i = 0; i < n_pre; ++i) {
-                    const int64_t at = prefix_row(p, i, s, head0 + r);
-                    const float2 ml = p.pre_ml[at];
-                    float w, w2;
-                    join(m, l, ml.x, ml.y, w, w2);
-                    x = x * w + p.pre_o[at * D + col] * w2;
+                    for (int e = 0; e < kCols; ++e) o[r][e] *= corr;
+                    weight[r] = exp2f(x[r] - mx);
                 }
-                if (whole) {
-                    static_cast<float*>(a.o)[s * a.o_stride + (int64_t)(head0 + r) * D + col] = l == 0.f ? 0.f : x / l;
-                    if (col == 0) write_lse(a, s, head0 + r, m, l);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) l[r] += weight[r];
+            if (my_part == 0)
+#pragma unroll
+                for (int r = 0; r < R; r += 4)
+                    *reinterpret_cast<float4*>(w + my_key * R + r) = make_float4(weight[r], weight[r + 1], weight[r + 2], weight[r + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+                float v[kCols];
+                const int y = kCols * lane / 4 ^ (j * kLanes & 7);
+                if constexpr (kCols == 4) {
+                    const float4 z = load4(vb + (j * kPieces + y) * 4);
+                    v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
                 } else {
-                    p.part_o[(slot * kRows + r) * D + col] = x;
-                    if (col == 0) p.part_ml[slot * kRows + r] = make_float2(m, l);
+                    const float2 z = *reinterpret_cast<const float2*>(vb + (j * kPieces + y) * 4 + 2 * (lane & 1));
+                    v[0] = z.x, v[1] = z.y;
+                }
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const float4 z = load4(w + j * R + r);
+                    const float ww[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e) o[r + k][e] = fmaf(ww[k], v[e], o[r + k][e]);
                 }
             }
+            __syncwarp();                                // the stage and the weights are read
         }
-        if (tid == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, pieces, all);
+        const bool whole = k_first == 0 && k_last == c.T;
+        const int n_pre = whole && info.x > 0 ? p.n_split : 0;
+        const int64_t slot = part_slot(piece, k_first == 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r >= rows) break;
+            // every key's lanes hold its weight: one of them counts
+            float lt = my_part == 0 ? l[r] : 0.f, mt = m[r];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
+            if (lt == 0.f) mt = -CUDART_INF_F;
+            for (int i = 0; i < n_pre; ++i) {
+                const int64_t pr = prefix_row(p, i, s, head0 + r);
+                const float2 ml = p.pre_ml[pr];
+                float w1, w2;
+                join(mt, lt, ml.x, ml.y, w1, w2);
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) o[r][e] = o[r][e] * w1 + p.pre_o[pr * D + kCols * lane + e] * w2;
+            }
+            float* out = whole ? static_cast<float*>(a.o) + s * a.o_stride + (int64_t)(head0 + r) * D : p.part_o + (slot * R + r) * D;
+            const float f = !whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) out[kCols * lane + e] = o[r][e] * f;
+            if (lane == 0) {
+                if (whole) write_lse(a, s, head0 + r, mt, lt);
+                else p.part_ml[slot * R + r] = make_float2(mt, lt);
+            }
+        }
+        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, pieces, all);
         c.next_unit(p, kKeys);
     }
+    copy_wait<0>();
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t launch_t(const AttnDecodeLaunch& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(decode_suffix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(DecodeSmem<D>));
+    cudaError_t e = cudaFuncSetAttribute(decode_suffix_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(DecodeSmem<D, R>));
     if (e != cudaSuccess) return e;
     note_launch();
-    e = launch_overlapped(decode_suffix_kernel<D>, dim3(p.n_pieces), dim3(kThreads), sizeof(DecodeSmem<D>), s, p);
-    return e == cudaSuccess ? launch_join<float, D, kRows>(p, s) : e;
+    e = launch_overlapped(decode_suffix_kernel<D, R>, dim3(p.n_pieces / kWarps), dim3(kThreads), sizeof(DecodeSmem<D, R>), s, p);
+    return e == cudaSuccess ? launch_join<float, D, R>(p, s) : e;
 }
 
 }  // namespace
@@ -236,8 +288,12 @@ cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// Up to four query heads of a key/value head cost half of eight in the kernel's
+// arithmetic, which is what bounds it beyond two.
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s) {
-    return p.a.d == 128 ? launch_t<128>(p, s) : launch_t<64>(p, s);
+    const bool few = p.a.n_heads / p.a.n_kv_heads <= 4;
+    if (p.a.d == 128) return few ? launch_t<128, 4>(p, s) : launch_t<128, 8>(p, s);
+    return few ? launch_t<64, 4>(p, s) : launch_t<64, 8>(p, s);
 }
 
 }  // namespace kda

@@ -2,9 +2,8 @@
 //
 // The keys that a sequence does not share (its suffix) are cut into tiles.  All
 // tiles of all units (sequence, key/value head, block of query heads), in that
-// order, form one line; it is cut into equal pieces, one for each worker (a warp of
-// the bf16 kernel, a thread block of the fp32 one), so that the workers finish
-// together whatever the lengths are.  A unit inside one piece is finished there
+// order, form one line; it is cut into equal pieces, one for each worker (a warp),
+// so that the workers finish together whatever the lengths are.  A unit inside one piece is finished there
 // (with its prefix's partial results); of a unit that several pieces share, each
 // leaves (m, l, unnormalised o), the piece in which it begins notes it, and the
 // join adds the parts up from the first piece to the last, behind the prefix's
@@ -54,6 +53,15 @@ struct Cursor {
     int2 info;
 
     __device__ __forceinline__ int64_t run() const { return T - k < left ? T - k : left; }   // tiles in this unit
+    // One tile on.
+    __device__ __forceinline__ void step(const AttnDecodeLaunch& p, int tile_keys) {
+        if (k + 1 == T || left == 1) {
+            next_unit(p, tile_keys);                     // (run() is 1 here)
+        } else {
+            ++k;
+            --left;
+        }
+    }
     // To the next unit of the piece (left > 0 afterwards unless it was the last).
     __device__ __forceinline__ void next_unit(const AttnDecodeLaunch& p, int tile_keys) {
         left -= run();

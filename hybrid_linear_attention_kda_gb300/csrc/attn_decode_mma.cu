@@ -17,7 +17,7 @@ namespace kda {
 namespace {
 using namespace decode;
 
-constexpr int kWarps = kDecodeWarpsBf16, kThreads = 32 * kWarps, kRows = kDecodeRowsBf16, kKeys = 16;
+constexpr int kWarps = kDecodeWarps, kThreads = 32 * kWarps, kRows = kDecodeRowsBf16, kKeys = 16;
 constexpr int kLeastTiles = 4;           // of a piece
 constexpr float kMaxGrowth = 8.f;        // log2 of how far weights may exceed 1 before their maximum moves
 
@@ -116,13 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
                 copy16(kd + to, ks + from, j < live);
                 copy16(vd + to, vs + from, j < live);
             }
-            if (++f.k == f.T || f.left == 1) {
-                f.k -= 1;
-                // run() counts from k: hand it the unit's last tile
-                f.next_unit(p, kKeys);
-            } else {
-                f.left -= 1;
-            }
+            f.step(p, kKeys);
             look_up();
         }
         copy_commit();

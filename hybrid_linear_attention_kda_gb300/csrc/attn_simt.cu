@@ -6,11 +6,13 @@
 // in one pass over key tiles, with o and l rescaled whenever m grows.  Scores are
 // kept times log2(e), so that exp is exp2.
 //
-// 256 threads own 64 rows x 64 keys, thread (ty, tx) the rows 4 ty .. 4 ty + 3, the
-// keys tx + 16 c of the score tile and the columns 4 tx + 64 c of the output.  K is
-// padded by 16 bytes a row, so that the 16 threads of a row group read distinct
-// banks; the weights reuse K's place.  Bound by the FP32 pipe and the shared-memory
-// reads that feed it.
+// A thread owns 4 rows, the keys tx + 16 c of a score tile of 64 and the columns
+// 4 tx + 64 c of the output.  A block's 256 threads are one group with 64 rows, or,
+// where that would leave SMs idle, several groups with the same 64 / groups rows and
+// every so manieth key tile each, whose results are joined at the end: the chain of
+// key tiles gets as much shorter.  K is padded by 16 bytes a row, so that the 16
+// threads of a row group read distinct banks; the weights reuse K's place.  Bound by
+// the FP32 pipe and the shared-memory reads that feed it.
 #include <math_constants.h>
 
 #include "attn_common.cuh"
@@ -18,30 +20,41 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kKeys = 64, kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kPacked, kPaged, kPrefix };
 
 template <int D> constexpr int kPad = D + 4;
 template <int D> constexpr int kPPad = kKeys + 4;
-template <int D> constexpr size_t smem_bytes() {
-    return sizeof(float) * ((size_t)kRows * kPad<D> + (size_t)kKeys * kPad<D> + (size_t)kKeys * D);
+constexpr int rows_of(int groups) { return 64 / groups; }
+template <int D> constexpr int kGroupFloats = kKeys * kPad<D> + kKeys * D;         // one group's K and V
+template <int D> constexpr size_t smem_bytes(int groups) {
+    return sizeof(float) * ((size_t)rows_of(groups) * kPad<D> + (size_t)groups * kGroupFloats<D>);
 }
+// Most groups whose tiles fit beside each other.
+template <int D> constexpr int kGroups = D == 64 ? 4 : 2;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 
-template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, int32_t Gp, int32_t chunks) {
+template <int D, int MODE, int GROUPS>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_constant__ AttnTileLaunch p, int32_t Gp, int32_t chunks) {
+    constexpr int kRows = rows_of(GROUPS), kGroupThreads = kThreads / GROUPS;
     extern __shared__ __align__(16) float smem[];
+    const int tid = threadIdx.x, group = tid / kGroupThreads, gt = tid % kGroupThreads;
+    const int tx = gt & 15, ty = gt >> 4;
     float* Qs = smem;
-    float* Ks = Qs + kRows * kPad<D>;
+    float* Ks = Qs + kRows * kPad<D> + group * kGroupFloats<D>;
     float* Vs = Ks + kKeys * kPad<D>;
     float* Ps = Ks;
     static_assert(kPPad<D> <= kPad<D>, "the weights fit in K's place");
+    // a group's own barrier
+    auto group_sync = [&]() {
+        if (GROUPS == 1) __syncthreads();
+        else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+    };
     const kda_attn_prefill_args& a = p.a;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int G = a.n_heads / a.n_kv_heads;
     const int hk = (int)(blockIdx.y / chunks), hc = (int)(blockIdx.y % chunks);
     const int head0 = hk * G + hc * Gp, gn = min(Gp, G - hc * Gp);
@@ -122,9 +135,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
     }
     const float sl = a.scale * kLog2e;
 
-    for (int64_t k0 = k_lo; k0 < k_hi; k0 += kKeys) {
-        __syncthreads();                              // the previous tile is consumed (or Q is written)
-        for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+    __syncthreads();                                  // Q is written
+    for (int64_t k0 = k_lo + group * kKeys; k0 < k_hi; k0 += GROUPS * kKeys) {
+        group_sync();                                 // the previous tile is consumed
+        for (int i = gt; i < kKeys * (D / 4); i += kGroupThreads) {
             const int j = i / (D / 4), c = i % (D / 4) * 4;
             float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
             const float *kr, *vr;
@@ -135,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
             store4(Ks + j * kPad<D> + c, kx);
             store4(Vs + j * D + c, vx);
         }
-        __syncthreads();
+        group_sync();
         float s[4][4] = {};
 #pragma unroll 8
         for (int c = 0; c < D; c += 4) {
@@ -150,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
                 for (int j = 0; j < 4; ++j)
                     s[r][j] = fmaf(qv[r].w, kv[j].w, fmaf(qv[r].z, kv[j].z, fmaf(qv[r].y, kv[j].y, fmaf(qv[r].x, kv[j].x, s[r][j]))));
         }
-        __syncthreads();                              // K is read: the weights take its place
+        group_sync();                                 // K is read: the weights take its place
         // the tile's last key against what the tile's first token sees
         const bool masked = k0 + kKeys > (MODE == kPrefix ? k_hi : min(k_hi, first + rt.t0 + 1));
 #pragma unroll
@@ -212,6 +226,40 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
         else product(std::false_type{});
     }
 
+    if (GROUPS > 1) {
+        // the other groups' results, from their tiles' places, onto the first one's
+        __syncthreads();
+        float* mine = Ks;                             // [row][D], then [row] (m, l)
+        if (group > 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                for (int c = 0; c < OC; ++c) store4(mine + (ty * 4 + r) * D + 4 * tx + 64 * c, o[r][c]);
+                if (tx == 0) *reinterpret_cast<float2*>(mine + kRows * D + 2 * (ty * 4 + r)) = make_float2(m[r], l[r]);
+            }
+        }
+        __syncthreads();
+        if (group > 0) return;
+        for (int x = 1; x < GROUPS; ++x) {
+            const float* from = Ks + x * kGroupFloats<D>;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float2 ml = *reinterpret_cast<const float2*>(from + kRows * D + 2 * (ty * 4 + r));
+                const float mx = fmaxf(m[r], ml.x), ms = mx == -CUDART_INF_F ? 0.f : mx;
+                const float w = exp2f(m[r] - ms), w2 = exp2f(ml.x - ms);
+                m[r] = mx;
+                l[r] = l[r] * w + ml.y * w2;
+#pragma unroll
+                for (int c = 0; c < OC; ++c) {
+                    const float4 z = load4(from + (ty * 4 + r) * D + 4 * tx + 64 * c);
+                    o[r][c].x = o[r][c].x * w + z.x * w2;
+                    o[r][c].y = o[r][c].y * w + z.y * w2;
+                    o[r][c].z = o[r][c].z * w + z.z * w2;
+                    o[r][c].w = o[r][c].w * w + z.w * w2;
+                }
+            }
+        }
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int t = (ty * 4 + r) / Gp, g = (ty * 4 + r) % Gp;
@@ -234,19 +282,34 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(AttnTileLaunch p, i
     }
 }
 
-template <int D, int MODE>
-cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
-    const kda_attn_prefill_args& a = p.a;
-    const int G = a.n_heads / a.n_kv_heads, Gp = G < kRows ? G : kRows, chunks = (G + Gp - 1) / Gp;
-    int64_t tiles = a.total_tokens / (kRows / Gp) + a.n_seqs;
-    if (MODE == kPrefix) tiles *= p.n_split;
-    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem_bytes<D>());
+// Blocks of a launch with the given groups, at most.
+int64_t blocks_of(const AttnTileLaunch& p, int groups, bool prefix, int* Gp, int* chunks) {
+    const int G = p.a.n_heads / p.a.n_kv_heads, rows = rows_of(groups);
+    *Gp = G < rows ? G : rows;
+    *chunks = (G + *Gp - 1) / *Gp;
+    return (p.a.total_tokens / (rows / *Gp) + p.a.n_seqs) * (prefix ? p.n_split : 1);
+}
+
+template <int D, int MODE, int GROUPS>
+cudaError_t launch_g(const AttnTileLaunch& p, cudaStream_t s) {
+    int Gp, chunks;
+    const int64_t tiles = blocks_of(p, GROUPS, MODE == kPrefix, &Gp, &chunks);
+    if (tiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<D, MODE, GROUPS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>(GROUPS));
     if (e != cudaSuccess) return e;
     note_launch();
-    attn_simt_kernel<D, MODE><<<dim3((unsigned)tiles, (unsigned)(a.n_kv_heads * chunks)), kThreads, smem_bytes<D>(), s>>>(
-        p, Gp, chunks);
+    attn_simt_kernel<D, MODE, GROUPS>
+        <<<dim3((unsigned)tiles, (unsigned)(p.a.n_kv_heads * chunks)), kThreads, smem_bytes<D>(GROUPS), s>>>(p, Gp, chunks);
     return cudaGetLastError();
+}
+
+// Several groups where the blocks of one group would not give every SM one.
+template <int D, int MODE>
+cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
+    int Gp, chunks;
+    const int64_t tiles = blocks_of(p, 1, MODE == kPrefix, &Gp, &chunks);
+    return tiles * p.a.n_kv_heads * chunks <= 152 ? launch_g<D, MODE, kGroups<D>>(p, s) : launch_g<D, MODE, 1>(p, s);
 }
 
 template <int D>

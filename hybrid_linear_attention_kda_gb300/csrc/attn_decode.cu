@@ -89,23 +89,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + R - 1) / R;
     __shared__ PieceStart at_[kWarps];
-    int64_t all, pieces;
-    find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_, all, pieces);
+    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
     finish_empty<float, D>(p, piece, p.n_pieces, lane);
-    if (piece >= pieces) {
+    if (piece >= line.pieces) {
         if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
         return;
     }
-    Cursor c = start(p, at_[warp], a.n_kv_heads * blocks, kKeys);
+    Cursor c = start(at_[warp], line, piece, a.n_kv_heads * blocks, kKeys);
 
     // ------------------------------------------------------------------ copies, kStages - 1 tiles ahead
     Cursor f = c;
     int32_t next_block = 0;                              // table entry of the place f
+    const int page_shift = __ffs(a.block_size) - 1;
     auto look_up = [&]() {
         const int64_t key = f.info.x + f.k * kKeys;
-        next_block = f.left > 0 && key < f.info.y ? a.block_table[(int64_t)f.s * a.table_stride + key / a.block_size] : -2;
+        next_block = f.left > 0 && key < f.info.y ? a.block_table[(int64_t)f.s * a.table_stride + (key >> page_shift)] : -2;
     };
     auto fetch = [&](int stage) {
         if (f.left > 0) {
@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
                 flag(p.status, KDA_DEV_BAD_SLOT);
                 live = 0;
             }
-            const int hk = f.u / blocks;
-            const int64_t row = live > 0 ? ((int64_t)next_block * a.n_kv_heads + hk) * a.block_size + key % a.block_size : 0;
+            const int hk = blocks == 1 ? f.u : f.u / blocks;
+            const int64_t row = live > 0 ? ((int64_t)next_block * a.n_kv_heads + hk) * a.block_size + (key & (a.block_size - 1)) : 0;
             const float* ks = static_cast<const float*>(a.k_cache) + row * D;
             const float* vs = static_cast<const float*>(a.v_cache) + row * D;
 #pragma unroll
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
                 else p.part_ml[slot * R + r] = make_float2(mt, lt);
             }
         }
-        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, pieces, all);
+        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, line);
         c.next_unit(p, kKeys);
     }
     copy_wait<0>();

@@ -30,19 +30,31 @@ __device__ __forceinline__ int2 seq_info(const AttnDecodeLaunch& p, int32_t s) {
     return make_int2(0, kv < 0 || kv > (int64_t)p.a.table_stride * p.a.block_size ? 0 : (int)kv);
 }
 __device__ __forceinline__ int64_t seq_tiles(int2 info, int tile_keys) {
-    return info.y > info.x ? ((int64_t)info.y - info.x + tile_keys - 1) / tile_keys : 0;
+    return info.y > info.x ? ((uint32_t)(info.y - info.x) + (uint32_t)tile_keys - 1) / (uint32_t)tile_keys : 0;
 }
 
-// The line has as many pieces as there are workers, or fewer of at least `least`
-// tiles: a shorter one costs more in the join than it saves.  Piece c holds the tiles
-// [begin(c), begin(c + 1)).
-__device__ __forceinline__ int64_t n_pieces(int64_t all, int64_t most, int least) {
-    const int64_t n = (all + least - 1) / least;
-    return n < most ? n : most;
+// Division of counts that mostly fit 32 bits, where it takes a quarter of the time.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
-__device__ __forceinline__ int64_t piece_begin(int64_t all, int64_t c, int64_t n) {
-    return all / n * c + all % n * c / n;
-}
+
+// The line of `all` tiles has as many pieces as there are workers, or fewer of at least
+// `least` tiles: a shorter one costs more in the join than it saves.  Piece c holds the
+// tiles [begin(c), begin(c + 1)); the first `more` pieces hold one tile more than the
+// others.
+struct Line {
+    int64_t all, pieces, size, more;
+    __device__ __forceinline__ Line(int64_t tiles, int64_t most, int least) : all(tiles) {
+        pieces = min(most, divide(all + least - 1, least));
+        size = pieces > 0 ? divide(all, pieces) : 0;
+        more = all - size * pieces;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * size + min(c, more); }
+    __device__ __forceinline__ int64_t piece_of(int64_t x) const {
+        const int64_t long_ones = more * (size + 1);
+        return x < long_ones ? divide(x, size + 1) : more + divide(x - long_ones, size);
+    }
+};
 
 // A place on the line: unit u of sequence s, tiles k .. of its T.
 struct Cursor {
@@ -76,17 +88,16 @@ struct Cursor {
 };
 
 // The pieces of a thread block of NT threads with PIECES workers: fills at[] for
-// them (the caller's shared memory) and returns the line's length in tiles and pieces.
-// Thread i counts the tiles of its share of the sequences, one block scan gives the
-// line's length, and the thread whose share holds a piece's first tile walks it
-// again.
+// them (the caller's shared memory) and returns the line.  Thread i counts the tiles
+// of its share of the sequences, one block scan gives the line's length, and the
+// thread whose share holds a piece's first tile walks it again.
 struct PieceStart {
     int32_t s;
-    int64_t rel, left;     // tiles past the first of s, tiles of the piece
+    int2 info;
+    int64_t rel;           // tiles past the first of s
 };
 template <int NT, int PIECES>
-__device__ void find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, int least, PieceStart* at, int64_t& all,
-                            int64_t& pieces) {
+__device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, int least, PieceStart* at) {
     __shared__ int64_t scan_buf[NT / 32];
     const int32_t n = p.a.n_seqs;
     const int32_t share = (n + NT - 1) / NT, s0 = min(n, (int32_t)threadIdx.x * share), s1 = min(n, s0 + share);
@@ -95,35 +106,36 @@ __device__ void find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys,
     for (int32_t s = s0; s < s1; ++s) mine += seq_tiles(seq_info(p, s), tile_keys);
     int64_t total;
     const int64_t before = block_scan<NT>(mine, scan_buf, &total) - mine;
-    all = total * units;
-    pieces = n_pieces(all, p.n_pieces, least);
+    const Line line(total * units, p.n_pieces, least);
     for (int i = 0; i < PIECES; ++i) {
         const int64_t c = (int64_t)blockIdx.x * PIECES + i;
-        if (c >= pieces) break;
-        const int64_t begin = piece_begin(all, c, pieces);
+        if (c >= line.pieces) break;
+        const int64_t begin = line.begin(c);
         if (before * units > begin || begin >= (before + mine) * units) continue;
         int64_t x = before;
         for (int32_t s = s0;; ++s) {
-            const int64_t t = seq_tiles(seq_info(p, s), tile_keys);
+            const int2 info = seq_info(p, s);
+            const int64_t t = seq_tiles(info, tile_keys);
             if (begin < (x + t) * units) {
-                at[i] = PieceStart{s, begin - x * units, piece_begin(all, c + 1, pieces) - begin};
+                at[i] = PieceStart{s, info, begin - x * units};
                 break;
             }
             x += t;
         }
     }
     __syncthreads();
+    return line;
 }
 
-__device__ __forceinline__ Cursor start(const AttnDecodeLaunch& p, const PieceStart& at, int units, int tile_keys) {
+__device__ __forceinline__ Cursor start(const PieceStart& at, const Line& line, int64_t piece, int units, int tile_keys) {
     Cursor c;
     c.s = at.s;
     c.units = units;
-    c.info = seq_info(p, at.s);
-    c.T = seq_tiles(c.info, tile_keys);
-    c.u = (int32_t)(at.rel / c.T);
+    c.info = at.info;
+    c.T = seq_tiles(at.info, tile_keys);
+    c.u = (int32_t)divide(at.rel, c.T);
     c.k = at.rel - c.u * c.T;
-    c.left = at.left;
+    c.left = line.begin(piece + 1) - line.begin(piece);
     return c;
 }
 
@@ -250,17 +262,12 @@ cudaError_t launch_join(const AttnDecodeLaunch& p, cudaStream_t s) {
     return launch_overlapped(join_kernel<T, D, ROWS>, dim3((unsigned)p.n_pieces), dim3(32 * kJoinWarps), 0, s, p);
 }
 
-// Notes for the join whether the unit of the piece that ends at cursor c's run
-// begins there and goes on: `done` tiles of the unit lie in the piece.
-__device__ __forceinline__ int4 open_unit(const Cursor& c, int64_t piece, int64_t pieces, int64_t all) {
+// Notes for the join whether the last unit of the piece, at cursor c, begins there
+// and goes on in later pieces.
+__device__ __forceinline__ int4 open_unit(const Cursor& c, int64_t piece, const Line& line) {
     const int64_t rest = c.T - (c.k + c.run());          // its tiles in later pieces
     if (c.k != 0 || rest == 0) return make_int4(-1, 0, 0, 0);
-    const int64_t x = piece_begin(all, piece + 1, pieces) + rest - 1;    // its last tile
-    int64_t last = (int64_t)((double)x * pieces / (double)all);
-    last = last < piece ? piece : last >= pieces ? pieces - 1 : last;
-    while (last > piece && piece_begin(all, last, pieces) > x) --last;
-    while (last + 1 < pieces && piece_begin(all, last + 1, pieces) <= x) ++last;
-    return make_int4(c.s, c.u, (int)last, 0);
+    return make_int4(c.s, c.u, (int)line.piece_of(line.begin(piece + 1) + rest - 1), 0);
 }
 
 }  // namespace decode

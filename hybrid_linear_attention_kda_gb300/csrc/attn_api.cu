@@ -93,15 +93,15 @@ size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 int decode_rows(int32_t dtype) { return dtype == KDA_BF16 ? kda::kDecodeRowsBf16 : kda::kDecodeRowsF32; }
 
-// Blocks of keys that a shared prefix is cut into: enough row tiles (256 rows in
-// bf16, 64 in fp32) times blocks for the thread blocks that run at once (one on
-// each of 152 SMs, two), at most 64.
+// Blocks of keys that a shared prefix is cut into: bf16 enough for a thread block (256
+// rows) on each of 152 SMs, fp32 enough for one (64 rows) on every second one, whose
+// blocks then split up further (attn_simt.cu); at most 64.
 int prefix_splits(const kda_attn_decode_args& a) {
     if (a.n_groups == 0) return 0;
     const bool bf16 = a.dtype == KDA_BF16;
     const int64_t G = a.n_heads / a.n_kv_heads;
     const int64_t items = ((int64_t)a.n_seqs * G / (bf16 ? 256 : 64) + a.n_groups) * a.n_kv_heads;
-    const int64_t n = ((bf16 ? 152 : 304) + items - 1) / items;
+    const int64_t n = bf16 ? (152 + items - 1) / items : 76 / items;
     return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 
@@ -191,7 +191,6 @@ kda_status_t kda_cache_append(int64_t n_tokens, int32_t n_kv_heads, int32_t d, i
     const int vec = 16 / esize(dtype);
     kda::CacheAppendLaunch p{n_tokens, n_kv_heads, n_kv_heads * (d / vec), d / vec, k, v, k_stride / vec, v_stride / vec,
                              slot_map, k_cache, v_cache, n_blocks, block_size, nullptr};
-    if (n_tokens * 2 * p.row_vecs / 1024 >= (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "n_tokens * n_kv_heads * d too large");
     KDA_TRY(kda::device_status_word(&p.status));
     const cudaError_t e = kda::launch_cache_append(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache append launch");
@@ -275,6 +274,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     p.a = a;
     p.n_pieces = kda::kDecodePieces;
     p.n_split = prefix_splits(a);
+    p.prefix_tile = a.dtype == KDA_BF16 ? kda::kTileKeysBf16 : kda::kTileKeysF32;
     p.pre_o = reinterpret_cast<float*>(ws + sp.pre_o);
     p.pre_ml = reinterpret_cast<float2*>(ws + sp.pre_ml);
     p.part_o = reinterpret_cast<float*>(ws + sp.part_o);

@@ -106,6 +106,7 @@ struct AttnTileLaunch {
 };
 
 // Prompt attention, and the shared-prefix part of decode attention (prefix_lens set).
+constexpr int kTileKeysF32 = 64, kTileKeysBf16 = 128;                    // keys of a tile
 cudaError_t launch_attn_simt(const AttnTileLaunch& p, cudaStream_t s);   // fp32
 cudaError_t launch_attn_tc(const AttnTileLaunch& p, cudaStream_t s);     // bf16
 inline cudaError_t launch_attn_tile(const AttnTileLaunch& p, cudaStream_t s) {
@@ -118,6 +119,7 @@ struct AttnDecodeLaunch {
     uint32_t* status;
     int32_t n_pieces;             // workers of the suffix kernel
     int32_t n_split;              // key blocks of the prefix (0: no groups)
+    int32_t prefix_tile;          // keys of a tile of the prefix kernel, which the blocks are made of
     float* pre_o;                 // [n_split, n_seqs, H, d] the prefix's partial results
     float2* pre_ml;               // [n_split, n_seqs, H]
     float* part_o;                // [2 * n_pieces, rows, d]: a piece's first unit, its last unit

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
             __syncwarp();                                // the stage and the weights are read
         }
         const bool whole = k_first == 0 && k_last == c.T;
-        const int n_pre = whole && info.x > 0 ? p.n_split : 0;
+        const int n_pre = whole ? prefix_parts(p, info.x) : 0;
         const int64_t slot = part_slot(piece, k_first == 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
             if (lt == 0.f) mt = -CUDART_INF_F;
+#pragma unroll 2
             for (int i = 0; i < n_pre; ++i) {
                 const int64_t pr = prefix_row(p, i, s, head0 + r);
                 const float2 ml = p.pre_ml[pr];

@@ -151,6 +151,14 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, flo
     m = mx;
 }
 
+// Blocks of keys that hold something of a shared prefix (the others' results are
+// empty): as the prefix kernels cut it.
+__device__ __forceinline__ int prefix_parts(const AttnDecodeLaunch& p, int shared) {
+    if (shared <= 0) return 0;
+    const uint32_t tiles = ((uint32_t)shared + p.prefix_tile - 1) / p.prefix_tile;
+    const uint32_t per = (tiles + p.n_split - 1) / p.n_split;
+    return (int)((tiles + per - 1) / per);
+}
 __device__ __forceinline__ int64_t prefix_row(const AttnDecodeLaunch& p, int i, int32_t s, int head) {
     return ((int64_t)i * p.a.n_seqs + s) * p.a.n_heads + head;
 }
@@ -168,9 +176,10 @@ __device__ void finish_empty(const AttnDecodeLaunch& p, int64_t w, int64_t n, in
         const int2 info = seq_info(p, (int32_t)s);
         if (a.n_groups == 0 && info.y != a.kv_lens[s] && lane == 0) flag(p.status, KDA_DEV_BAD_SEQLENS);
         if (info.y > info.x) continue;
-        const int n_pre = info.x > 0 ? p.n_split : 0;
+        const int n_pre = prefix_parts(p, info.x);
         for (int head = 0; head < a.n_heads; ++head) {
             float m = -CUDART_INF_F, l = 0.f, o[kCols] = {};
+#pragma unroll 4
             for (int i = 0; i < n_pre; ++i) {
                 const int64_t at = prefix_row(p, i, (int32_t)s, head);
                 const float2 ml = p.pre_ml[at];
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + ROWS - 1) / ROWS;
     const int hk = open.y / blocks, rb = open.y % blocks;
     const int head0 = hk * G + rb * ROWS, rows = min(ROWS, G - rb * ROWS);
-    const int2 info = seq_info(p, s);
+    const int n_pre = prefix_parts(p, seq_info(p, s).x);
     const int row_warps = rows >= 8 ? 8 : rows >= 4 ? 4 : rows >= 2 ? 2 : 1, part_warps = kJoinWarps / row_warps;
     const int r0 = warp % row_warps, pw = warp / row_warps;
     const int64_t per = (parts + part_warps - 1) / part_warps;
@@ -226,8 +235,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
             for (int e = 0; e < kCols; ++e) o[e] = o[e] * w + x[e] * w2;
         };
         if (r < rows) {
-            if (pw == 0 && info.x > 0)
-                for (int i = 0; i < p.n_split; ++i) {
+            if (pw == 0)
+#pragma unroll 4
+                for (int i = 0; i < n_pre; ++i) {
                     const int64_t at = prefix_row(p, i, s, head);
                     add(p.pre_ml[at], p.pre_o + at * D);
                 }

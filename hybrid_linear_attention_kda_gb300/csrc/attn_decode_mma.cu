@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
         }
 
         const bool whole = k_first == 0 && k_last == c.T;
-        const int n_pre = whole && info.x > 0 ? p.n_split : 0;
+        const int n_pre = whole ? prefix_parts(p, info.x) : 0;
         const int64_t slot = part_slot(piece, k_first == 0);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
             lt += __shfl_xor_sync(0xffffffffu, lt, 2);
             const int rr = row + 8 * r, head = head0 + rr;
             if (rr >= rows) continue;
+#pragma unroll 2
             for (int i = 0; i < n_pre; ++i) {
                 const int64_t pr = prefix_row(p, i, s, head);
                 const float2 ml = p.pre_ml[pr];

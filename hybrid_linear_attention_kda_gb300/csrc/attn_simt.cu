@@ -20,7 +20,7 @@
 namespace kda {
 namespace {
 
-constexpr int kKeys = 64, kThreads = 256;
+constexpr int kKeys = kTileKeysF32, kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kPacked, kPaged, kPrefix };

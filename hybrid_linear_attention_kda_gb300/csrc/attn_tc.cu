@@ -810,6 +810,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     }
 }
 
+static_assert(kTile == kTileKeysBf16, "the decode join counts a prefix's tiles");
+
 // ------------------------------------------------------------------ launch
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

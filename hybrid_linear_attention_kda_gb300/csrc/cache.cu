@@ -118,41 +118,43 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(CachePlanLaunc
 }
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendVecs = 4;
+constexpr int kAppendVecs = 8;
 
-// Pure copy: 16-byte pieces, four in flight per thread.  Piece i of the launch is
-// (token, k or v, piece of the token's heads).
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppendLaunch p) {
-    const int64_t per_token = 2 * (int64_t)p.row_vecs;
-    const int64_t n = p.n_tokens * per_token;
-    const int64_t i0 = (int64_t)blockIdx.x * kAppendThreads * kAppendVecs + threadIdx.x;
-    float4 r[kAppendVecs];
-    float4* dst[kAppendVecs];
+// Pure copy: 16-byte pieces, eight in flight per thread.  A block takes whole tokens
+// (k and v, all heads), as many as fill its threads' eight pieces, at least one.
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ CacheAppendLaunch p,
+                                                                      int32_t block_tokens) {
+    const int64_t t0 = (int64_t)blockIdx.x * block_tokens;
+    const uint32_t row_vecs = (uint32_t)p.row_vecs, head_vecs = (uint32_t)p.head_vecs;
+    const uint32_t n = 2 * row_vecs * (uint32_t)min((int64_t)block_tokens, p.n_tokens - t0);
+    const uint32_t page = (uint32_t)p.block_size;
     const int64_t n_slots = p.n_blocks * p.block_size;
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kAppendThreads * kAppendVecs) {
+        float4 r[kAppendVecs];
+        float4* dst[kAppendVecs];
 #pragma unroll
-    for (int m = 0; m < kAppendVecs; ++m) {
-        const int64_t i = i0 + m * kAppendThreads;
-        dst[m] = nullptr;
-        if (i >= n) continue;
-        const int64_t t = i / per_token;
-        int32_t x = (int32_t)(i - t * per_token);
-        const bool is_v = x >= p.row_vecs;
-        x -= is_v ? p.row_vecs : 0;
-        const int32_t slot = p.slot_map[t];
-        if (slot < 0 || slot >= n_slots) {
-            if (slot != -1) flag(p.status, KDA_DEV_BAD_SLOT);
-            continue;
+        for (int m = 0; m < kAppendVecs; ++m) {
+            const uint32_t i = i0 + m * kAppendThreads;
+            dst[m] = nullptr;
+            if (i >= n) continue;
+            const uint32_t half = i / row_vecs, x = i - half * row_vecs;     // half: 2 * token, or that + 1 for v
+            const int64_t t = t0 + (half >> 1);
+            const bool is_v = half & 1;
+            const int32_t slot = p.slot_map[t];
+            if (slot < 0 || slot >= n_slots) {
+                if (slot != -1) flag(p.status, KDA_DEV_BAD_SLOT);
+                continue;
+            }
+            const uint32_t block = (uint32_t)slot / page, off = (uint32_t)slot - block * page;
+            const uint32_t h = x / head_vecs, e = x - h * head_vecs;
+            r[m] = __ldcs(static_cast<const float4*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) + x);
+            dst[m] = static_cast<float4*>(is_v ? p.v_cache : p.k_cache) +
+                     (((int64_t)block * p.n_kv_heads + h) * page + off) * head_vecs + e;
         }
-        const int32_t block = slot / p.block_size, off = slot - block * p.block_size;
-        const int32_t h = x / p.head_vecs, e = x - h * p.head_vecs;
-        const float4* src = static_cast<const float4*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) + x;
-        r[m] = __ldcs(src);
-        dst[m] = static_cast<float4*>(is_v ? p.v_cache : p.k_cache) +
-                 (((int64_t)block * p.n_kv_heads + h) * p.block_size + off) * p.head_vecs + e;
-    }
 #pragma unroll
-    for (int m = 0; m < kAppendVecs; ++m)
-        if (dst[m]) *dst[m] = r[m];
+        for (int m = 0; m < kAppendVecs; ++m)
+            if (dst[m]) *dst[m] = r[m];
+    }
 }
 
 }  // namespace
@@ -169,10 +171,11 @@ cudaError_t launch_cache_plan(const CachePlanLaunch& p, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& p, cudaStream_t s) {
-    const int64_t n = p.n_tokens * 2 * p.row_vecs;
-    const int64_t per = (int64_t)kAppendThreads * kAppendVecs;
+    const int32_t fit = kAppendThreads * kAppendVecs / (2 * p.row_vecs);
+    // few tokens: spread them over the SMs, one to a block
+    const int32_t block_tokens = fit > 1 && p.n_tokens > 2 * 152 * (int64_t)fit ? fit : 1;
     note_launch();
-    cache_append_kernel<<<(unsigned)((n + per - 1) / per), kAppendThreads, 0, s>>>(p);
+    cache_append_kernel<<<(unsigned)((p.n_tokens + block_tokens - 1) / block_tokens), kAppendThreads, 0, s>>>(p, block_tokens);
     return cudaGetLastError();
 }
 

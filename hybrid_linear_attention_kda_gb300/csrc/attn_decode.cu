@@ -26,6 +26,8 @@ __device__ int32_t group_of(const int32_t* start, int32_t n_groups, int32_t s) {
 }
 
 __global__ void __launch_bounds__(kInfoThreads) decode_info_kernel(const __grid_constant__ AttnDecodeLaunch p) {
+    griddep_wait();
+    griddep_launch();
     const kda_attn_decode_args& a = p.a;
     const int64_t cap = (int64_t)a.table_stride * a.block_size;
     const int32_t x = (int32_t)(blockIdx.x * kInfoThreads + threadIdx.x);
@@ -84,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     constexpr int kKeys = S::kKeys, kLanes = S::kLanesPerKey, kPieces = D / 4, kCols = D / 32;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>(smem_raw);
-    griddep_wait();
+    start_after(p);
     const kda_attn_decode_args& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + R - 1) / R;
@@ -92,9 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
-    finish_empty<float, D>(p, piece, p.n_pieces, lane);
     if (piece >= line.pieces) {
         if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
+        finish_empty<float, D>(p, piece, lane);
         return;
     }
     Cursor c = start(at_[warp], line, piece, a.n_kv_heads * blocks, kKeys);
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
         }
         const bool whole = k_first == 0 && k_last == c.T;
         const int n_pre = whole ? prefix_parts(p, info.x) : 0;
+        if (n_pre > 0) griddep_wait();                   // the prefix's results
         const int64_t slot = part_slot(piece, k_first == 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -268,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
         c.next_unit(p, kKeys);
     }
     copy_wait<0>();
+    finish_empty<float, D>(p, piece, lane);
 }
 
 template <int D, int R>
@@ -285,8 +289,8 @@ cudaError_t launch_t(const AttnDecodeLaunch& p, cudaStream_t s) {
 cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s) {
     const int32_t n = p.a.n_seqs > p.a.n_groups ? p.a.n_seqs : p.a.n_groups;
     note_launch();
-    decode_info_kernel<<<(unsigned)((n + kInfoThreads - 1) / kInfoThreads), kInfoThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(decode_info_kernel, dim3((unsigned)((n + kInfoThreads - 1) / kInfoThreads)), dim3(kInfoThreads), 0,
+                             s, p);
 }
 
 // Up to four query heads of a key/value head cost half of eight in the kernel's

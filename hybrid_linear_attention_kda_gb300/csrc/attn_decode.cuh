@@ -22,6 +22,15 @@ namespace decode {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The suffix kernel follows the prefix's kernel, where there are groups, and then starts
+// beside it: that kernel starts when everything before it, the info kernel included,
+// has completed, so only its own results are still to come.  They are waited for where
+// they are joined, and by every worker before it ends, so that the join kernel follows
+// both.
+__device__ __forceinline__ void start_after(const AttnDecodeLaunch& p) {
+    if (p.a.n_groups == 0) griddep_wait();
+}
+
 // Shared and total positions of sequence s.  With groups the info kernel has
 // written them; without, they come straight from kv_lens.
 __device__ __forceinline__ int2 seq_info(const AttnDecodeLaunch& p, int32_t s) {
@@ -166,11 +175,14 @@ __device__ __forceinline__ void write_lse(const kda_attn_decode_args& a, int32_t
     if (a.lse) a.lse[(int64_t)s * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m, kLn2, logf(l));
 }
 
-// Sequences without a suffix: zeros, or the prefix's results.  Worker w of n takes
-// every n-th sequence, a lane D / 32 columns.  Also reports bad lengths.
+// A worker's end: sequences without a suffix give zeros, or the prefix's results.
+// Worker w of n takes every n-th sequence, a lane D / 32 columns.  Also reports bad
+// lengths.
 template <typename T, int D>
-__device__ void finish_empty(const AttnDecodeLaunch& p, int64_t w, int64_t n, int lane) {
+__device__ void finish_empty(const AttnDecodeLaunch& p, int64_t w, int lane) {
     constexpr int kCols = D / 32;
+    griddep_wait();
+    const int64_t n = p.n_pieces;
     const kda_attn_decode_args& a = p.a;
     for (int64_t s = w; s < a.n_seqs; s += n) {
         const int2 info = seq_info(p, (int32_t)s);

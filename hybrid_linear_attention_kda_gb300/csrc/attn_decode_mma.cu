@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     constexpr int kChunks = D / 8, kStages = S::kStages;  // 16-byte pieces of a key
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S& sm = *reinterpret_cast<S*>(smem_raw);
-    griddep_wait();
+    start_after(p);
     const kda_attn_decode_args& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
-    finish_empty<__nv_bfloat16, D>(p, piece, p.n_pieces, lane);
     if (piece >= line.pieces) {
         if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
+        finish_empty<__nv_bfloat16, D>(p, piece, lane);
         return;
     }
     Cursor c = start(at_[warp], line, piece, a.n_kv_heads * blocks, kKeys);
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
 
         const bool whole = k_first == 0 && k_last == c.T;
         const int n_pre = whole ? prefix_parts(p, info.x) : 0;
+        if (n_pre > 0) griddep_wait();                   // the prefix's results
         const int64_t slot = part_slot(piece, k_first == 0);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
         c.next_unit(p, kKeys);
     }
     copy_wait<0>();
+    finish_empty<__nv_bfloat16, D>(p, piece, lane);
 }
 
 template <int D>

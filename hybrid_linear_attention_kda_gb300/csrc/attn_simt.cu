@@ -41,6 +41,8 @@ __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<f
 template <int D, int MODE, int GROUPS>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_constant__ AttnTileLaunch p, int32_t Gp, int32_t chunks) {
     constexpr int kRows = rows_of(GROUPS), kGroupThreads = kThreads / GROUPS;
+    griddep_wait();
+    griddep_launch();
     extern __shared__ __align__(16) float smem[];
     const int tid = threadIdx.x, group = tid / kGroupThreads, gt = tid % kGroupThreads;
     const int tx = gt & 15, ty = gt >> 4;
@@ -292,16 +294,15 @@ int64_t blocks_of(const AttnTileLaunch& p, int groups, bool prefix, int* Gp, int
 
 template <int D, int MODE, int GROUPS>
 cudaError_t launch_g(const AttnTileLaunch& p, cudaStream_t s) {
-    int Gp, chunks;
+    int32_t Gp, chunks;
     const int64_t tiles = blocks_of(p, GROUPS, MODE == kPrefix, &Gp, &chunks);
     if (tiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<D, MODE, GROUPS>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>(GROUPS));
     if (e != cudaSuccess) return e;
     note_launch();
-    attn_simt_kernel<D, MODE, GROUPS>
-        <<<dim3((unsigned)tiles, (unsigned)(p.a.n_kv_heads * chunks)), kThreads, smem_bytes<D>(GROUPS), s>>>(p, Gp, chunks);
-    return cudaGetLastError();
+    return launch_overlapped(attn_simt_kernel<D, MODE, GROUPS>, dim3((unsigned)tiles, (unsigned)(p.a.n_kv_heads * chunks)),
+                             dim3(kThreads), smem_bytes<D>(GROUPS), s, p, Gp, chunks);
 }
 
 // Several groups where the blocks of one group would not give every SM one.

@@ -335,6 +335,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     const kda_attn_prefill_args& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, tokens = kTile / G;
+    griddep_wait();
+    griddep_launch();
 
     if (warp == kMmaWarp) tmem_alloc(&ms.tslot, kTmemCols);
     if (tid == 0) {
@@ -624,6 +626,9 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     if (!(ok = wait_all(&ms.want, i & 1))) break;
                     ++i;
                 }
+                // a shared prefix's blocks do not claim: the kernel that starts beside this one
+                // waits for every block to have started
+                if (MODE == kPrefix) break;
                 if (lane == 0) {
                     mbar_expect_tx(&ms.next, 16);
                     ask_next_block(&ms.next_block, &ms.next);
@@ -877,8 +882,7 @@ cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
                                                (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
     note_launch();
-    attn_tc_kernel<D, MODE><<<(unsigned)blocks, kThreads, smem_bytes<D>(), s>>>(p, maps);
-    return cudaGetLastError();
+    return launch_overlapped(attn_tc_kernel<D, MODE>, dim3((unsigned)blocks), dim3(kThreads), smem_bytes<D>(), s, p, maps);
 }
 
 template <int D>

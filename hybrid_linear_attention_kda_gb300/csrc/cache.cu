@@ -15,7 +15,9 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 
-__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(CachePlanLaunch p, int64_t slice) {
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_constant__ CachePlanLaunch p,
+                                                                  int64_t slice) {
+    griddep_wait();
     __shared__ int64_t scan_buf[kPlanThreads / 32];
     __shared__ int32_t s_cu[kPlanThreads + 1], s_cached[kPlanThreads];
     __shared__ int64_t s_first[kPlanThreads];
@@ -118,12 +120,13 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(CachePlanLaunc
 }
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendVecs = 8;
+constexpr int kAppendVecs = 4;
 
-// Pure copy: 16-byte pieces, eight in flight per thread.  A block takes whole tokens
-// (k and v, all heads), as many as fill its threads' eight pieces, at least one.
+// Pure copy: 16-byte pieces, four in flight per thread.  A block takes whole tokens
+// (k and v, all heads), as many as fill its threads' four pieces, at least one.
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ CacheAppendLaunch p,
                                                                       int32_t block_tokens) {
+    griddep_wait();
     const int64_t t0 = (int64_t)blockIdx.x * block_tokens;
     const uint32_t row_vecs = (uint32_t)p.row_vecs, head_vecs = (uint32_t)p.head_vecs;
     const uint32_t n = 2 * row_vecs * (uint32_t)min((int64_t)block_tokens, p.n_tokens - t0);
@@ -166,8 +169,7 @@ cudaError_t launch_cache_plan(const CachePlanLaunch& p, cudaStream_t s) {
     slice = slice < kPlanThreads ? kPlanThreads : slice;
     const int64_t blocks = p.a.max_tokens > 0 ? (p.a.max_tokens + slice - 1) / slice : 1;
     note_launch();
-    cache_plan_kernel<<<(unsigned)blocks, kPlanThreads, 0, s>>>(p, slice);
-    return cudaGetLastError();
+    return launch_overlapped(cache_plan_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), 0, s, p, slice);
 }
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& p, cudaStream_t s) {
@@ -175,8 +177,8 @@ cudaError_t launch_cache_append(const CacheAppendLaunch& p, cudaStream_t s) {
     // few tokens: spread them over the SMs, one to a block
     const int32_t block_tokens = fit > 1 && p.n_tokens > 2 * 152 * (int64_t)fit ? fit : 1;
     note_launch();
-    cache_append_kernel<<<(unsigned)((p.n_tokens + block_tokens - 1) / block_tokens), kAppendThreads, 0, s>>>(p, block_tokens);
-    return cudaGetLastError();
+    return launch_overlapped(cache_append_kernel, dim3((unsigned)((p.n_tokens + block_tokens - 1) / block_tokens)),
+                             dim3(kAppendThreads), 0, s, p, block_tokens);
 }
 
 }  // namespace kda

@@ -75,7 +75,11 @@ def declare(lib):
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
-_I32, _F32, _Tensor = torch.int32, torch.float32, torch.Tensor
+_CODES = {torch.bfloat16: _kda.KDA_BF16, torch.float32: _kda.KDA_FP32}
+_I32, _F32, _U8, _Tensor, _empty, _byref = torch.int32, torch.float32, torch.uint8, torch.Tensor, torch.empty, ctypes.byref
+
+# A serving step makes these calls for every layer, so each tensor that passes is settled
+# in one expression; what does not goes through the checks that name the fault.
 
 
 def _shape(x, name, ndim):
@@ -86,26 +90,28 @@ def _shape(x, name, ndim):
 
 
 def _dev(x, name, dtype, shape, dev, index):
-    """``_kda._dev`` of a tensor that must have this dtype, shape and device (of index
-    ``index``).  A serving step makes these calls for every layer, so what passes is
-    settled in one expression; what does not goes through the checks that name the fault."""
+    """``_kda._dev`` of a tensor that must have this dtype, shape and device (of index ``index``)."""
     if type(x) is _Tensor and x.dtype is dtype and x.shape == shape and x.get_device() == index and x.is_contiguous():
         return x.data_ptr()
     return _kda._dev(x, name, dtype, shape, dev)
 
 
-def _tokens(x, name, dtype, shape, dev=None):
-    """(address, elements between tokens) of a [T, heads, d] tensor whose tokens are
-    evenly spaced and whose heads are dense."""
+def _tokens(x, name, dtype, shape, dev, index):
+    """(address, elements between tokens) of a [T, heads, d] tensor whose tokens are evenly
+    spaced and whose heads are dense."""
     T, heads, d = shape
-    if not isinstance(x, torch.Tensor):
+    if type(x) is _Tensor and x.dtype is dtype and x.shape == shape and x.get_device() == index and index >= 0:
+        stride, inner, last = x.stride()
+        if last == 1 and inner == d and stride >= heads * d:
+            return x.data_ptr(), stride
+    if not isinstance(x, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor (got {type(x).__name__})")
     if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {x.dtype})")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(x.shape)})")
     stride, inner, last = x.stride()
-    if (last != 1 and d > 1) or (inner != d and heads > 1):
+    if last != 1 or (inner != d and heads > 1):
         raise ValueError(f"{name}'s heads must be dense within a token (strides {x.stride()})")
     if T <= 1:
         stride = heads * d
@@ -113,45 +119,50 @@ def _tokens(x, name, dtype, shape, dev=None):
         raise ValueError(f"{name}'s tokens overlap (strides {x.stride()})")
     if not x.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (got {x.device})")
-    if dev is not None and x.device != dev:
+    if x.device != dev:
         raise ValueError(f"{name} is on {x.device}, the other operands on {dev}")
     return x.data_ptr(), stride
 
 
 def _first(x, name):
-    """(shape, address, stride, device, device index, dtype code) of the tensor that the others
-    have to match."""
+    """(shape, dtype, its code, device, device index, address, stride) of the tensor that the
+    others have to match."""
     shape = _shape(x, name, 3)
-    if x.dtype not in _FLOATS:
-        raise TypeError(f"{name} must be {_FLOATS[0]} or {_FLOATS[1]} (got {x.dtype})")
-    ptr, stride = _tokens(x, name, x.dtype, shape)
-    return shape, ptr, stride, x.device, x.get_device(), _kda._dtype_code(x)
+    dtype = x.dtype
+    if dtype not in _CODES:
+        raise TypeError(f"{name} must be {_FLOATS[0]} or {_FLOATS[1]} (got {dtype})")
+    dev, index = x.device, x.get_device()
+    ptr, stride = _tokens(x, name, dtype, shape, dev, index)
+    return shape, dtype, _CODES[dtype], dev, index, ptr, stride
 
 
-def _on_stream(stream, dev, call):
-    """``call(handle)`` with ``stream`` current, so that what is allocated inside belongs to it."""
-    if stream is None:
-        return call(_current_stream(dev))
+def _on(stream, x):
+    """A context in which ``stream`` is current, so that what is allocated belongs to it."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        stream = torch.cuda.ExternalStream(stream, device=x.device)
+    return torch.cuda.stream(stream)
 
 
-def _current_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+def _elsewhere(stream, x):
+    """Whether a call has to be repeated under ``_on(stream, x)``; a tensor that is not on a GPU
+    is left to the checks."""
+    return stream is not None and isinstance(x, _Tensor) and x.is_cuda
+
+
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):          # the handle without a Stream object around it
-    def _current_stream(dev):                                # noqa: F811
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+    _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _cache(k_cache, v_cache, dtype, heads, d, dev, index):
     """(addresses, n_blocks, block_size) of the paged cache."""
-    n_blocks, _, bs, _ = _shape(k_cache, "k_cache", 4)
-    shape = (n_blocks, heads, bs, d)
-    return (_dev(k_cache, "k_cache", dtype, shape, dev, index), _dev(v_cache, "v_cache", dtype, shape, dev, index),
+    shape = _shape(k_cache, "k_cache", 4)
+    n_blocks, bs = shape[0], shape[2]
+    want = (n_blocks, heads, bs, d)
+    return (_dev(k_cache, "k_cache", dtype, want, dev, index), _dev(v_cache, "v_cache", dtype, want, dev, index),
             n_blocks, bs)
 
 
@@ -166,89 +177,92 @@ def cache_plan(cached_lens, new_lens, block_table, free_blocks, free_begin, free
     free_end int32 [1], two different tensors.  The outputs are allocated unless given.
     Returns a ``CachePlan`` of cu_seqlens [n + 1], kv_lens [n], slot_map and positions
     [max_tokens]."""
+    if _elsewhere(stream, cached_lens):
+        with _on(stream, cached_lens):
+            return cache_plan(cached_lens, new_lens, block_table, free_blocks, free_begin, free_end,
+                              block_size=block_size, n_blocks=n_blocks, max_tokens=max_tokens, cu_seqlens=cu_seqlens,
+                              kv_lens=kv_lens, slot_map=slot_map, positions=positions)
     n, = _shape(cached_lens, "cached_lens", 1)
-    _, stride = _shape(block_table, "block_table", 2)
+    stride = _shape(block_table, "block_table", 2)[1]
     n_free, = _shape(free_blocks, "free_blocks", 1)
     T = int(max_tokens)
     if T < 0:
         raise ValueError(f"max_tokens must be >= 0 (got {T})")
     dev, ix = cached_lens.device, cached_lens.get_device()
-    ptrs = (_dev(cached_lens, "cached_lens", _I32, (n,), None, ix if ix >= 0 else None),
-            _dev(new_lens, "new_lens", _I32, (n,), dev, ix),
-            _dev(free_blocks, "free_blocks", _I32, (n_free,), dev, ix),
-            _dev(free_begin, "free_begin", _I32, (1,), dev, ix), _dev(free_end, "free_end", _I32, (1,), dev, ix),
-            _dev(block_table, "block_table", _I32, (n, stride), dev, ix))
-
-    def call(handle):
-        def out(x, name, size):
-            if x is None:
-                x = torch.empty(size, dtype=_I32, device=dev)
-                return x, x.data_ptr()
-            return x, _dev(x, name, _I32, (size,), dev, ix)
-        kv, kv_p = out(kv_lens, "kv_lens", n)
-        cu, cu_p = out(cu_seqlens, "cu_seqlens", n + 1)
-        slots, slots_p = out(slot_map, "slot_map", T)
-        pos, pos_p = out(positions, "positions", T)
-        a = CachePlanArgs(n, int(block_size), stride, n_free, int(n_blocks), T, *ptrs, kv_p, cu_p, slots_p, pos_p)
-        _kda._check(_kda.load().kda_cache_plan(ctypes.byref(a), handle))
-        return CachePlan(cu, kv, slots, pos)
-    return _on_stream(stream, dev, call)
+    a0 = _dev(cached_lens, "cached_lens", _I32, (n,), None, ix if ix >= 0 else None)
+    a1 = _dev(new_lens, "new_lens", _I32, (n,), dev, ix)
+    a2 = _dev(free_blocks, "free_blocks", _I32, (n_free,), dev, ix)
+    a3 = _dev(free_begin, "free_begin", _I32, (1,), dev, ix)
+    a4 = _dev(free_end, "free_end", _I32, (1,), dev, ix)
+    a5 = _dev(block_table, "block_table", _I32, (n, stride), dev, ix)
+    kv_lens = _empty(n, dtype=_I32, device=dev) if kv_lens is None else kv_lens
+    cu_seqlens = _empty(n + 1, dtype=_I32, device=dev) if cu_seqlens is None else cu_seqlens
+    slot_map = _empty(T, dtype=_I32, device=dev) if slot_map is None else slot_map
+    positions = _empty(T, dtype=_I32, device=dev) if positions is None else positions
+    a = CachePlanArgs(n, int(block_size), stride, n_free, int(n_blocks), T, a0, a1, a2, a3, a4, a5,
+                      _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix), _dev(cu_seqlens, "cu_seqlens", _I32, (n + 1,), dev, ix),
+                      _dev(slot_map, "slot_map", _I32, (T,), dev, ix), _dev(positions, "positions", _I32, (T,), dev, ix))
+    status = _kda.load().kda_cache_plan(_byref(a), _current_stream(ix))
+    if status:
+        _kda._check(status)
+    return CachePlan(cu_seqlens, kv_lens, slot_map, positions)
 
 
 def kda_cache_append(k, v, slot_map, k_cache, v_cache, stream=None):
     """k_cache[slot] = k[t], v_cache[slot] = v[t] with slot = slot_map[t] (-1 skips the token).
     k, v [T, H_kv, d]; slot_map int32 [T]; caches [n_blocks, H_kv, block_size, d]."""
-    shape, kp, ks, dev, ix, code = _first(k, "k")
+    shape, dtype, code, dev, ix, kp, ks = _first(k, "k")
     T, H, d = shape
-    vp, vs = _tokens(v, "v", k.dtype, shape, dev)
+    vp, vs = _tokens(v, "v", dtype, shape, dev, ix)
     sp = _dev(slot_map, "slot_map", _I32, (T,), dev, ix)
-    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, k.dtype, H, d, dev, ix)
-    handle = _current_stream(dev) if stream is None else _kda._stream_handle(stream)
-    _kda._check(_kda.load().kda_cache_append(T, H, d, code, kp, ks, vp, vs, sp, kc, vc, n_blocks, bs, handle))
+    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, dtype, H, d, dev, ix)
+    handle = _current_stream(ix) if stream is None else _kda._stream_handle(stream)
+    status = _kda.load().kda_cache_append(T, H, d, code, kp, ks, vp, vs, sp, kc, vc, n_blocks, bs, handle)
+    if status:
+        _kda._check(status)
 
 
 def kda_attn_prefill(args: AttnPrefillArgs, stream=None):
     _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(args), _kda._stream_handle(stream)))
 
 
-def _outputs(q, shape, dev, ix, o, lse, want_lse):
+def _outputs(dtype, shape, dev, ix, o, lse, want_lse):
     """(o, its address and stride, lse, its address), allocated where they are not given."""
     T, H, d = shape
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
+        o = _empty(shape, dtype=dtype, device=dev)
         op, os_ = o.data_ptr(), H * d
     else:
-        op, os_ = _tokens(o, "o", q.dtype, shape, dev)
+        op, os_ = _tokens(o, "o", dtype, shape, dev, ix)
     if lse is not None:
         return o, op, os_, lse, _dev(lse, "lse", _F32, (T, H), dev, ix)
     if not want_lse:
         return o, op, os_, None, None
-    lse = torch.empty((T, H), dtype=_F32, device=dev)
+    lse = _empty((T, H), dtype=_F32, device=dev)
     return o, op, os_, lse, lse.data_ptr()
-
-
-def _scale(scale, d):
-    return d ** -0.5 if scale is None else float(scale)
 
 
 def attn_prefill(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse=False, stream=None):
     """Causal attention over packed prompts (``kda_attn_prefill``): q [T, H, d]; k, v
     [T, H_kv, d]; cu_seqlens int32 [n + 1].  scale defaults to d^-0.5; o and lse are allocated
     unless given (tokens past cu_seqlens[n] are left unwritten).  Returns (o, lse or None)."""
-    shape, qp, qs, dev, ix, code = _first(q, "q")
+    if _elsewhere(stream, q):
+        with _on(stream, q):
+            return attn_prefill(q, k, v, cu_seqlens, scale=scale, o=o, lse=lse, want_lse=want_lse)
+    shape, dtype, code, dev, ix, qp, qs = _first(q, "q")
     T, H, d = shape
-    H_kv = _shape(k, "k", 3)[1]
-    kp, ks = _tokens(k, "k", q.dtype, (T, H_kv, d), dev)
-    vp, vs = _tokens(v, "v", q.dtype, (T, H_kv, d), dev)
+    kv = (T, _shape(k, "k", 3)[1], d)
+    kp, ks = _tokens(k, "k", dtype, kv, dev, ix)
+    vp, vs = _tokens(v, "v", dtype, kv, dev, ix)
     entries, = _shape(cu_seqlens, "cu_seqlens", 1)
     cu = _dev(cu_seqlens, "cu_seqlens", _I32, (entries,), dev, ix)
-
-    def call(handle):
-        out, op, os_, z, zp = _outputs(q, shape, dev, ix, o, lse, want_lse)
-        a = AttnPrefillArgs(entries - 1, H, H_kv, d, code, _scale(scale, d), T, qs, ks, vs, os_, qp, kp, vp, op, zp, cu)
-        _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(a), handle))
-        return out, z
-    return _on_stream(stream, dev, call)
+    o, op, os_, lse, zp = _outputs(dtype, shape, dev, ix, o, lse, want_lse)
+    a = AttnPrefillArgs(entries - 1, H, kv[1], d, code, d ** -0.5 if scale is None else scale, T, qs, ks, vs, os_, qp, kp, vp,
+                        op, zp, cu)
+    status = _kda.load().kda_attn_prefill(_byref(a), _current_stream(ix))
+    if status:
+        _kda._check(status)
+    return o, lse
 
 
 def attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *, scale=None, o=None, lse=None,
@@ -257,25 +271,28 @@ def attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *,
     positions, the last of which are its queries.  caches [n_blocks, H_kv, block_size, d];
     block_table int32 [n, stride]; kv_lens int32 [n]; cu_seqlens int32 [n + 1].  Returns (o, lse
     or None)."""
-    shape, qp, qs, dev, ix, code = _first(q, "q")
+    if _elsewhere(stream, q):
+        with _on(stream, q):
+            return attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=scale, o=o, lse=lse,
+                                      want_lse=want_lse)
+    shape, dtype, code, dev, ix, qp, qs = _first(q, "q")
     T, H, d = shape
     H_kv = _shape(k_cache, "k_cache", 4)[1]
     n, stride = _shape(block_table, "block_table", 2)
-    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, q.dtype, H_kv, d, dev, ix)
+    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, dtype, H_kv, d, dev, ix)
     table = _dev(block_table, "block_table", _I32, (n, stride), dev, ix)
     kv = _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix)
     cu = _dev(cu_seqlens, "cu_seqlens", _I32, (n + 1,), dev, ix)
     if n and not stride:
         raise ValueError("block_table must have at least one column")
-
-    def call(handle):
-        out, op, os_, z, zp = _outputs(q, shape, dev, ix, o, lse, want_lse)
-        if n and T:
-            a = AttnPrefillArgs(n, H, H_kv, d, code, _scale(scale, d), T, qs, 0, 0, os_, qp, None, None, op, zp, cu, kc, vc,
-                                table, kv, n_blocks, bs, stride)
-            _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(a), handle))
-        return out, z
-    return _on_stream(stream, dev, call)
+    o, op, os_, lse, zp = _outputs(dtype, shape, dev, ix, o, lse, want_lse)
+    if n and T:
+        a = AttnPrefillArgs(n, H, H_kv, d, code, d ** -0.5 if scale is None else scale, T, qs, 0, 0, os_, qp, None, None, op,
+                            zp, cu, kc, vc, table, kv, n_blocks, bs, stride)
+        status = _kda.load().kda_attn_prefill(_byref(a), _current_stream(ix))
+        if status:
+            _kda._check(status)
+    return o, lse
 
 
 def kda_attn_decode_workspace_size(args: AttnDecodeArgs) -> int:
@@ -295,11 +312,16 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_lens, *, group_start=None, 
     Returns (o, lse or None)."""
     if (group_start is None) != (prefix_lens is None):
         raise ValueError("group_start and prefix_lens come together")
-    shape, qp, qs, dev, ix, code = _first(q, "q")
+    if _elsewhere(stream, q):
+        with _on(stream, q):
+            return attn_decode(q, k_cache, v_cache, block_table, kv_lens, group_start=group_start,
+                               prefix_lens=prefix_lens, scale=scale, o=o, lse=lse, want_lse=want_lse,
+                               workspace=workspace)
+    shape, dtype, code, dev, ix, qp, qs = _first(q, "q")
     n, H, d = shape
     H_kv = _shape(k_cache, "k_cache", 4)[1]
     stride = _shape(block_table, "block_table", 2)[1]
-    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, q.dtype, H_kv, d, dev, ix)
+    kc, vc, n_blocks, bs = _cache(k_cache, v_cache, dtype, H_kv, d, dev, ix)
     table = _dev(block_table, "block_table", _I32, (n, stride), dev, ix)
     kv = _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix)
     groups, start, prefix = 0, None, None
@@ -307,18 +329,19 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_lens, *, group_start=None, 
         groups, = _shape(prefix_lens, "prefix_lens", 1)
         start = _dev(group_start, "group_start", _I32, (groups + 1,), dev, ix)
         prefix = _dev(prefix_lens, "prefix_lens", _I32, (groups,), dev, ix)
-
-    def call(handle):
-        out, op, os_, z, zp = _outputs(q, shape, dev, ix, o, lse, want_lse)
-        a = AttnDecodeArgs(n, H, H_kv, d, code, _scale(scale, d), qs, os_, qp, op, zp, kc, vc, table, kv, n_blocks, bs,
-                           stride, groups, 0, start, prefix)
-        lib = _kda.load()
-        need, ws = lib.kda_attn_decode_workspace_size(ctypes.byref(a)), workspace
-        if need:
-            if ws is None or ws.numel() * ws.element_size() < need:
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            a.workspace = _kda._dev(ws, "workspace", device=dev)
-            a.workspace_bytes = ws.numel() * ws.element_size()
-        _kda._check(lib.kda_attn_decode(ctypes.byref(a), handle))
-        return out, z
-    return _on_stream(stream, dev, call)
+    o, op, os_, lse, zp = _outputs(dtype, shape, dev, ix, o, lse, want_lse)
+    a = AttnDecodeArgs(n, H, H_kv, d, code, d ** -0.5 if scale is None else scale, qs, os_, qp, op, zp, kc, vc, table, kv,
+                       n_blocks, bs, stride, groups, 0, start, prefix)
+    lib = _kda.load()
+    need = lib.kda_attn_decode_workspace_size(_byref(a))
+    if need:
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = _empty(need, dtype=_U8, device=dev)
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+        else:
+            a.workspace = _kda._dev(workspace, "workspace", device=dev)
+            a.workspace_bytes = workspace.numel() * workspace.element_size()
+    status = lib.kda_attn_decode(_byref(a), _current_stream(ix))
+    if status:
+        _kda._check(status)
+    return o, lse

@@ -91,7 +91,16 @@ kda_status_t check_scale(float scale) {
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-int decode_rows(int32_t dtype) { return dtype == KDA_BF16 ? kda::kDecodeRowsBf16 : kda::kDecodeRowsF32; }
+// Workers of the suffix kernel: all, or as many as the longest sequences that the
+// table can name would give work.
+int decode_pieces(const kda_attn_decode_args& a) {
+    const int64_t G = a.n_heads / a.n_kv_heads, rows = kda::decode_rows(a.dtype, (int)G);
+    const int64_t tiles = ((int64_t)a.table_stride * a.block_size + kda::decode_tile(a.dtype, a.d) - 1) / kda::decode_tile(a.dtype, a.d);
+    const int64_t units = (int64_t)a.n_seqs * a.n_kv_heads * ((G + rows - 1) / rows);
+    if (tiles >= kda::kDecodePieces * kda::kDecodeLeastTiles) return kda::kDecodePieces;
+    const int64_t pieces = (units * tiles / kda::kDecodeLeastTiles + kda::kDecodeWarps) / kda::kDecodeWarps * kda::kDecodeWarps;
+    return (int)(pieces < kda::kDecodePieces ? pieces : kda::kDecodePieces);
+}
 
 // Blocks of keys that a shared prefix is cut into: bf16 enough for a thread block (256
 // rows) on each of 152 SMs, fp32 enough for one (64 rows) on every second one, whose
@@ -118,12 +127,12 @@ DecodeSpace decode_space(const kda_attn_decode_args& a) {
         return r;
     };
     const size_t rows = (size_t)a.n_seqs * a.n_heads * prefix_splits(a);
-    const size_t parts = (size_t)2 * kda::kDecodePieces * decode_rows(a.dtype);
+    const size_t parts = (size_t)2 * decode_pieces(a) * kda::decode_rows(a.dtype, a.n_heads / a.n_kv_heads);
     s.pre_o = take(rows * a.d * sizeof(float));
     s.pre_ml = take(rows * sizeof(float2));
     s.part_o = take(parts * a.d * sizeof(float));
     s.part_ml = take(parts * sizeof(float2));
-    s.open = take((size_t)kda::kDecodePieces * sizeof(int4));
+    s.open = take((size_t)decode_pieces(a) * sizeof(int4));
     s.info = take(a.n_groups > 0 ? (size_t)a.n_seqs * sizeof(int2) : 0);
     s.bytes = at;
     return s;
@@ -133,6 +142,8 @@ kda_status_t check_decode_sizes(const kda_attn_decode_args& a) {
     KDA_TRY(check_heads(a.n_heads, a.n_kv_heads, a.d, a.dtype));
     KDA_TRY(check_seqs(a.n_seqs, "n_seqs"));
     KDA_TRY(check_seqs(a.n_groups, "n_groups"));
+    KDA_TRY(check_block_size(a.block_size));
+    KDA_TRY(check_table(a.table_stride, a.block_size));
     if ((int64_t)a.n_seqs * a.n_heads > (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "n_seqs * n_heads too large");
     return KDA_OK;
 }
@@ -247,8 +258,6 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     KDA_TRY(check_decode_sizes(a));
     KDA_TRY(check_scale(a.scale));
     if (a.reserved0 != 0) return fail(KDA_ERR_INVALID_ARG, "reserved0 must be 0");
-    KDA_TRY(check_block_size(a.block_size));
-    KDA_TRY(check_table(a.table_stride, a.block_size));
     KDA_TRY(check_cache_size(a.n_blocks, a.block_size, a.n_kv_heads));
     KDA_TRY(check_stride(a.q_stride, a.n_heads, a.d, a.dtype, "q_stride"));
     KDA_TRY(check_stride(a.o_stride, a.n_heads, a.d, a.dtype, "o_stride"));
@@ -272,7 +281,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     kda::AttnDecodeLaunch p{};
     p.a = a;
-    p.n_pieces = kda::kDecodePieces;
+    p.n_pieces = decode_pieces(a);
     p.n_split = prefix_splits(a);
     p.prefix_tile = a.dtype == KDA_BF16 ? kda::kTileKeysBf16 : kda::kTileKeysF32;
     p.pre_o = reinterpret_cast<float*>(ws + sp.pre_o);

@@ -127,7 +127,14 @@ struct AttnDecodeLaunch {
     int4* open;                   // [n_pieces] the unit that begins in a piece and goes on
     int2* info;                   // [n_seqs] (shared positions, all positions), where there are groups
 };
-constexpr int kDecodeRowsF32 = 8, kDecodeRowsBf16 = 16;   // at most: query heads of one unit
+// Query heads of one unit.  fp32: up to four heads of a key/value head cost half of
+// eight in the kernel's arithmetic, which is what bounds it beyond two.
+constexpr int kDecodeRowsBf16 = 16;
+constexpr int decode_rows(int dtype, int G) { return dtype == KDA_BF16 ? kDecodeRowsBf16 : G <= 4 ? 4 : 8; }
+// Keys of a tile, and tiles of the shortest piece: a shorter one costs more in the
+// join than it saves.
+constexpr int decode_tile(int dtype, int d) { return dtype == KDA_BF16 ? 16 : 1024 / d; }
+constexpr int kDecodeLeastTiles = 4;
 constexpr int kDecodeWarps = 8, kDecodePieces = kDecodeWarps * 152;   // workers: eight warps on each of 152 SMs
 cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s);   // p.info, where there are groups
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s);   // fp32

@@ -55,7 +55,6 @@ __global__ void __launch_bounds__(kInfoThreads) decode_info_kernel(const __grid_
 
 constexpr int kWarps = kDecodeWarps, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kLeastTiles = 4;           // of a piece
 // The maximum that weights refer to is the first tile's, and is moved when a weight
 // passes kMostWeight; kLeastMaximum until a row has seen a score above -inf.
 constexpr float kMostWeight = 1024.f, kLeastMaximum = -1e30f;
@@ -64,7 +63,7 @@ constexpr float kMostWeight = 1024.f, kLeastMaximum = -1e30f;
 // piece ^ (j * lanes per key) of its row, so that eight lanes of a score (two or four
 // to a key) and the lanes of a value row read distinct banks.
 template <int D, int R> struct DecodeSmem {
-    static constexpr int kKeys = 1024 / D, kLanesPerKey = D / 32;
+    static constexpr int kKeys = decode_tile(KDA_FP32, D), kLanesPerKey = D / 32;
     float ring[kWarps][kStages][2][kKeys * D];
     float q[kWarps][R * D];
     float w[kWarps][kKeys * R];          // weights, key-major
@@ -91,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + R - 1) / R;
     __shared__ PieceStart at_[kWarps];
-    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kLeastTiles, at_);
+    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kDecodeLeastTiles, at_);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
     if (piece >= line.pieces) {
@@ -293,10 +292,8 @@ cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s) {
                              s, p);
 }
 
-// Up to four query heads of a key/value head cost half of eight in the kernel's
-// arithmetic, which is what bounds it beyond two.
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s) {
-    const bool few = p.a.n_heads / p.a.n_kv_heads <= 4;
+    const bool few = decode_rows(KDA_FP32, p.a.n_heads / p.a.n_kv_heads) == 4;
     if (p.a.d == 128) return few ? launch_t<128, 4>(p, s) : launch_t<128, 8>(p, s);
     return few ? launch_t<64, 4>(p, s) : launch_t<64, 8>(p, s);
 }

@@ -191,8 +191,9 @@ typedef struct kda_attn_decode_args {
     size_t workspace_bytes;
 } kda_attn_decode_args;
 
-/* Bytes of workspace for these sizes (only n_seqs, n_heads, n_kv_heads, d,
- * dtype and n_groups are read); 0 for an empty batch or invalid sizes. */
+/* Bytes of workspace for these sizes (only n_seqs, n_heads, n_kv_heads, d, dtype,
+ * n_groups, block_size and table_stride are read); 0 for an empty batch or invalid
+ * sizes. */
 size_t kda_attn_decode_workspace_size(const kda_attn_decode_args *args);
 
 kda_status_t kda_attn_decode(const kda_attn_decode_args *args, void *stream);

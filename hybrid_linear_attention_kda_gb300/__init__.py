@@ -413,7 +413,7 @@ def prefill(q, k, v, alpha, beta, cu_seqlens, total_tokens=None, *, start_pos=No
 
 _ATTENTION = ("KDA_DEV_NO_BLOCKS", "KDA_DEV_BAD_GROUP", "CachePlanArgs", "AttnPrefillArgs", "AttnDecodeArgs", "CachePlan",
               "kda_cache_plan", "kda_cache_append", "kda_attn_prefill", "kda_attn_decode",
-              "kda_attn_decode_workspace_size", "cache_plan", "attn_prefill", "attn_prefill_paged", "attn_decode")
+              "kda_attn_prefill_workspace_size", "kda_attn_decode_workspace_size", "cache_plan", "attn_prefill", "attn_prefill_paged", "attn_decode")
 
 
 def __getattr__(name):

@@ -38,6 +38,7 @@ class AttnPrefillArgs(ctypes.Structure):
         ("lse", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p), ("k_cache", ctypes.c_void_p),
         ("v_cache", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
         ("n_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -68,6 +69,8 @@ def declare(lib):
     lib.kda_cache_append.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i64, i32, vp]
     lib.kda_attn_prefill.restype = ctypes.c_int
     lib.kda_attn_prefill.argtypes = [P(AttnPrefillArgs), vp]
+    lib.kda_attn_prefill_workspace_size.restype = ctypes.c_size_t
+    lib.kda_attn_prefill_workspace_size.argtypes = [P(AttnPrefillArgs)]
     lib.kda_attn_decode_workspace_size.restype = ctypes.c_size_t
     lib.kda_attn_decode_workspace_size.argtypes = [P(AttnDecodeArgs)]
     lib.kda_attn_decode.restype = ctypes.c_int
@@ -226,6 +229,17 @@ def kda_attn_prefill(args: AttnPrefillArgs, stream=None):
     _kda._check(_kda.load().kda_attn_prefill(ctypes.byref(args), _kda._stream_handle(stream)))
 
 
+def _workspace(a, workspace, need, dev):
+    """Give ``a`` the workspace, or a new one where it is missing or too small; the caller's
+    frame keeps it until the launch."""
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        a._held = workspace = _empty(need, dtype=_U8, device=dev)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+    else:
+        a.workspace = _kda._dev(workspace, "workspace", device=dev)
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+
+
 def _outputs(dtype, shape, dev, ix, o, lse, want_lse):
     """(o, its address and stride, lse, its address), allocated where they are not given."""
     T, H, d = shape
@@ -242,13 +256,28 @@ def _outputs(dtype, shape, dev, ix, o, lse, want_lse):
     return o, op, os_, lse, lse.data_ptr()
 
 
-def attn_prefill(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse=False, stream=None):
+def kda_attn_prefill_workspace_size(args: AttnPrefillArgs) -> int:
+    return int(_kda.load().kda_attn_prefill_workspace_size(_byref(args)))
+
+
+def _prefill(a, workspace, dev, ix):
+    lib = _kda.load()
+    need = lib.kda_attn_prefill_workspace_size(_byref(a))
+    if need:
+        _workspace(a, workspace, need, dev)
+    status = lib.kda_attn_prefill(_byref(a), _current_stream(ix))
+    if status:
+        _kda._check(status)
+
+
+def attn_prefill(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse=False, workspace=None, stream=None):
     """Causal attention over packed prompts (``kda_attn_prefill``): q [T, H, d]; k, v
     [T, H_kv, d]; cu_seqlens int32 [n + 1].  scale defaults to d^-0.5; o and lse are allocated
-    unless given (tokens past cu_seqlens[n] are left unwritten).  Returns (o, lse or None)."""
+    unless given (tokens past cu_seqlens[n] are left unwritten), and so is the workspace
+    (uint8), where one is of use.  Returns (o, lse or None)."""
     if _elsewhere(stream, q):
         with _on(stream, q):
-            return attn_prefill(q, k, v, cu_seqlens, scale=scale, o=o, lse=lse, want_lse=want_lse)
+            return attn_prefill(q, k, v, cu_seqlens, scale=scale, o=o, lse=lse, want_lse=want_lse, workspace=workspace)
     shape, dtype, code, dev, ix, qp, qs = _first(q, "q")
     T, H, d = shape
     kv = (T, _shape(k, "k", 3)[1], d)
@@ -259,14 +288,12 @@ def attn_prefill(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse=
     o, op, os_, lse, zp = _outputs(dtype, shape, dev, ix, o, lse, want_lse)
     a = AttnPrefillArgs(entries - 1, H, kv[1], d, code, d ** -0.5 if scale is None else scale, T, qs, ks, vs, os_, qp, kp, vp,
                         op, zp, cu)
-    status = _kda.load().kda_attn_prefill(_byref(a), _current_stream(ix))
-    if status:
-        _kda._check(status)
+    _prefill(a, workspace, dev, ix)
     return o, lse
 
 
 def attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *, scale=None, o=None, lse=None,
-                       want_lse=False, stream=None):
+                       want_lse=False, workspace=None, stream=None):
     """``attn_prefill`` with all keys and values in the paged cache: sequence s holds kv_lens[s]
     positions, the last of which are its queries.  caches [n_blocks, H_kv, block_size, d];
     block_table int32 [n, stride]; kv_lens int32 [n]; cu_seqlens int32 [n + 1].  Returns (o, lse
@@ -274,7 +301,7 @@ def attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *,
     if _elsewhere(stream, q):
         with _on(stream, q):
             return attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale=scale, o=o, lse=lse,
-                                      want_lse=want_lse)
+                                      want_lse=want_lse, workspace=workspace)
     shape, dtype, code, dev, ix, qp, qs = _first(q, "q")
     T, H, d = shape
     H_kv = _shape(k_cache, "k_cache", 4)[1]
@@ -289,9 +316,7 @@ def attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *,
     if n and T:
         a = AttnPrefillArgs(n, H, H_kv, d, code, d ** -0.5 if scale is None else scale, T, qs, 0, 0, os_, qp, None, None, op,
                             zp, cu, kc, vc, table, kv, n_blocks, bs, stride)
-        status = _kda.load().kda_attn_prefill(_byref(a), _current_stream(ix))
-        if status:
-            _kda._check(status)
+        _prefill(a, workspace, dev, ix)
     return o, lse
 
 
@@ -335,12 +360,7 @@ def attn_decode(q, k_cache, v_cache, block_table, kv_lens, *, group_start=None, 
     lib = _kda.load()
     need = lib.kda_attn_decode_workspace_size(_byref(a))
     if need:
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = _empty(need, dtype=_U8, device=dev)
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), need
-        else:
-            a.workspace = _kda._dev(workspace, "workspace", device=dev)
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
+        _workspace(a, workspace, need, dev)
     status = lib.kda_attn_decode(_byref(a), _current_stream(ix))
     if status:
         _kda._check(status)

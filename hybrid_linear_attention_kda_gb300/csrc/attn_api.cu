@@ -114,6 +114,23 @@ int prefix_splits(const kda_attn_decode_args& a) {
     return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 
+// Blocks of keys that a prompt's tiles are cut into: several where the row tiles (256
+// rows in bf16, 64 in fp32) would leave most SMs idle and the keys are many, with at
+// least 512 keys each.
+int prompt_splits(const kda_attn_prefill_args& a) {
+    if (a.n_seqs == 0 || a.total_tokens == 0) return 1;
+    const bool bf16 = a.dtype == KDA_BF16;
+    const int64_t G = a.n_heads / a.n_kv_heads;
+    const int64_t items = (a.total_tokens * G / (bf16 ? 256 : 64) + a.n_seqs) * a.n_kv_heads;
+    const int64_t keys = a.block_table ? (int64_t)a.table_stride * a.block_size : a.total_tokens;
+    const int64_t n = 152 / items, most = keys / 512;
+    const int64_t r = n < most ? n : most;
+    return (int)(r < 2 ? 1 : r > 32 ? 32 : r);
+}
+
+size_t prompt_part_bytes(const kda_attn_prefill_args& a, int n) { return round_up((size_t)n * a.total_tokens * a.n_heads * a.d * sizeof(float)); }
+size_t prompt_ml_bytes(const kda_attn_prefill_args& a, int n) { return round_up((size_t)n * a.total_tokens * a.n_heads * sizeof(float2)); }
+
 struct DecodeSpace {
     size_t pre_o, pre_ml, part_o, part_ml, open, info, bytes;
 };
@@ -145,6 +162,27 @@ kda_status_t check_decode_sizes(const kda_attn_decode_args& a) {
     KDA_TRY(check_block_size(a.block_size));
     KDA_TRY(check_table(a.table_stride, a.block_size));
     if ((int64_t)a.n_seqs * a.n_heads > (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "n_seqs * n_heads too large");
+    return KDA_OK;
+}
+
+kda_status_t check_prefill_sizes(const kda_attn_prefill_args& a) {
+    KDA_TRY(check_heads(a.n_heads, a.n_kv_heads, a.d, a.dtype));
+    KDA_TRY(check_seqs(a.n_seqs, "n_seqs"));
+    KDA_TRY(check_scale(a.scale));
+    if (a.total_tokens < 0 || a.total_tokens > (int64_t)INT32_MAX)
+        return fail(KDA_ERR_INVALID_ARG, "total_tokens %lld outside [0, 2^31)", (long long)a.total_tokens);
+    KDA_TRY(check_stride(a.q_stride, a.n_heads, a.d, a.dtype, "q_stride"));
+    KDA_TRY(check_stride(a.o_stride, a.n_heads, a.d, a.dtype, "o_stride"));
+    if (a.block_table) {
+        KDA_TRY(check_block_size(a.block_size));
+        KDA_TRY(check_table(a.table_stride, a.block_size));
+        KDA_TRY(check_cache_size(a.n_blocks, a.block_size, a.n_kv_heads));
+    } else {
+        KDA_TRY(check_stride(a.k_stride, a.n_kv_heads, a.d, a.dtype, "k_stride"));
+        KDA_TRY(check_stride(a.v_stride, a.n_kv_heads, a.d, a.dtype, "v_stride"));
+    }
+    // one thread block for each tile of at least one token
+    if ((a.total_tokens + a.n_seqs) * 2 > (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "total_tokens + n_seqs too large");
     return KDA_OK;
 }
 
@@ -207,26 +245,16 @@ kda_status_t kda_cache_append(int64_t n_tokens, int32_t n_kv_heads, int32_t d, i
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache append launch");
 }
 
+size_t kda_attn_prefill_workspace_size(const kda_attn_prefill_args* args) {
+    if (!args || check_prefill_sizes(*args) != KDA_OK) return 0;
+    const int n = prompt_splits(*args);
+    return n > 1 ? prompt_part_bytes(*args, n) + prompt_ml_bytes(*args, n) : 0;
+}
+
 kda_status_t kda_attn_prefill(const kda_attn_prefill_args* args, void* stream) {
     if (!args) return fail(KDA_ERR_INVALID_ARG, "args is NULL");
     const kda_attn_prefill_args& a = *args;
-    KDA_TRY(check_heads(a.n_heads, a.n_kv_heads, a.d, a.dtype));
-    KDA_TRY(check_seqs(a.n_seqs, "n_seqs"));
-    KDA_TRY(check_scale(a.scale));
-    if (a.total_tokens < 0 || a.total_tokens > (int64_t)INT32_MAX)
-        return fail(KDA_ERR_INVALID_ARG, "total_tokens %lld outside [0, 2^31)", (long long)a.total_tokens);
-    KDA_TRY(check_stride(a.q_stride, a.n_heads, a.d, a.dtype, "q_stride"));
-    KDA_TRY(check_stride(a.o_stride, a.n_heads, a.d, a.dtype, "o_stride"));
-    if (a.block_table) {
-        KDA_TRY(check_block_size(a.block_size));
-        KDA_TRY(check_table(a.table_stride, a.block_size));
-        KDA_TRY(check_cache_size(a.n_blocks, a.block_size, a.n_kv_heads));
-    } else {
-        KDA_TRY(check_stride(a.k_stride, a.n_kv_heads, a.d, a.dtype, "k_stride"));
-        KDA_TRY(check_stride(a.v_stride, a.n_kv_heads, a.d, a.dtype, "v_stride"));
-    }
-    // one thread block for each tile of at least one token
-    if ((a.total_tokens + a.n_seqs) * 2 > (int64_t)INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "total_tokens + n_seqs too large");
+    KDA_TRY(check_prefill_sizes(a));
     if (a.n_seqs == 0 || a.total_tokens == 0) return KDA_OK;
     KDA_TRY(check_ptr(a.q, "q"));
     KDA_TRY(check_ptr(a.o, "o"));
@@ -241,10 +269,22 @@ kda_status_t kda_attn_prefill(const kda_attn_prefill_args* args, void* stream) {
         KDA_TRY(check_ptr(a.k, "k"));
         KDA_TRY(check_ptr(a.v, "v"));
     }
-    kda::AttnTileLaunch p{a, nullptr, nullptr, 0, nullptr, nullptr};
+    kda::AttnTileLaunch p{a, nullptr, nullptr, 1, nullptr, nullptr};
     KDA_TRY(kda::device_status_word(&p.status));
-    const cudaError_t e = kda::launch_attn_tile(p, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "prompt attention launch");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int n = prompt_splits(a);
+    if (n > 1 && a.workspace && a.workspace_bytes >= prompt_part_bytes(a, n) + prompt_ml_bytes(a, n)) {
+        if (reinterpret_cast<uintptr_t>(a.workspace) & 255u) return fail(KDA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+        p.n_split = n;
+        p.part_o = static_cast<float*>(a.workspace);
+        p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + prompt_part_bytes(a, n));
+        const cudaError_t e = cudaMemsetAsync(p.part_ml, kda::kUnwritten, (size_t)a.total_tokens * a.n_heads * sizeof(float2), s);
+        if (e != cudaSuccess) return cuda_fail(e, "prompt attention workspace");
+    }
+    cudaError_t e = kda::launch_attn_tile(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+    if (p.n_split > 1) e = kda::launch_prompt_join(p, s);
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "prompt attention join launch");
 }
 
 size_t kda_attn_decode_workspace_size(const kda_attn_decode_args* args) {

@@ -97,9 +97,9 @@ __device__ RowTile find_tile(const int32_t* cu, int32_t n_seqs, int64_t total_to
 struct AttnTileLaunch {
     kda_attn_prefill_args a;      // q, strides, caches, ...; cu_seqlens = group_start for a shared prefix
     uint32_t* status;
-    // shared prefixes only: keys 0 .. prefix_lens[g] of the group's first row, split over n_split blocks of keys,
-    // partial results to part_o [n_split, total_tokens, H, d] and part_ml [n_split, total_tokens, H] (m, l)
-    const int32_t* prefix_lens;
+    const int32_t* prefix_lens;   // shared prefixes only: keys 0 .. prefix_lens[g] of the group's first row
+    // Shared prefixes, and prompts where n_split > 1: the keys are cut into n_split blocks, with partial results in
+    // part_o [n_split, total_tokens, H, d] (unnormalised) and part_ml [n_split, total_tokens, H] (m, l).
     int32_t n_split;
     float* part_o;
     float2* part_ml;
@@ -139,6 +139,11 @@ constexpr int kDecodeWarps = 8, kDecodePieces = kDecodeWarps * 152;   // workers
 cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s);   // p.info, where there are groups
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s);   // fp32
 cudaError_t launch_decode_mma(const AttnDecodeLaunch& p, cudaStream_t s);    // bf16
+
+// Joins a split prompt's partial results into o and lse.  Rows that no sequence wrote are those whose part_ml
+// still holds the bytes kUnwritten.
+constexpr int kUnwritten = 0xFF;
+cudaError_t launch_prompt_join(const AttnTileLaunch& p, cudaStream_t s);
 
 struct CachePlanLaunch {
     kda_cache_plan_args a;

@@ -38,7 +38,7 @@ template <int D> constexpr int kGroups = D == 64 ? 4 : 2;
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 
-template <int D, int MODE, int GROUPS>
+template <int D, int MODE, int GROUPS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_constant__ AttnTileLaunch p, int32_t Gp, int32_t chunks) {
     constexpr int kRows = rows_of(GROUPS), kGroupThreads = kThreads / GROUPS;
     griddep_wait();
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
     const int hk = (int)(blockIdx.y / chunks), hc = (int)(blockIdx.y % chunks);
     const int head0 = hk * G + hc * Gp, gn = min(Gp, G - hc * Gp);
     const int bt = kRows / Gp;                       // tokens of a tile
-    const int64_t idx = MODE == kPrefix ? blockIdx.x / p.n_split : blockIdx.x;
-    const int split = MODE == kPrefix ? (int)(blockIdx.x % p.n_split) : 0;
+    const int64_t idx = SPLIT ? blockIdx.x / p.n_split : blockIdx.x;
+    const int split = SPLIT ? (int)(blockIdx.x % p.n_split) : 0;
     const bool report = MODE != kPrefix && blockIdx.x == 0 && blockIdx.y == 0;
     const RowTile rt = find_tile<kThreads>(a.cu_seqlens, a.n_seqs, a.total_tokens, bt, idx, report,
                                            KDA_DEV_BAD_SEQLENS, p.status);
@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
         first = K;
     }
     int64_t k_lo = 0, k_hi = min(K, first + rt.t0 + nt);
-    if (MODE == kPrefix) {
+    if (SPLIT) {
+        if (MODE != kPrefix) K = max((int64_t)0, k_hi);      // the tile's keys
         const int64_t per = ((K + kKeys - 1) / kKeys + p.n_split - 1) / p.n_split * kKeys;
         k_lo = min(K, split * per);
         k_hi = min(K, k_lo + per);
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
         if (t >= nt || g >= gn) continue;
         const int64_t row = rt.row0 + rt.t0 + t;
         const int head = head0 + g;
-        if (MODE == kPrefix) {
+        if (SPLIT) {
             const int64_t at = ((int64_t)split * a.total_tokens + row) * a.n_heads + head;
 #pragma unroll
             for (int c = 0; c < OC; ++c) store4(p.part_o + at * D + 4 * tx + 64 * c, o[r][c]);
@@ -285,38 +286,40 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
 }
 
 // Blocks of a launch with the given groups, at most.
-int64_t blocks_of(const AttnTileLaunch& p, int groups, bool prefix, int* Gp, int* chunks) {
+int64_t blocks_of(const AttnTileLaunch& p, int groups, bool split, int* Gp, int* chunks) {
     const int G = p.a.n_heads / p.a.n_kv_heads, rows = rows_of(groups);
     *Gp = G < rows ? G : rows;
     *chunks = (G + *Gp - 1) / *Gp;
-    return (p.a.total_tokens / (rows / *Gp) + p.a.n_seqs) * (prefix ? p.n_split : 1);
+    return (p.a.total_tokens / (rows / *Gp) + p.a.n_seqs) * (split ? p.n_split : 1);
 }
 
-template <int D, int MODE, int GROUPS>
+template <int D, int MODE, int GROUPS, bool SPLIT>
 cudaError_t launch_g(const AttnTileLaunch& p, cudaStream_t s) {
     int32_t Gp, chunks;
-    const int64_t tiles = blocks_of(p, GROUPS, MODE == kPrefix, &Gp, &chunks);
+    const int64_t tiles = blocks_of(p, GROUPS, SPLIT, &Gp, &chunks);
     if (tiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<D, MODE, GROUPS>,
+    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<D, MODE, GROUPS, SPLIT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>(GROUPS));
     if (e != cudaSuccess) return e;
     note_launch();
-    return launch_overlapped(attn_simt_kernel<D, MODE, GROUPS>, dim3((unsigned)tiles, (unsigned)(p.a.n_kv_heads * chunks)),
+    return launch_overlapped(attn_simt_kernel<D, MODE, GROUPS, SPLIT>, dim3((unsigned)tiles, (unsigned)(p.a.n_kv_heads * chunks)),
                              dim3(kThreads), smem_bytes<D>(GROUPS), s, p, Gp, chunks);
 }
 
 // Several groups where the blocks of one group would not give every SM one.
-template <int D, int MODE>
+template <int D, int MODE, bool SPLIT>
 cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
     int Gp, chunks;
-    const int64_t tiles = blocks_of(p, 1, MODE == kPrefix, &Gp, &chunks);
-    return tiles * p.a.n_kv_heads * chunks <= 152 ? launch_g<D, MODE, kGroups<D>>(p, s) : launch_g<D, MODE, 1>(p, s);
+    const int64_t tiles = blocks_of(p, 1, SPLIT, &Gp, &chunks);
+    return tiles * p.a.n_kv_heads * chunks <= 152 ? launch_g<D, MODE, kGroups<D>, SPLIT>(p, s)
+                                                    : launch_g<D, MODE, 1, SPLIT>(p, s);
 }
 
 template <int D>
 cudaError_t launch_d(const AttnTileLaunch& p, cudaStream_t s) {
-    if (p.prefix_lens) return launch_t<D, kPrefix>(p, s);
-    return p.a.block_table ? launch_t<D, kPaged>(p, s) : launch_t<D, kPacked>(p, s);
+    if (p.prefix_lens) return launch_t<D, kPrefix, true>(p, s);
+    if (p.n_split > 1) return p.a.block_table ? launch_t<D, kPaged, true>(p, s) : launch_t<D, kPacked, true>(p, s);
+    return p.a.block_table ? launch_t<D, kPaged, false>(p, s) : launch_t<D, kPacked, false>(p, s);
 }
 
 }  // namespace

@@ -244,8 +244,9 @@ struct Place {
 
 // Fills `it` for grid index `block`; false when that block has nothing to do.  One
 // warp; later indexes mostly lie further on, so the search goes on where the last one
-// ended.  Tiles of one sequence come last first: the later ones see more keys.
-template <int MODE>
+// ended.  Tiles of one sequence come last first: the later ones see more keys.  SPLIT:
+// the keys of a tile are cut into n_split blocks, an item each.
+template <int MODE, bool SPLIT>
 __device__ bool find_item(const AttnTileLaunch& p, int64_t block, Place& place, Item& it) {
     const kda_attn_prefill_args& a = p.a;
     const int lane = threadIdx.x & 31;
@@ -253,7 +254,7 @@ __device__ bool find_item(const AttnTileLaunch& p, int64_t block, Place& place, 
     int64_t idx = block / a.n_kv_heads;
     it.hk = (int32_t)(block - idx * a.n_kv_heads);
     it.split = 0;
-    if (MODE == kPrefix) {
+    if (SPLIT) {
         it.split = (int32_t)(idx % p.n_split);
         idx /= p.n_split;
     }
@@ -318,12 +319,19 @@ __device__ bool find_item(const AttnTileLaunch& p, int64_t block, Place& place, 
         it.n_keys[1] = (it.k_hi + kTile - 1) / kTile;
     }
     if (left <= tokens) it.n_keys[1] = 0;
+    if (MODE != kPrefix && SPLIT) {
+        const int per = (max(it.n_keys[0], it.n_keys[1]) + p.n_split - 1) / p.n_split, from = it.split * per;
+        it.k_lo = from * kTile;
+        it.k_hi = max(it.k_lo, min(it.k_hi, it.k_lo + per * kTile));
+        it.n_keys[0] = max(0, min(per, it.n_keys[0] - from));
+        it.n_keys[1] = max(0, min(per, it.n_keys[1] - from));
+    }
     return true;
 }
 
 // ------------------------------------------------------------------ kernel
 
-template <int D, int MODE>
+template <int D, int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__ Maps maps) {
     using Sh = Shape<D>;
@@ -616,7 +624,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             bool ok = true;
             for (uint32_t asked = 0;; ++asked) {
                 Item it;
-                if (find_item<MODE>(p, block, place, it)) {
+                if (find_item<MODE, SPLIT>(p, block, place, it)) {
                     if (!(ok = wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1))) break;
                     it.live = 1;
                     if (lane == 0) {
@@ -776,7 +784,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             }
             if (live) {
                 const float m2 = l == 0.f ? -CUDART_INF_F : m * c;
-                if (MODE == kPrefix) {
+                if (SPLIT) {
                     float4* out = reinterpret_cast<float4*>(p.part_o + at * D);
 #pragma unroll
                     for (int x = 0; x < D; x += 4)
@@ -862,7 +870,7 @@ bool cache_map(CUtensorMap* m, const void* base, const kda_attn_prefill_args& a)
     return make_map(m, base, 2, dims, strides, box);
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool SPLIT>
 cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
     const kda_attn_prefill_args& a = p.a;
     const int G = a.n_heads / a.n_kv_heads, tokens = kTile / G;
@@ -876,19 +884,20 @@ cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
     int64_t blocks = (a.total_tokens / (2 * tokens) + a.n_seqs) * a.n_kv_heads;
-    if (MODE == kPrefix) blocks *= p.n_split;
+    if (SPLIT) blocks *= p.n_split;
     if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, MODE, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
     note_launch();
-    return launch_overlapped(attn_tc_kernel<D, MODE>, dim3((unsigned)blocks), dim3(kThreads), smem_bytes<D>(), s, p, maps);
+    return launch_overlapped(attn_tc_kernel<D, MODE, SPLIT>, dim3((unsigned)blocks), dim3(kThreads), smem_bytes<D>(), s, p, maps);
 }
 
 template <int D>
 cudaError_t launch_d(const AttnTileLaunch& p, cudaStream_t s) {
-    if (p.prefix_lens) return launch_t<D, kPrefix>(p, s);
-    return p.a.block_table ? launch_t<D, kPaged>(p, s) : launch_t<D, kPacked>(p, s);
+    if (p.prefix_lens) return launch_t<D, kPrefix, true>(p, s);
+    if (p.n_split > 1) return p.a.block_table ? launch_t<D, kPaged, true>(p, s) : launch_t<D, kPacked, true>(p, s);
+    return p.a.block_table ? launch_t<D, kPaged, false>(p, s) : launch_t<D, kPacked, false>(p, s);
 }
 
 }  // namespace

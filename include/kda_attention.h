@@ -142,7 +142,15 @@ typedef struct kda_attn_prefill_args {
     int64_t n_blocks;
     int32_t block_size;
     int32_t table_stride;
+    void *workspace;           /* 256-byte aligned, or NULL */
+    size_t workspace_bytes;
 } kda_attn_prefill_args;
+
+/* Bytes of workspace with which kda_attn_prefill cuts the keys of few rows into
+ * blocks that run side by side (only the sizes and whether block_table is NULL are
+ * read); 0 where it would not, and for invalid sizes.  The workspace is optional:
+ * with none, or a smaller one, every row's keys are walked by one thread block. */
+size_t kda_attn_prefill_workspace_size(const kda_attn_prefill_args *args);
 
 kda_status_t kda_attn_prefill(const kda_attn_prefill_args *args, void *stream);
 

@@ -57,7 +57,7 @@ INV, UNS = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED
 
 def test_struct_sizes(lib):
     assert ctypes.sizeof(kda.CachePlanArgs) == 4 * 4 + 8 * 2 + 8 * 10
-    assert ctypes.sizeof(kda.AttnPrefillArgs) == 4 * 6 + 8 * 5 + 8 * 10 + 8 + 4 * 2
+    assert ctypes.sizeof(kda.AttnPrefillArgs) == 4 * 6 + 8 * 5 + 8 * 10 + 8 + 4 * 2 + 8 * 2
     assert ctypes.sizeof(kda.AttnDecodeArgs) == 4 * 6 + 8 * 2 + 8 * 7 + 8 + 4 * 4 + 8 * 3 + 8
 
 

@@ -32,8 +32,14 @@
 // values of the others by zero and notes the first key of each column that held a
 // NaN, +inf or -inf; at the end, rows that see such a key get it added.
 //
-// Bound by the tensor pipe: 4 d flops per (row, key) pair.  Measured on 4 x 8192
-// tokens, 32 query and 8 key/value heads, d = 128: 1.48 ms, 1485 TFLOP/s.
+// Bound by the tensor pipe where sequences are long: 4 d flops per (row, key) pair.
+// Measured on 4 x 8192 tokens, 32 query and 8 key/value heads, d = 128: 1.30 ms, 1690
+// TFLOP/s.  Items of few tiles are bound by the steps between them, and those by
+// fetching instructions: straight code that is not in the 32 KB of instruction cache
+// costs 6 cycles an instruction, and a jump a trip to L2.  So what is rarely executed
+// is kept in loops, and what every item executes in one place: 2880 items of one or two
+// tiles (180 x 256 tokens, 16 query and 2 key/value heads, d = 64) took 112 us with 96
+// KB of code and take 91 us with 72 KB.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -69,17 +75,20 @@ template <int D> struct Shape {
     static constexpr uint32_t kQ = 0, kRing = 2 * kTileBytes, kMisc = kRing + kStages * kTileBytes;
 };
 
-// One item of work; positions fit 32 bits (a table row has fewer than 2^31).
+// One item of work; positions and rows of cu_seqlens fit 32 bits (a table row has fewer
+// than 2^31 positions).  An item whose sequence is bad has no key tiles and no rows.
 struct Item {
-    int64_t row0;                 // packed row of the first token (or member)
-    int32_t live;                 // 0: no further items
+    int32_t n_keys0, n_keys1;     // key tiles of each row tile
+    int32_t n_tiles;              // the more of the two; -1: no further items
+    int32_t edge;                 // from this key tile on some row sees only a part of it
+    int32_t row0;                 // packed row of the first token (or member)
     int32_t t0, n;                // first token of the item, tokens of the sequence
     int32_t hk, split;
     int32_t table_row;
     int32_t first;                // token t sees the keys j <= first + t
     int32_t k_lo, k_hi;           // keys that some row of the item sees
     int32_t all_see;              // every row sees the keys below this one
-    int32_t n_keys[2];            // key tiles of each row tile
+    __device__ __forceinline__ int32_t n_keys(int q) const { return q ? n_keys1 : n_keys0; }
 };
 
 template <int D> struct Misc {
@@ -169,6 +178,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+// A bounded wait (about a second) in few instructions: there are dozens, and outside a
+// loop what one costs is mostly fetching it.
+constexpr uint32_t kWaitCycles = 2000000000u;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return true;
+    const uint32_t t0 = (uint32_t)clock();
+    while (!mbar_test(bar, parity))
+        if ((uint32_t)clock() - t0 > kWaitCycles) return false;
+    return true;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -181,9 +200,9 @@ __device__ __forceinline__ void ask_next_block(uint4* to, uint64_t* bar) {
                  "r"(smem_u32(bar))
                  : "memory");
 }
-// The answer: the block's index, or -1.
-__device__ __forceinline__ int64_t next_block(const uint4* from) {
-    uint32_t taken, x;
+// Whether the answer is a block, and its index.
+__device__ __forceinline__ bool next_block(const uint4* from, uint32_t& x) {
+    uint32_t taken;
     asm volatile(
         "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
         "ld.shared.b128 h, [%2];\n\t"
@@ -194,7 +213,7 @@ __device__ __forceinline__ int64_t next_block(const uint4* from) {
         : "=r"(taken), "=r"(x)
         : "r"(smem_u32(from))
         : "memory");
-    return taken ? (int64_t)x : -1;
+    return taken;
 }
 
 // Pairs of fp32 values in one 64-bit register, for the two-wide fp32 instructions.
@@ -236,61 +255,62 @@ struct Ring {
 
 // ------------------------------------------------------------------ items
 
-// The finder's place among the sequences: tiles of the ones before `s`.
+// The finder's place: 32 sequences, one a lane, and the item tiles up to and with each.
 struct Place {
-    int32_t s = 0;
-    int64_t tiles = 0;
+    int32_t s0 = -32;             // the first of them
+    int32_t lo = 0, hi = 0;       // the lane's rows
+    int32_t before = 0, upto = 0; // tiles before the 32, and with the lane's own
 };
 
 // Fills `it` for grid index `block`; false when that block has nothing to do.  One
 // warp; later indexes mostly lie further on, so the search goes on where the last one
-// ended.  Tiles of one sequence come last first: the later ones see more keys.  SPLIT:
-// the keys of a tile are cut into n_split blocks, an item each.
+// ended, mostly without a load.  Tiles of one sequence come last first: the later ones
+// see more keys.  SPLIT: the keys of a tile are cut into n_split blocks, an item each.
 template <int MODE, bool SPLIT>
-__device__ bool find_item(const AttnTileLaunch& p, int64_t block, Place& place, Item& it) {
+__device__ bool find_item(const AttnTileLaunch& p, uint32_t block, Place& place, Item& it) {
     const kda_attn_prefill_args& a = p.a;
     const int lane = threadIdx.x & 31;
     const int tokens = kTile / (a.n_heads / a.n_kv_heads);
-    int64_t idx = block / a.n_kv_heads;
-    it.hk = (int32_t)(block - idx * a.n_kv_heads);
+    uint32_t rest = block / (uint32_t)a.n_kv_heads;
+    it.hk = (int32_t)(block - rest * a.n_kv_heads);
     it.split = 0;
     if (SPLIT) {
-        it.split = (int32_t)(idx % p.n_split);
-        idx /= p.n_split;
+        const uint32_t x = rest / (uint32_t)p.n_split;
+        it.split = (int32_t)(rest - x * p.n_split);
+        rest = x;
     }
-    if (idx < place.tiles) place = Place{};
-    int32_t seq = 0;
-    for (; place.s < a.n_seqs; place.s += 32) {
-        const int32_t s = place.s + lane;
-        int64_t lo = 0, hi = 0;
-        if (s < a.n_seqs) {
-            lo = a.cu_seqlens[s];
-            hi = a.cu_seqlens[s + 1];
-            if (lo < 0 || hi < lo || hi > a.total_tokens) hi = lo;
+    const int32_t idx = (int32_t)rest;
+    if (idx < place.before) place = Place{};
+    uint32_t here;
+    while (!(here = __ballot_sync(0xffffffffu, idx < place.upto))) {
+        place.before = __shfl_sync(0xffffffffu, place.upto, 31);
+        if (place.s0 + 32 >= a.n_seqs) {                                   // past the last tile, as later blocks will be
+            place.upto = place.before;
+            return false;
         }
-        const int64_t mine = (hi - lo + 2 * tokens - 1) / (2 * tokens);
-        int64_t upto = mine;
+        place.s0 += 32;
+        const int32_t s = place.s0 + lane;
+        place.lo = place.hi = 0;
+        if (s < a.n_seqs) {
+            place.lo = a.cu_seqlens[s];
+            place.hi = a.cu_seqlens[s + 1];
+            if (place.lo < 0 || place.hi < place.lo || place.hi > a.total_tokens) place.hi = place.lo;
+        }
+        int32_t upto = (int32_t)(((uint32_t)(place.hi - place.lo) + 2 * tokens - 1) / (uint32_t)(2 * tokens));
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+            const int32_t y = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += y;
         }
-        upto += place.tiles;
-        const uint32_t here = __ballot_sync(0xffffffffu, idx < upto);
-        if (here) {
-            const int src = __ffs(here) - 1;
-            it.row0 = __shfl_sync(0xffffffffu, lo, src);
-            it.n = (int32_t)(__shfl_sync(0xffffffffu, hi, src) - it.row0);
-            it.t0 = (int32_t)(__shfl_sync(0xffffffffu, upto, src) - 1 - idx) * 2 * tokens;
-            seq = place.s + src;
-            it.table_row = MODE == kPrefix ? (int32_t)it.row0 : seq;
-            break;
-        }
-        place.tiles = __shfl_sync(0xffffffffu, upto, 31);
+        place.upto = place.before + upto;
     }
-    if (place.s >= a.n_seqs) return false;
+    const int src = __ffs(here) - 1, seq = place.s0 + src;
+    it.row0 = __shfl_sync(0xffffffffu, place.lo, src);
+    it.n = __shfl_sync(0xffffffffu, place.hi, src) - it.row0;
+    it.t0 = (__shfl_sync(0xffffffffu, place.upto, src) - 1 - idx) * 2 * tokens;
+    it.table_row = MODE == kPrefix ? it.row0 : seq;
     const int64_t cap = (int64_t)a.table_stride * a.block_size;
-    int64_t K;
+    int32_t K;
     if (MODE == kPacked) {
         K = it.n;
     } else if (MODE == kPaged) {
@@ -301,31 +321,35 @@ __device__ bool find_item(const AttnTileLaunch& p, int64_t block, Place& place, 
         }
     } else {
         K = p.prefix_lens[seq];
-        if (K < 0 || K > cap || K % a.block_size) K = 0;                   // flagged by the decode plan
+        if (K < 0 || K > cap || (K & (a.block_size - 1))) K = 0;           // flagged by the decode plan
     }
-    it.first = (int32_t)(MODE == kPacked ? 0 : MODE == kPaged ? K - it.n : K);
+    it.first = MODE == kPacked ? 0 : MODE == kPaged ? K - it.n : K;
     const int left = it.n - it.t0;                                         // tokens from the first one on
+    auto tiles = [](int32_t keys) { return (int32_t)(((uint32_t)keys + kTile - 1) / kTile); };
     if (MODE == kPrefix) {
-        const int64_t per = ((K + kTile - 1) / kTile + p.n_split - 1) / p.n_split * kTile;
-        it.k_lo = (int32_t)min(K, it.split * per);
-        it.k_hi = it.all_see = (int32_t)min(K, it.k_lo + per);
-        it.n_keys[0] = it.n_keys[1] = (it.k_hi - it.k_lo + kTile - 1) / kTile;
+        const int64_t per = (int64_t)(((uint32_t)tiles(K) + p.n_split - 1) / (uint32_t)p.n_split) * kTile;
+        it.k_lo = (int32_t)min((int64_t)K, it.split * per);
+        it.k_hi = it.all_see = (int32_t)min((int64_t)K, it.k_lo + per);
+        it.n_keys0 = it.n_keys1 = tiles(it.k_hi - it.k_lo);
     } else {
         it.k_lo = 0;
-        auto seen = [&](int tokens) { return (int32_t)max((int64_t)0, min(K, (int64_t)it.first + it.t0 + tokens)); };
+        // (first + t0 + tokens <= K + 2 kTile, which may pass 2^31)
+        auto seen = [&](int tokens) { return max(0, (int32_t)min((int64_t)K, (int64_t)it.first + it.t0 + tokens)); };
         it.all_see = seen(1);
         it.k_hi = seen(min(left, 2 * tokens));
-        it.n_keys[0] = (seen(min(left, tokens)) + kTile - 1) / kTile;
-        it.n_keys[1] = (it.k_hi + kTile - 1) / kTile;
+        it.n_keys0 = tiles(seen(min(left, tokens)));
+        it.n_keys1 = tiles(it.k_hi);
     }
-    if (left <= tokens) it.n_keys[1] = 0;
+    if (left <= tokens) it.n_keys1 = 0;
     if (MODE != kPrefix && SPLIT) {
-        const int per = (max(it.n_keys[0], it.n_keys[1]) + p.n_split - 1) / p.n_split, from = it.split * per;
-        it.k_lo = from * kTile;
-        it.k_hi = max(it.k_lo, min(it.k_hi, it.k_lo + per * kTile));
-        it.n_keys[0] = max(0, min(per, it.n_keys[0] - from));
-        it.n_keys[1] = max(0, min(per, it.n_keys[1] - from));
+        const int per = (int)((uint32_t)(max(it.n_keys0, it.n_keys1) + p.n_split - 1) / (uint32_t)p.n_split), from = it.split * per;
+        it.k_lo = min(it.k_hi, from * kTile);
+        it.k_hi = (int32_t)min((int64_t)it.k_hi, it.k_lo + (int64_t)per * kTile);
+        it.n_keys0 = max(0, min(per, it.n_keys0 - from));
+        it.n_keys1 = max(0, min(per, it.n_keys1 - from));
     }
+    it.n_tiles = max(it.n_keys0, it.n_keys1);
+    it.edge = max(0, it.all_see - it.k_lo) / kTile;
     return true;
 }
 
@@ -379,14 +403,15 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
     // roles that depend on it run out of theirs.  Between a tile's steps, where the
     // vote's time counts, lanes wait with `pass`, each for itself: one that ran out goes
     // on without waiting, to the vote at the item's end.
+    bool late = false;                            // a wait ran out: flagged at the end
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
-        if (!ok) flag(p.status, KDA_DEV_WAIT_TIMEOUT);
+        const bool ok = __all_sync(0xffffffffu, wait(bar, parity));
+        late |= !ok;
         return ok;
     };
     auto pass = [&](bool& ok, uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity)) {
-            flag(p.status, KDA_DEV_WAIT_TIMEOUT);
+        if (ok && !wait(bar, parity)) {
+            late = true;
             ok = false;
         }
     };
@@ -396,10 +421,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         it = ms.item[i & 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.item_empty[i & 1]);
-        return it.live != 0;
+        return it.n_tiles >= 0;
     };
-    // from this tile on some row sees only a part of the keys
-    auto edge_of = [](const Item& it) { return max(0, it.all_see - it.k_lo) / kTile; };
 
     // the register split is made inside the branches: after a merge of the two the
     // compiler would hold everything to the smaller share
@@ -413,27 +436,28 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
             auto at = [](uint64_t desc, uint32_t byte) { return desc + (uint64_t)(byte >> 4); };
             auto scores = [&](int q, uint32_t stage) {
-                const uint32_t qb = s_base + Sh::kQ + q * Sh::kTileBytes, kb = s_base + Sh::kRing + stage * Sh::kTileBytes;
+                const uint64_t qd = at(d_kmajor, s_base + Sh::kQ + q * Sh::kTileBytes);
+                const uint64_t kd = at(d_kmajor, s_base + Sh::kRing + stage * Sh::kTileBytes);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
-                    mma_ss(leader, tS(q), at(d_kmajor, qb + off), at(d_kmajor, kb + off), id_s, ks > 0);
+                    mma_ss(leader, tS(q), at(qd, off), at(kd, off), id_s, ks > 0);
                 }
                 commit(leader, &ms.s_full[q]);
             };
             auto values = [&](int q, uint32_t stage, bool first) {
-                const uint32_t vb = s_base + Sh::kRing + stage * Sh::kTileBytes;
+                const uint64_t vd = at(d_mnmajor, s_base + Sh::kRing + stage * Sh::kTileBytes);
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks)
-                    mma_ts(leader, tO(q), tS(q) + 8 * ks, at(d_mnmajor, vb + ks * 2048), id_o, !first || ks > 0);
+                    mma_ts(leader, tO(q), tS(q) + 8 * ks, at(vd, ks * 2048), id_o, !first || ks > 0);
             };
             uint32_t guard_phase = 0;                             // a bit for each stage
-            uint32_t p_phase[2] = {0, 0}, o_items[2] = {0, 0};
+            uint32_t p_phase = 0, o_items = 0;                    // a bit for each row tile
             Ring r;
             bool ok = true;
             Item it;
             for (uint32_t i = 0; __all_sync(0xffffffffu, ok) && get_item(i, it); ++i) {
-                const int n_tiles = max(it.n_keys[0], it.n_keys[1]), first_edge = edge_of(it);
+                const int n_tiles = it.n_tiles;
                 pass(ok, &ms.q_full, i & 1);
                 if (n_tiles == 0) {
                     commit(leader, &ms.q_free);
@@ -441,68 +465,70 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 }
                 pass(ok, &ms.full[r.stage], r.phase);
                 fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 2; ++q)
-                    if (it.n_keys[q] > 0) scores(q, r.stage);
+                    if (it.n_keys(q) > 0) scores(q, r.stage);
                 commit(leader, &ms.empty[r.stage]);
                 if (n_tiles == 1) commit(leader, &ms.q_free);
                 r.next(Sh::kStages);
                 auto v_ready = [&](int j) {
                     pass(ok, &ms.full[r.stage], r.phase);
-                    if (j >= first_edge) {
+                    if (j >= it.edge) {
                         pass(ok, &ms.guarded[r.stage], guard_phase >> r.stage & 1);
                         guard_phase ^= 1u << r.stage;
                     }
                 };
-                v_ready(0);
-                for (int j = 0;; ++j) {
+                for (int j = 0; j < n_tiles; ++j) {
+                    v_ready(j);
                     const uint32_t vs = r.stage;
                     r.next(Sh::kStages);
                     const bool more = j + 1 < n_tiles;
                     if (more) pass(ok, &ms.full[r.stage], r.phase);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        if (j < it.n_keys[q]) {
-                            if (j == 0) pass(ok, &ms.o_free[q], (o_items[q]++ & 1) ^ 1);
-                            pass(ok, &ms.p_ready[q], p_phase[q]);
-                            if (!ok) break;
-                            p_phase[q] ^= 1;
+                        const int n_keys = it.n_keys(q);
+                        if (j < n_keys) {
+                            if (j == 0) {
+                                pass(ok, &ms.o_free[q], (o_items >> q & 1) ^ 1);
+                                o_items ^= 1u << q;
+                            }
+                            pass(ok, &ms.p_ready[q], p_phase >> q & 1);
+                            p_phase ^= 1u << q;
                             fence_after_sync();
                             values(q, vs, j == 0);
-                            if (j + 1 == it.n_keys[q]) commit(leader, &ms.o_done[q]);
+                            if (j + 1 == n_keys) commit(leader, &ms.o_done[q]);
                         }
                         if (q == 1) commit(leader, &ms.empty[vs]);
-                        if (j + 1 < it.n_keys[q]) scores(q, r.stage);
+                        if (j + 1 < n_keys) scores(q, r.stage);
                     }
-                    if (!more || !ok) break;
+                    if (!more) break;
                     commit(leader, &ms.empty[r.stage]);
                     if (j + 2 == n_tiles) commit(leader, &ms.q_free);   // after the item's last scores
                     r.next(Sh::kStages);
-                    v_ready(j + 1);
                 }
             }
             // the MMAs in flight finish before shared and tensor memory go
             commit(leader, &ms.drained);
-            mbar_wait(&ms.drained, 0);
+            wait(&ms.drained, 0);
         } else if (warp == kLoadWarp) {
             // -------------------------------------------------------------- copies
             const int box = MODE == kPacked ? kTile : min(a.block_size, kTile);           // rows of one copy
-            const int boxes = kTile / box;
+            const int boxes = kTile / box, page_shift = MODE == kPacked ? 0 : __ffs(a.block_size) - 1;
             const int mine = lane / kRegions, region = lane % kRegions;                   // this lane's copy
             uint32_t q_loads = 0, issued = 0;
             Ring ring;
             bool ok = true;
             Item it;
             for (uint32_t i = 0; ok && get_item(i, it); ++i) {
-                const int n_tiles = max(it.n_keys[0], it.n_keys[1]);
+                const int n_tiles = it.n_tiles;
                 if (i > 0 && !(ok = wait_all(&ms.q_free, (i - 1) & 1))) break;
                 if (lane == 0) {
-                    const int tiles = it.n_keys[1] > 0 ? 2 : 1;
+                    const int tiles = it.n_keys1 > 0 ? 2 : 1;
                     mbar_expect_tx(&ms.q_full, (uint32_t)tiles * kRegions * (uint32_t)(tokens * G) * 128u);
                     for (int q = 0; q < tiles; ++q)
                         for (int c = 0; c < kRegions; ++c)
                             tma_load_3d(sm + Sh::kQ + q * Sh::kTileBytes + c * Sh::kRegion, &maps.q, 64 * c, it.hk * G,
-                                        (int32_t)(it.row0 + it.t0 + q * tokens), &ms.q_full);
+                                        it.row0 + it.t0 + q * tokens, &ms.q_full);
                 }
                 q_loads = i + 1;
                 const int32_t* table = MODE == kPacked ? nullptr : a.block_table + (int64_t)it.table_row * a.table_stride;
@@ -513,14 +539,15 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     int32_t row = 0;
                     if (MODE != kPacked && mine < live) {
                         const int32_t key = k0 + mine * box;
-                        const int32_t block = table[key / a.block_size];
+                        const int32_t block = table[key >> page_shift];
                         if (block < 0 || block >= a.n_blocks) {
                             flag(p.status, KDA_DEV_BAD_SLOT);
                             row = (int32_t)(a.n_blocks * a.n_kv_heads * a.block_size);     // past the end: reads zeros
                         } else {
-                            row = (int32_t)((block * (int64_t)a.n_kv_heads + it.hk) * a.block_size + key % a.block_size);
+                            row = (int32_t)((block * (int64_t)a.n_kv_heads + it.hk) * a.block_size + (key & (a.block_size - 1)));
                         }
                     }
+#pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const uint32_t st = ring.stage;
                         if (!(ok = wait_all(&ms.empty[st], ring.phase ^ 1u))) break;
@@ -531,7 +558,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         __syncwarp();
                         if (mine < live) {
                             uint8_t* to = dst + region * Sh::kRegion + mine * box * 128;
-                            if (MODE == kPacked) tma_load_3d(to, map, 64 * region, it.hk, (int32_t)(it.row0 + k0), &ms.full[st]);
+                            if (MODE == kPacked) tma_load_3d(to, map, 64 * region, it.hk, it.row0 + k0, &ms.full[st]);
                             else tma_load_2d(to, map, 64 * region, row, &ms.full[st]);
                         }
                         ++issued;
@@ -541,9 +568,9 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             }
             // copies in flight land before the block's shared memory goes: the last of
             // Q, and the last of every stage
-            if (q_loads > 0) mbar_wait(&ms.q_full, (q_loads - 1) & 1);
+            if (q_loads > 0) wait(&ms.q_full, (q_loads - 1) & 1);
             for (uint32_t i = issued < Sh::kStages ? 0 : issued - Sh::kStages; i < issued; ++i)
-                mbar_wait(&ms.full[i % Sh::kStages], i / Sh::kStages & 1);
+                wait(&ms.full[i % Sh::kStages], i / Sh::kStages & 1);
         } else if (warp == kGuardWarp) {
             // -------------------------------------------------------------- hidden values
             // This warp follows every load and releases its stage with the MMAs, so that
@@ -553,7 +580,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             uint32_t o_items[2] = {0, 0};                         // items before this one that each row tile takes part in
             Item it;
             for (uint32_t i = 0; ok && get_item(i, it); ++i) {
-                const int n_tiles = max(it.n_keys[0], it.n_keys[1]), first_edge = edge_of(it);
+                const int n_tiles = it.n_tiles, first_edge = it.edge;
                 bool noted = false;
                 for (int x = 0; x < 2 * n_tiles; ++x) {
                     const int j = x >> 1;
@@ -612,21 +639,20 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                     if (lane == 0) mbar_arrive(&ms.empty[st]);
                 }
-                for (int q = 0; q < 2; ++q) o_items[q] += it.n_keys[q] > 0;
+                for (int q = 0; q < 2; ++q) o_items[q] += it.n_keys(q) > 0;
             }
         } else {
             // -------------------------------------------------------------- items
             // The next item is claimed when the last one's copies are under way, not before:
             // what a block claims early, a block that gets free first cannot have.
             Place place;
-            int64_t block = blockIdx.x;
+            uint32_t block = blockIdx.x;
             uint32_t i = 0;
             bool ok = true;
             for (uint32_t asked = 0;; ++asked) {
                 Item it;
                 if (find_item<MODE, SPLIT>(p, block, place, it)) {
                     if (!(ok = wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1))) break;
-                    it.live = 1;
                     if (lane == 0) {
                         ms.item[i & 1] = it;
                         mbar_arrive(&ms.item_full[i & 1]);
@@ -643,13 +669,13 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 }
                 __syncwarp();
                 if (!(ok = wait_all(&ms.next, asked & 1))) break;
-                block = next_block(&ms.next_block);
+                const bool any = next_block(&ms.next_block, block);
                 fence_async_smem();
                 __syncwarp();
-                if (block < 0) break;
+                if (!any) break;
             }
             if (ok && wait_all(&ms.item_empty[i & 1], (i >> 1 & 1) ^ 1) && lane == 0) {
-                ms.item[i & 1].live = 0;
+                ms.item[i & 1].n_tiles = -1;
                 mbar_arrive(&ms.item_full[i & 1]);
             }
         }
@@ -663,6 +689,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             }
         const int q = warp >> 2;
         const int r = 32 * (warp & 3) + lane;                     // row of the tile = TMEM lane
+        const int r_token = r / G, g = r % G;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         // a scale of 0 becomes the least normal number, so that a hidden score of -inf stays one
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
@@ -670,7 +697,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         bool ok = true;
         Item it;
         for (uint32_t i = 0; __all_sync(0xffffffffu, ok) && get_item(i, it); ++i) {
-            const int t = it.t0 + q * tokens + r / G, g = r % G;
+            const int t = it.t0 + q * tokens + r_token;
             const bool live = r < tokens * G && t < it.n;
             // keys that this row sees, and keys that all rows of the warp see for sure.  Rows
             // past the end see none: what their scores hold is never looked at.
@@ -678,7 +705,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             const int row_sees = max(0, seen - it.k_lo);
             int tile_sees = max(0, (MODE == kPrefix ? it.k_hi : min(it.k_hi, it.first + it.t0 + q * tokens + 1)) - it.k_lo);
             if (__any_sync(0xffffffffu, !live)) tile_sees = 0;
-            const int n = it.n_keys[q];
+            const int n = it.n_keys(q);
             float m = kLeastMaximum;
             uint64_t l2 = pair2(0.f);
             for (int j = 0; j < n; ++j) {
@@ -693,7 +720,11 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 if ((j + 1) * kTile > tile_sees) {
                     const int visible = row_sees - j * kTile;
 #pragma unroll
-                    for (int x = 0; x < kTile; ++x) s[x] = x < visible ? s[x] : 0xFF800000u;
+                    for (int y = 0; y < kTile; y += 32) {
+                        const uint32_t keep = visible >= y + 32 ? 0xFFFFFFFFu : visible <= y ? 0u : (1u << (visible - y)) - 1u;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) s[y + x] = keep & (1u << x) ? s[y + x] : 0xFF800000u;
+                    }
                 }
                 auto maximum = [&]() {                             // of the tile's scores, and m
                     float top[4] = {m, m, m, m};
@@ -722,20 +753,18 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                     return add2(sums[0], sums[1]);
                 };
-                if (j == 0) m = maximum();
-                uint64_t sum = weights();
-                const float2 both = unpair2(sum);
-                const bool grow = !(both.x + both.y <= kMostWeight);
-                if (__any_sync(0xffffffffu, grow)) {
-                    // rare: move the maximum, rescale what was summed so far, weigh again
-                    const float mx = grow ? maximum() : m;         // a row's result depends on no other row
-                    const float f = mx > m ? ex2((m - mx) * c) : 1.f;
-                    m = mx;
-                    const float2 lf = unpair2(l2);
-                    l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
-                    if (j > 0) {
+                uint64_t sum;
+                bool move = j == 0, grow = true;                   // the first tile's maximum, and the rows that want one
+                for (;;) {
+                    if (move) {
+                        const float mx = grow ? maximum() : m;     // a row's result depends on no other row
+                        const float f = mx > m ? ex2((m - mx) * c) : 1.f;
+                        m = mx;
+                        const float2 lf = unpair2(l2);
+                        l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
+                        // rare: rescale what was summed so far
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 16) {
+                        for (int x = j == 0 ? D : 0; x < D; x += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO(q) + lanes + x, o);
                             tmem_wait_ld();
@@ -744,8 +773,13 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                             tmem_st16(tO(q) + lanes + x, o);
                         }
                     }
-                    tmem_wait_st();
                     sum = weights();
+                    if (move) break;
+                    const float2 both = unpair2(sum);
+                    grow = !(both.x + both.y <= kMostWeight);
+                    move = __any_sync(0xffffffffu, grow);
+                    if (!move) break;
+                    tmem_wait_st();
                 }
                 l2 = add2(l2, sum);
                 tmem_wait_st();
@@ -754,7 +788,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             }
             const float l = unpair2(l2).x + unpair2(l2).y;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int64_t row = it.row0 + t;
+            const int64_t row = (int64_t)it.row0 + t;
             const int head = it.hk * G + g;
             const int64_t at = ((int64_t)it.split * a.total_tokens + row) * a.n_heads + head;
             uint32_t o[D];
@@ -763,18 +797,26 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 __syncwarp();
                 o_phase ^= 1;
                 fence_after_sync();
+                if (MODE != kPrefix && *(volatile int32_t*)&ms.poison == (int32_t)i) {
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        uint32_t y[16];
+                        tmem_ld16(tO(q) + lanes + x, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const bool pos = seen > ms.first_pos[x + k], neg = seen > ms.first_neg[x + k];
+                            float add = pos ? CUDART_INF_F : neg ? -CUDART_INF_F : 0.f;
+                            if (seen > ms.first_nan[x + k] || (pos && neg)) add = CUDART_NAN_F;
+                            y[k] = __float_as_uint(__uint_as_float(y[k]) + add);
+                        }
+                        tmem_st16(tO(q) + lanes + x, y);
+                    }
+                    tmem_wait_st();
+                }
 #pragma unroll
                 for (int x = 0; x < D; x += 32) tmem_ld32(tO(q) + lanes + x, o + x);
                 tmem_wait_ld();
-                if (MODE != kPrefix && *(volatile int32_t*)&ms.poison == (int32_t)i) {
-#pragma unroll
-                    for (int x = 0; x < D; ++x) {
-                        const bool pos = seen > ms.first_pos[x], neg = seen > ms.first_neg[x];
-                        float add = pos ? CUDART_INF_F : neg ? -CUDART_INF_F : 0.f;
-                        if (seen > ms.first_nan[x] || (pos && neg)) add = CUDART_NAN_F;
-                        o[x] = __float_as_uint(__uint_as_float(o[x]) + add);
-                    }
-                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.o_free[q]);
@@ -816,6 +858,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         }
         fence_before_sync();
     }
+    if (late) flag(p.status, KDA_DEV_WAIT_TIMEOUT);
     __syncthreads();
     if (warp == kMmaWarp) {
         fence_after_sync();

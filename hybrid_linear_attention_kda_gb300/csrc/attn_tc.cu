@@ -238,6 +238,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -693,6 +698,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         // a scale of 0 becomes the least normal number, so that a hidden score of -inf stays one
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
+        // rows that begin on 32 bytes are written in whole sectors
+        const bool wide = !SPLIT && ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)(a.o_stride * 2)) & 31u) == 0;
         uint32_t phase = 0, o_phase = 0;                          // of the tiles, of the items with tiles
         bool ok = true;
         Item it;
@@ -791,7 +798,6 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             const int64_t row = (int64_t)it.row0 + t;
             const int head = it.hk * G + g;
             const int64_t at = ((int64_t)it.split * a.total_tokens + row) * a.n_heads + head;
-            uint32_t o[D];
             if (n > 0) {
                 pass(ok, &ms.o_done[q], o_phase);
                 __syncwarp();
@@ -814,45 +820,82 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                     tmem_wait_st();
                 }
-#pragma unroll
-                for (int x = 0; x < D; x += 32) tmem_ld32(tO(q) + lanes + x, o + x);
-                tmem_wait_ld();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.o_free[q]);
-            } else {
-#pragma unroll
-                for (int x = 0; x < D; ++x) o[x] = 0u;
+            } else {                                               // no keys: zeros
+                const uint32_t zero[16] = {};
+#pragma unroll 1
+                for (int x = 0; x < D; x += 16) tmem_st16(tO(q) + lanes + x, zero);
+                tmem_wait_st();
             }
-            if (live) {
-                const float m2 = l == 0.f ? -CUDART_INF_F : m * c;
+            const float m2 = l == 0.f ? -CUDART_INF_F : m * c;
+            char* out = SPLIT ? reinterpret_cast<char*>(p.part_o + at * D)
+                              : reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_stride + (int64_t)head * D);
+            if (!live) out = nullptr;
+            const uint64_t inv2 = pair2(inv);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 64) {
+                uint32_t o[64];
+                tmem_ld32(tO(q) + lanes + x, o);
+                tmem_ld32(tO(q) + lanes + x + 32, o + 32);
+                tmem_wait_ld();
+                if (x + 64 == D && n > 0) {
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.o_free[q]);
+                }
                 if (SPLIT) {
-                    float4* out = reinterpret_cast<float4*>(p.part_o + at * D);
+                    float4* to = reinterpret_cast<float4*>(out) + x / 4;
+                    if (live)
 #pragma unroll
-                    for (int x = 0; x < D; x += 4)
-                        out[x / 4] = make_float4(__uint_as_float(o[x]), __uint_as_float(o[x + 1]), __uint_as_float(o[x + 2]),
-                                                 __uint_as_float(o[x + 3]));
-                    p.part_ml[at] = make_float2(m2, l);
-                } else {
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + row * a.o_stride + (int64_t)head * D;
-                    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;      // whole 32-byte sectors
+                        for (int k = 0; k < 16; ++k)
+                            to[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                                __uint_as_float(o[4 * k + 3]));
+                    continue;
+                }
+                uint32_t b[4][8];
 #pragma unroll
-                    for (int x = 0; x < D; x += 16) {
-                        uint32_t b[8];
+                for (int k = 0; k < 32; ++k) {
+                    const float2 y = unpair2(mul2(pair2(o[2 * k], o[2 * k + 1]), inv2));
+                    b[k >> 3][k & 7] = pack_bf16(y.x, y.y);
+                }
+                if (wide) {
+                    // Four lanes trade 32-byte pieces, so that together they write 128 bytes of
+                    // one row at a time: a store instruction takes a cycle a line.  Lane x of the
+                    // four puts piece x ^ y in place y; from lane x ^ y that is that row's piece x.
+#pragma unroll
+                    for (int bit = 1; bit < 4; bit <<= 1) {
+                        const bool up = lane & bit;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (!(y & bit)) {
+                                    const uint32_t lo = b[y][k], hi = b[y | bit][k];
+                                    b[y][k] = up ? hi : lo;
+                                    b[y | bit][k] = up ? lo : hi;
+                                }
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            b[k] = pack_bf16(__uint_as_float(o[x + 2 * k]) * inv, __uint_as_float(o[x + 2 * k + 1]) * inv);
-                        if (wide) {
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + x), "r"(b[0]),
-                                         "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7])
+                            if (y > 0) b[y][k] = __shfl_xor_sync(0xffffffffu, b[y][k], y);
+                        char* to = reinterpret_cast<char*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), y));
+                        if (to)
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * x + 32 * (lane & 3)),
+                                         "r"(b[y][0]), "r"(b[y][1]), "r"(b[y][2]), "r"(b[y][3]), "r"(b[y][4]), "r"(b[y][5]),
+                                         "r"(b[y][6]), "r"(b[y][7])
                                          : "memory");
-                        } else {
-                            reinterpret_cast<uint4*>(out + x)[0] = make_uint4(b[0], b[1], b[2], b[3]);
-                            reinterpret_cast<uint4*>(out + x)[1] = make_uint4(b[4], b[5], b[6], b[7]);
-                        }
                     }
-                    if (a.lse) a.lse[row * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m2, kLn2, logf(l));
+                } else if (live) {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        reinterpret_cast<uint4*>(out + 2 * x)[y] = make_uint4(b[y >> 1][4 * (y & 1)], b[y >> 1][4 * (y & 1) + 1],
+                                                                              b[y >> 1][4 * (y & 1) + 2], b[y >> 1][4 * (y & 1) + 3]);
                 }
+            }
+            if (live) {
+                if (SPLIT) p.part_ml[at] = make_float2(m2, l);
+                else if (a.lse) a.lse[row * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m2, kLn2, logf(l));
             }
             __syncwarp();
         }

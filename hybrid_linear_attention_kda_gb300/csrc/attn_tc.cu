@@ -118,6 +118,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int32_t
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+            "r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
 // The MMA warp runs its loop as a whole and lets one lane issue, so that the
 // descriptors stay in uniform registers: issued from inside a one-lane branch, each
 // MMA took 90 cycles of register moves, against 64 of the tensor pipe.
@@ -365,6 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__ Maps maps) {
     using Sh = Shape<D>;
     constexpr int kRegions = D / 64;
+    // Tiles of keys and values: 1024 bytes hold 8 rows x 64 columns.  Packed ones come in one
+    // copy for each 64 columns; a page, in one copy of all columns, 8 rows at a time (half as
+    // many copies for d = 128: with pages of 16 keys they are what bounds the kernel).
+    constexpr uint32_t kColumnStep = MODE == kPacked ? Sh::kRegion : 1024u;      // to the next 64 columns
+    constexpr uint32_t kRowStep = MODE == kPacked ? 1024u : 1024u * kRegions;    // to the next 8 rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc<D>& ms = *reinterpret_cast<Misc<D>*>(sm + Sh::kMisc);
@@ -438,23 +450,22 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             const uint32_t leader = elect_one();
             const uint32_t id_s = idesc_bf16(kTile, kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
             const uint32_t id_o = idesc_bf16(kTile, D, false, true);
-            const uint64_t d_kmajor = sdesc(0, 16, 1024), d_mnmajor = sdesc(0, Sh::kRegion, 1024);
+            const uint64_t d_q = sdesc(0, 16, 1024), d_k = sdesc(0, 16, kRowStep), d_v = sdesc(0, kColumnStep, kRowStep);
             auto at = [](uint64_t desc, uint32_t byte) { return desc + (uint64_t)(byte >> 4); };
             auto scores = [&](int q, uint32_t stage) {
-                const uint64_t qd = at(d_kmajor, s_base + Sh::kQ + q * Sh::kTileBytes);
-                const uint64_t kd = at(d_kmajor, s_base + Sh::kRing + stage * Sh::kTileBytes);
+                const uint64_t qd = at(d_q, s_base + Sh::kQ + q * Sh::kTileBytes);
+                const uint64_t kd = at(d_k, s_base + Sh::kRing + stage * Sh::kTileBytes);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * Sh::kRegion + (ks & 3) * 32;
-                    mma_ss(leader, tS(q), at(qd, off), at(kd, off), id_s, ks > 0);
-                }
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss(leader, tS(q), at(qd, (ks >> 2) * Sh::kRegion + (ks & 3) * 32),
+                           at(kd, (ks >> 2) * kColumnStep + (ks & 3) * 32), id_s, ks > 0);
                 commit(leader, &ms.s_full[q]);
             };
             auto values = [&](int q, uint32_t stage, bool first) {
-                const uint64_t vd = at(d_mnmajor, s_base + Sh::kRing + stage * Sh::kTileBytes);
+                const uint64_t vd = at(d_v, s_base + Sh::kRing + stage * Sh::kTileBytes);
 #pragma unroll
                 for (int ks = 0; ks < kTile / 16; ++ks)
-                    mma_ts(leader, tO(q), tS(q) + 8 * ks, at(vd, ks * 2048), id_o, !first || ks > 0);
+                    mma_ts(leader, tO(q), tS(q) + 8 * ks, at(vd, 2 * ks * kRowStep), id_o, !first || ks > 0);
             };
             uint32_t guard_phase = 0;                             // a bit for each stage
             uint32_t p_phase = 0, o_items = 0;                    // a bit for each row tile
@@ -519,7 +530,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             // -------------------------------------------------------------- copies
             const int box = MODE == kPacked ? kTile : min(a.block_size, kTile);           // rows of one copy
             const int boxes = kTile / box, page_shift = MODE == kPacked ? 0 : __ffs(a.block_size) - 1;
-            const int mine = lane / kRegions, region = lane % kRegions;                   // this lane's copy
+            // this lane's copy: of its columns, or of a page
+            const int mine = MODE == kPacked ? lane / kRegions : lane, region = MODE == kPacked ? lane % kRegions : 0;
             uint32_t q_loads = 0, issued = 0;
             Ring ring;
             bool ok = true;
@@ -537,21 +549,25 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 }
                 q_loads = i + 1;
                 const int32_t* table = MODE == kPacked ? nullptr : a.block_table + (int64_t)it.table_row * a.table_stride;
+                // copies that begin beyond the last key that a row sees are left out
+                auto copies = [&](int32_t k0) { return MODE == kPacked ? 1 : max(0, min(boxes, (it.k_hi - k0 + box - 1) / box)); };
+                // the table's entry of this lane's page, read a tile ahead
+                auto look_up = [&](int32_t k0) { return MODE != kPacked && mine < copies(k0) ? table[(k0 + mine * box) >> page_shift] : 0; };
+                int32_t block = n_tiles > 0 ? look_up(it.k_lo) : 0;
                 for (int j = 0; j < n_tiles && ok; ++j) {
                     const int32_t k0 = it.k_lo + j * kTile;
-                    // copies that begin beyond the last key that a row sees are left out
-                    const int live = MODE == kPacked ? 1 : min(boxes, (it.k_hi - k0 + box - 1) / box);
-                    int32_t row = 0;
+                    const int live = copies(k0);
+                    int32_t rows8 = 0;                            // the page's place, in units of 8 rows
                     if (MODE != kPacked && mine < live) {
-                        const int32_t key = k0 + mine * box;
-                        const int32_t block = table[key >> page_shift];
                         if (block < 0 || block >= a.n_blocks) {
                             flag(p.status, KDA_DEV_BAD_SLOT);
-                            row = (int32_t)(a.n_blocks * a.n_kv_heads * a.block_size);     // past the end: reads zeros
+                            rows8 = (int32_t)(a.n_blocks * a.n_kv_heads * (a.block_size >> 3));     // past the end: reads zeros
                         } else {
-                            row = (int32_t)((block * (int64_t)a.n_kv_heads + it.hk) * a.block_size + (key & (a.block_size - 1)));
+                            rows8 = (int32_t)((block * (int64_t)a.n_kv_heads + it.hk) * (a.block_size >> 3) +
+                                              ((k0 + mine * box & (a.block_size - 1)) >> 3));
                         }
                     }
+                    if (j + 1 < n_tiles) block = look_up(k0 + kTile);
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const uint32_t st = ring.stage;
@@ -562,9 +578,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         if (lane == 0) mbar_expect_tx(&ms.full[st], (uint32_t)(live * box) * 128u * kRegions);
                         __syncwarp();
                         if (mine < live) {
-                            uint8_t* to = dst + region * Sh::kRegion + mine * box * 128;
-                            if (MODE == kPacked) tma_load_3d(to, map, 64 * region, it.hk, it.row0 + k0, &ms.full[st]);
-                            else tma_load_2d(to, map, 64 * region, row, &ms.full[st]);
+                            if (MODE == kPacked) tma_load_3d(dst + region * Sh::kRegion, map, 64 * region, it.hk, it.row0 + k0, &ms.full[st]);
+                            else tma_load_4d(dst + mine * box * 2 * D, map, 0, 0, 0, rows8, &ms.full[st]);
                         }
                         ++issued;
                     }
@@ -601,7 +616,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         auto key_of = [&](int y) { return from + y / (kRegions * 8); };
                         auto piece = [&](int y) {
                             const int z = y % (kRegions * 8);
-                            return reinterpret_cast<uint4*>(v + (z >> 3) * Sh::kRegion + row64_chunk_off(key_of(y), z & 7));
+                            const int key = key_of(y);
+                            return reinterpret_cast<uint4*>(v + (z >> 3) * kColumnStep + (key >> 3) * kRowStep + row64_chunk_off(key & 7, z & 7));
                         };
                         bool hit = false;
 #pragma unroll 4
@@ -842,55 +858,55 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.o_free[q]);
                 }
-                if (SPLIT) {
+                if constexpr (SPLIT) {
                     float4* to = reinterpret_cast<float4*>(out) + x / 4;
                     if (live)
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             to[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
                                                 __uint_as_float(o[4 * k + 3]));
-                    continue;
-                }
-                uint32_t b[4][8];
+                } else {
+                    uint32_t b[4][8];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 y = unpair2(mul2(pair2(o[2 * k], o[2 * k + 1]), inv2));
-                    b[k >> 3][k & 7] = pack_bf16(y.x, y.y);
-                }
-                if (wide) {
-                    // Four lanes trade 32-byte pieces, so that together they write 128 bytes of
-                    // one row at a time: a store instruction takes a cycle a line.  Lane x of the
-                    // four puts piece x ^ y in place y; from lane x ^ y that is that row's piece x.
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 y = unpair2(mul2(pair2(o[2 * k], o[2 * k + 1]), inv2));
+                        b[k >> 3][k & 7] = pack_bf16(y.x, y.y);
+                    }
+                    if (wide) {
+                        // Four lanes trade 32-byte pieces, so that together they write 128 bytes of
+                        // one row at a time: a store instruction takes a cycle a line.  Lane x of the
+                        // four puts piece x ^ y in place y; from lane x ^ y that is that row's piece x.
 #pragma unroll
-                    for (int bit = 1; bit < 4; bit <<= 1) {
-                        const bool up = lane & bit;
+                        for (int bit = 1; bit < 4; bit <<= 1) {
+                            const bool up = lane & bit;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
+                            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    if (!(y & bit)) {
+                                        const uint32_t lo = b[y][k], hi = b[y | bit][k];
+                                        b[y][k] = up ? hi : lo;
+                                        b[y | bit][k] = up ? lo : hi;
+                                    }
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                if (!(y & bit)) {
-                                    const uint32_t lo = b[y][k], hi = b[y | bit][k];
-                                    b[y][k] = up ? hi : lo;
-                                    b[y | bit][k] = up ? lo : hi;
-                                }
+                                if (y > 0) b[y][k] = __shfl_xor_sync(0xffffffffu, b[y][k], y);
+                            char* to = reinterpret_cast<char*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), y));
+                            if (to)
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * x + 32 * (lane & 3)),
+                                             "r"(b[y][0]), "r"(b[y][1]), "r"(b[y][2]), "r"(b[y][3]), "r"(b[y][4]), "r"(b[y][5]),
+                                             "r"(b[y][6]), "r"(b[y][7])
+                                             : "memory");
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            reinterpret_cast<uint4*>(out + 2 * x)[y] = make_uint4(b[y >> 1][4 * (y & 1)], b[y >> 1][4 * (y & 1) + 1],
+                                                                                  b[y >> 1][4 * (y & 1) + 2], b[y >> 1][4 * (y & 1) + 3]);
                     }
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (y > 0) b[y][k] = __shfl_xor_sync(0xffffffffu, b[y][k], y);
-                        char* to = reinterpret_cast<char*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), y));
-                        if (to)
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * x + 32 * (lane & 3)),
-                                         "r"(b[y][0]), "r"(b[y][1]), "r"(b[y][2]), "r"(b[y][3]), "r"(b[y][4]), "r"(b[y][5]),
-                                         "r"(b[y][6]), "r"(b[y][7])
-                                         : "memory");
-                    }
-                } else if (live) {
-#pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        reinterpret_cast<uint4*>(out + 2 * x)[y] = make_uint4(b[y >> 1][4 * (y & 1)], b[y >> 1][4 * (y & 1) + 1],
-                                                                              b[y >> 1][4 * (y & 1) + 2], b[y >> 1][4 * (y & 1) + 3]);
                 }
             }
             if (live) {
@@ -934,7 +950,7 @@ EncodeTiledFn encode_fn() {
 bool make_map(CUtensorMap* m, const void* base, uint32_t rank, const cuuint64_t* dims, const cuuint64_t* strides,
               const cuuint32_t* box) {
     const EncodeTiledFn fn = encode_fn();
-    const cuuint32_t one[3] = {1, 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
     return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -949,11 +965,14 @@ bool token_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int 
     return make_map(m, base, 3, dims, strides, box);
 }
 
+// The cache's rows in eights, a page (or 128 rows of one) a box: 64 columns x 8 rows x the
+// columns' 64s x the eights.
 bool cache_map(CUtensorMap* m, const void* base, const kda_attn_prefill_args& a) {
-    const cuuint64_t dims[2] = {(cuuint64_t)a.d, (cuuint64_t)(a.n_blocks * a.n_kv_heads * a.block_size)};
-    const cuuint64_t strides[1] = {(cuuint64_t)a.d * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)(a.block_size < kTile ? a.block_size : kTile)};
-    return make_map(m, base, 2, dims, strides, box);
+    const cuuint64_t row = (cuuint64_t)a.d * 2;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)a.d / 64, (cuuint64_t)(a.n_blocks * a.n_kv_heads * (a.block_size / 8))};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)a.d / 64, (cuuint32_t)(a.block_size < kTile ? a.block_size : kTile) / 8};
+    return make_map(m, base, 4, dims, strides, box);
 }
 
 template <int D, int MODE, bool SPLIT>

@@ -1,6 +1,6 @@
 // C entry points of kda_attention.h: argument checks and dispatch.
-#include <cstdarg>
 #include <cmath>
+#include <cstdarg>
 #include <cstdio>
 
 #include "attn_common.cuh"
@@ -102,16 +102,27 @@ int decode_pieces(const kda_attn_decode_args& a) {
     return (int)(pieces < kda::kDecodePieces ? pieces : kda::kDecodePieces);
 }
 
-// Blocks of keys that a shared prefix is cut into: bf16 enough for a thread block (256
-// rows) on each of 152 SMs, fp32 enough for one (64 rows) on every second one, whose
-// blocks then split up further (attn_simt.cu); at most 64.
+// What one more block of a shared prefix costs its rows' joins, in the unit of
+// prefix_block_tiles.  Fitted to the best of 1 to 32 blocks for 8 to 300 sequences of 16
+// and 40 heads behind 512 to 32768 positions (bf16, d = 128: 300 x 40 heads behind 512, one
+// block 142 us and four 215 us; 8 x 40 heads behind 8192, one 110 us and eight 29 us.
+// fp32: 83 x 16 behind 2048, one 288 us, eight 118 us, 32 170 us).
+float prefix_split_cost(const kda_attn_decode_args& a) {
+    return (a.dtype == KDA_BF16 ? 0.16f : 0.1f) * ((float)a.n_seqs * (float)a.n_heads + 300.f);
+}
+
+// Blocks of keys that a shared prefix is cut into at most: bf16 a thread block (256 rows)
+// for each of 152 SMs, fp32 two (64 rows), no more than the longest prefix that the table
+// can hold would be cut into, and 64.
 int prefix_splits(const kda_attn_decode_args& a) {
     if (a.n_groups == 0) return 0;
     const bool bf16 = a.dtype == KDA_BF16;
     const int64_t G = a.n_heads / a.n_kv_heads;
     const int64_t items = ((int64_t)a.n_seqs * G / (bf16 ? 256 : 64) + a.n_groups) * a.n_kv_heads;
-    const int64_t n = bf16 ? (152 + items - 1) / items : 76 / items;
-    return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+    const int64_t n = bf16 ? (152 + items - 1) / items : 304 / items;
+    const int64_t most = 1 + (int64_t)sqrtf((float)a.table_stride * (float)a.block_size / prefix_split_cost(a));
+    const int64_t r = n < most ? n : most;
+    return (int)(r < 1 ? 1 : r > 64 ? 64 : r);
 }
 
 // Blocks of keys that a prompt's tiles are cut into: several where the row tiles (256
@@ -269,7 +280,7 @@ kda_status_t kda_attn_prefill(const kda_attn_prefill_args* args, void* stream) {
         KDA_TRY(check_ptr(a.k, "k"));
         KDA_TRY(check_ptr(a.v, "v"));
     }
-    kda::AttnTileLaunch p{a, nullptr, nullptr, 1, nullptr, nullptr};
+    kda::AttnTileLaunch p{a, nullptr, nullptr, 1, 0.f, nullptr, nullptr};
     KDA_TRY(kda::device_status_word(&p.status));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int n = prompt_splits(a);
@@ -323,6 +334,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
     p.a = a;
     p.n_pieces = decode_pieces(a);
     p.n_split = prefix_splits(a);
+    p.split_cost = prefix_split_cost(a);
     p.prefix_tile = a.dtype == KDA_BF16 ? kda::kTileKeysBf16 : kda::kTileKeysF32;
     p.pre_o = reinterpret_cast<float*>(ws + sp.pre_o);
     p.pre_ml = reinterpret_cast<float2*>(ws + sp.pre_ml);
@@ -349,6 +361,7 @@ kda_status_t kda_attn_decode(const kda_attn_decode_args* args, void* stream) {
         t.status = p.status;
         t.prefix_lens = a.prefix_lens;
         t.n_split = p.n_split;
+        t.split_cost = p.split_cost;
         t.part_o = p.pre_o;
         t.part_ml = p.pre_ml;
         e = kda::launch_attn_tile(t, s);

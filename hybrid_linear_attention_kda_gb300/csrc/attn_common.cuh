@@ -101,9 +101,20 @@ struct AttnTileLaunch {
     // Shared prefixes, and prompts where n_split > 1: the keys are cut into n_split blocks, with partial results in
     // part_o [n_split, total_tokens, H, d] (unnormalised) and part_ml [n_split, total_tokens, H] (m, l).
     int32_t n_split;
+    float split_cost;             // shared prefixes: prefix_block_tiles
     float* part_o;
     float2* part_ml;
 };
+
+// A shared prefix's keys are cut into n_split blocks, or fewer of at least sqrt(keys *
+// split_cost) keys.  A block's time is its keys', and each block is one more partial
+// result to join for every row of the batch, so that the sum of the two is least for
+// blocks of that many; split_cost goes with the rows (prefix_split_cost).
+__host__ __device__ __forceinline__ uint32_t prefix_block_tiles(uint32_t keys, uint32_t tile, uint32_t n_split, float split_cost) {
+    const uint32_t even = ((keys + tile - 1) / tile + n_split - 1) / n_split;
+    const uint32_t least = (uint32_t)(sqrtf((float)keys * split_cost) / (float)tile);
+    return even > least ? (even > 1 ? even : 1) : (least > 1 ? least : 1);
+}
 
 // Prompt attention, and the shared-prefix part of decode attention (prefix_lens set).
 constexpr int kTileKeysF32 = 64, kTileKeysBf16 = 128;                    // keys of a tile
@@ -120,6 +131,7 @@ struct AttnDecodeLaunch {
     int32_t n_pieces;             // workers of the suffix kernel
     int32_t n_split;              // key blocks of the prefix (0: no groups)
     int32_t prefix_tile;          // keys of a tile of the prefix kernel, which the blocks are made of
+    float split_cost;             // prefix_block_tiles
     float* pre_o;                 // [n_split, n_seqs, H, d] the prefix's partial results
     float2* pre_ml;               // [n_split, n_seqs, H]
     float* part_o;                // [2 * n_pieces, rows, d]: a piece's first unit, its last unit

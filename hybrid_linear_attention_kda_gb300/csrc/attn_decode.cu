@@ -240,33 +240,51 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
         const int n_pre = whole ? prefix_parts(p, info.x) : 0;
         if (n_pre > 0) griddep_wait();                   // the prefix's results
         const int64_t slot = part_slot(piece, k_first == 0);
+        float lt[R], mt[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            // every key's lanes hold its weight: one of them counts
+            lt[r] = my_part == 0 ? l[r] : 0.f, mt[r] = m[r];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) lt[r] += __shfl_xor_sync(0xffffffffu, lt[r], off);
+            if (lt[r] == 0.f) mt[r] = -CUDART_INF_F;
+        }
+#pragma unroll 1
+        for (int i = 0; i < n_pre; ++i) {
+            float2 ml[R], v[R][kCols / 2];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r >= rows) break;
+                const int64_t pr = prefix_row(p, i, s, head0 + r);
+                ml[r] = load_now2(p.pre_ml + pr);
+#pragma unroll
+                for (int e = 0; e < kCols / 2; ++e) v[r][e] = load_now2(p.pre_o + pr * D + kCols * lane + 2 * e);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r >= rows) break;
+                float w1, w2;
+                join(mt[r], lt[r], ml[r].x, ml[r].y, w1, w2);
+#pragma unroll
+                for (int e = 0; e < kCols / 2; ++e) {
+                    o[r][2 * e] = o[r][2 * e] * w1 + v[r][e].x * w2;
+                    o[r][2 * e + 1] = o[r][2 * e + 1] * w1 + v[r][e].y * w2;
+                }
+            }
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r >= rows) break;
-            // every key's lanes hold its weight: one of them counts
-            float lt = my_part == 0 ? l[r] : 0.f, mt = m[r];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
-            if (lt == 0.f) mt = -CUDART_INF_F;
-#pragma unroll 2
-            for (int i = 0; i < n_pre; ++i) {
-                const int64_t pr = prefix_row(p, i, s, head0 + r);
-                const float2 ml = p.pre_ml[pr];
-                float w1, w2;
-                join(mt, lt, ml.x, ml.y, w1, w2);
-#pragma unroll
-                for (int e = 0; e < kCols; ++e) o[r][e] = o[r][e] * w1 + p.pre_o[pr * D + kCols * lane + e] * w2;
-            }
             float* out = whole ? static_cast<float*>(a.o) + s * a.o_stride + (int64_t)(head0 + r) * D : p.part_o + (slot * R + r) * D;
-            const float f = !whole ? 1.f : lt == 0.f ? 0.f : 1.f / lt;
+            const float f = !whole ? 1.f : lt[r] == 0.f ? 0.f : 1.f / lt[r];
 #pragma unroll
             for (int e = 0; e < kCols; ++e) out[kCols * lane + e] = o[r][e] * f;
             if (lane == 0) {
-                if (whole) write_lse(a, s, head0 + r, mt, lt);
-                else p.part_ml[slot * R + r] = make_float2(mt, lt);
+                if (whole) write_lse(a, s, head0 + r, mt[r], lt[r]);
+                else p.part_ml[slot * R + r] = make_float2(mt[r], lt[r]);
             }
         }
-        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, line);
+        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(p, c, piece, line);
         c.next_unit(p, kKeys);
     }
     copy_wait<0>();

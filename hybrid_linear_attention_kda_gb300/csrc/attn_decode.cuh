@@ -165,46 +165,99 @@ __device__ __forceinline__ void join(float& m, float& l, float m2, float l2, flo
 __device__ __forceinline__ int prefix_parts(const AttnDecodeLaunch& p, int shared) {
     if (shared <= 0) return 0;
     const uint32_t tiles = ((uint32_t)shared + p.prefix_tile - 1) / p.prefix_tile;
-    const uint32_t per = (tiles + p.n_split - 1) / p.n_split;
+    const uint32_t per = prefix_block_tiles(shared, p.prefix_tile, p.n_split, p.split_cost);
     return (int)((tiles + per - 1) / per);
 }
 __device__ __forceinline__ int64_t prefix_row(const AttnDecodeLaunch& p, int i, int32_t s, int head) {
     return ((int64_t)i * p.a.n_seqs + s) * p.a.n_heads + head;
 }
+// Loads that are issued where they stand: a unit's end reads the prefix's results from L2,
+// and among the results' stores the compiler asks for them a row at a time (53 requests of
+// up to 5 fp32 tokens behind 256, 15/3 heads: 53 us, 47 us with these).
+__device__ __forceinline__ float2 load_now2(const void* p) {
+    float2 v;
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
 __device__ __forceinline__ void write_lse(const kda_attn_decode_args& a, int32_t s, int head, float m, float l) {
     if (a.lse) a.lse[(int64_t)s * a.n_heads + head] = l == 0.f ? -CUDART_INF_F : fmaf(m, kLn2, logf(l));
 }
 
-// A worker's end: sequences without a suffix give zeros, or the prefix's results.
-// Worker w of n takes every n-th sequence, a lane D / 32 columns.  Also reports bad
-// lengths.
+// (m, l, o) of one row as a warp holds it, D / 32 columns a lane, and partial results
+// added to it.  They come from L2, a microsecond away: four are asked for at a time.
+template <int D> struct RowSum {
+    static constexpr int kCols = D / 32;
+    float m, l, o[kCols];
+
+    __device__ __forceinline__ RowSum() {
+        m = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) o[e] = 0.f;
+    }
+    __device__ __forceinline__ void add(float2 ml, const float (&x)[kCols]) {
+        float w, w2;
+        join(m, l, ml.x, ml.y, w, w2);
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) o[e] = o[e] * w + x[e] * w2;
+    }
+    // Parts from .. to - 1 in turn; where(i, ml, o) names the i-th one's place.
+    template <typename Where> __device__ __forceinline__ void add_parts(int64_t from, int64_t to, int lane, Where where) {
+        constexpr int kAtOnce = 4;
+        for (int64_t i = from; i < to; i += kAtOnce) {
+            float2 ml[kAtOnce];
+            alignas(8) float x[kAtOnce][kCols];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                ml[k] = make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) x[k][e] = 0.f;
+                if (i + k < to) {
+                    const float2* from_ml;
+                    const float* from_o;
+                    where(i + k, from_ml, from_o);
+                    ml[k] = *from_ml;
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 2)
+                        *reinterpret_cast<float2*>(&x[k][e]) = *reinterpret_cast<const float2*>(from_o + lane * kCols + e);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (i + k < to) add(ml[k], x[k]);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void write(const kda_attn_decode_args& a, int32_t s, int head, int lane) const {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + lane * kCols;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) Elem<T>::store(out + e, o[e] * inv);
+        if (lane == 0) write_lse(a, s, head, m, l);
+    }
+};
+
+// A worker's end: sequences without a suffix give zeros, or the prefix's results.  The
+// heads of one sequence are spread over as many workers as there are for it.  Also
+// reports bad lengths.
 template <typename T, int D>
-__device__ void finish_empty(const AttnDecodeLaunch& p, int64_t w, int lane) {
-    constexpr int kCols = D / 32;
+__device__ void finish_empty(const AttnDecodeLaunch& p, int64_t worker, int lane) {
     griddep_wait();
-    const int64_t n = p.n_pieces;
     const kda_attn_decode_args& a = p.a;
-    for (int64_t s = w; s < a.n_seqs; s += n) {
-        const int2 info = seq_info(p, (int32_t)s);
-        if (a.n_groups == 0 && info.y != a.kv_lens[s] && lane == 0) flag(p.status, KDA_DEV_BAD_SEQLENS);
+    const int n = p.n_pieces, w = (int)worker, each = max(1, n / a.n_seqs);
+    const int part = a.n_seqs < n ? w / a.n_seqs : 0;
+    if (part >= each) return;
+    for (int32_t s = a.n_seqs < n ? w % a.n_seqs : w; s < a.n_seqs; s += n) {
+        const int2 info = seq_info(p, s);
+        if (a.n_groups == 0 && info.y != a.kv_lens[s] && lane == 0 && part == 0) flag(p.status, KDA_DEV_BAD_SEQLENS);
         if (info.y > info.x) continue;
         const int n_pre = prefix_parts(p, info.x);
-        for (int head = 0; head < a.n_heads; ++head) {
-            float m = -CUDART_INF_F, l = 0.f, o[kCols] = {};
-#pragma unroll 4
-            for (int i = 0; i < n_pre; ++i) {
-                const int64_t at = prefix_row(p, i, (int32_t)s, head);
-                const float2 ml = p.pre_ml[at];
-                float w1, w2;
-                join(m, l, ml.x, ml.y, w1, w2);
-#pragma unroll
-                for (int e = 0; e < kCols; ++e) o[e] = o[e] * w1 + p.pre_o[at * D + lane * kCols + e] * w2;
-            }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + lane * kCols;
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) Elem<T>::store(out + e, o[e] * inv);
-            if (lane == 0) write_lse(a, (int32_t)s, head, m, l);
+        for (int head = part; head < a.n_heads; head += each) {
+            RowSum<D> sum;
+            sum.add_parts(0, n_pre, lane, [&](int64_t i, const float2*& ml, const float*& o) {
+                const int64_t at = prefix_row(p, (int)i, s, head);
+                ml = p.pre_ml + at;
+                o = p.pre_o + at * D;
+            });
+            sum.template write<T>(a, s, head, lane);
         }
     }
 }
@@ -212,8 +265,10 @@ __device__ void finish_empty(const AttnDecodeLaunch& p, int64_t w, int lane) {
 constexpr int kJoinWarps = 8;
 
 // Thread block c joins the unit that begins in piece c and ends in a later one, if
-// there is one.  Its warps are spread over the unit's rows, and over its parts when
-// there are fewer rows than warps; a lane takes D / 32 columns.
+// there is one.  Its warps are spread over the unit's rows, and over its parts (the
+// prefix's, then the pieces') when there are fewer rows than warps.  Bound by three
+// trips to L2 and its launch: 83 requests of up to 863 tokens, 40/8 heads take 43 us with
+// both kernels (47 us with the parts read one by one).
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ AttnDecodeLaunch p) {
     constexpr int kCols = D / 32;
@@ -223,58 +278,47 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const kda_attn_decode_args& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c0 = blockIdx.x;
-    const int4 open = p.open[c0];                        // sequence (-1: none), unit, last piece
+    const int4 open = p.open[c0];                        // sequence (-1: none), unit, last piece, prefix parts
     if (open.x < 0) return;
     const int32_t s = open.x;
-    const int64_t parts = open.z - c0 + 1;
+    const int n_pre = open.w;
+    const int64_t parts = n_pre + open.z - c0 + 1;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + ROWS - 1) / ROWS;
     const int hk = open.y / blocks, rb = open.y % blocks;
     const int head0 = hk * G + rb * ROWS, rows = min(ROWS, G - rb * ROWS);
-    const int n_pre = prefix_parts(p, seq_info(p, s).x);
-    const int row_warps = rows >= 8 ? 8 : rows >= 4 ? 4 : rows >= 2 ? 2 : 1, part_warps = kJoinWarps / row_warps;
+    const int row_warps = rows > 4 ? 8 : rows > 2 ? 4 : rows, part_warps = kJoinWarps / row_warps;
     const int r0 = warp % row_warps, pw = warp / row_warps;
     const int64_t per = (parts + part_warps - 1) / part_warps;
     for (int r = r0; r - r0 < rows; r += row_warps) {    // every warp the same number of times
         const int head = head0 + r;
-        float m = -CUDART_INF_F, l = 0.f, o[kCols] = {};
-        auto add = [&](const float2 ml, const float* src) {
-            float x[kCols];
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) x[e] = src[lane * kCols + e];
-            float w, w2;
-            join(m, l, ml.x, ml.y, w, w2);
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = o[e] * w + x[e] * w2;
-        };
-        if (r < rows) {
-            if (pw == 0)
-#pragma unroll 4
-                for (int i = 0; i < n_pre; ++i) {
-                    const int64_t at = prefix_row(p, i, s, head);
-                    add(p.pre_ml[at], p.pre_o + at * D);
+        RowSum<D> sum;
+        if (r < rows)
+            sum.add_parts(pw * per, min(parts, (pw + 1) * per), lane, [&](int64_t i, const float2*& ml, const float*& o) {
+                if (i < n_pre) {
+                    const int64_t at = prefix_row(p, (int)i, s, head);
+                    ml = p.pre_ml + at;
+                    o = p.pre_o + at * D;
+                } else {
+                    const int64_t at = part_slot(c0 + i - n_pre, i == n_pre) * ROWS + r;
+                    ml = p.part_ml + at;
+                    o = p.part_o + at * D;
                 }
-            const int64_t last = min(parts, (pw + 1) * per);
-#pragma unroll 8
-            for (int64_t i = pw * per; i < last; ++i) {
-                const int64_t at = part_slot(c0 + i, i == 0) * ROWS + r;
-                add(p.part_ml[at], p.part_o + at * D);
-            }
-        }
+            });
         if (part_warps > 1) {
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) s_o[warp][lane * kCols + e] = o[e];
-            if (lane == 0) s_ml[warp] = make_float2(m, l);
+            for (int e = 0; e < kCols; ++e) s_o[warp][lane * kCols + e] = sum.o[e];
+            if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
             __syncthreads();
             if (pw == 0)
-                for (int i = 1; i < part_warps; ++i) add(s_ml[warp + i * row_warps], s_o[warp + i * row_warps]);
-        }
-        if (pw != 0 || r >= rows) continue;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + lane * kCols;
+                for (int i = 1; i < part_warps; ++i) {
+                    float x[kCols];
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) Elem<T>::store(out + e, o[e] * inv);
-        if (lane == 0) write_lse(a, s, head, m, l);
+                    for (int e = 0; e < kCols; ++e) x[e] = s_o[warp + i * row_warps][lane * kCols + e];
+                    sum.add(s_ml[warp + i * row_warps], x);
+                }
+        }
+        if (pw == 0 && r < rows) sum.template write<T>(a, s, head, lane);
     }
 }
 
@@ -286,10 +330,10 @@ cudaError_t launch_join(const AttnDecodeLaunch& p, cudaStream_t s) {
 
 // Notes for the join whether the last unit of the piece, at cursor c, begins there
 // and goes on in later pieces.
-__device__ __forceinline__ int4 open_unit(const Cursor& c, int64_t piece, const Line& line) {
+__device__ __forceinline__ int4 open_unit(const AttnDecodeLaunch& p, const Cursor& c, int64_t piece, const Line& line) {
     const int64_t rest = c.T - (c.k + c.run());          // its tiles in later pieces
     if (c.k != 0 || rest == 0) return make_int4(-1, 0, 0, 0);
-    return make_int4(c.s, c.u, (int)line.piece_of(line.begin(piece + 1) + rest - 1), 0);
+    return make_int4(c.s, c.u, (int)line.piece_of(line.begin(piece + 1) + rest - 1), prefix_parts(p, c.info.x));
 }
 
 }  // namespace decode

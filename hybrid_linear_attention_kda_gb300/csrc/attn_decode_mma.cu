@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
             }
         }
         __syncwarp();
-        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(c, piece, line);
+        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(p, c, piece, line);
         c.next_unit(p, kKeys);
     }
     copy_wait<0>();

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_consta
     int64_t k_lo = 0, k_hi = min(K, first + rt.t0 + nt);
     if (SPLIT) {
         if (MODE != kPrefix) K = max((int64_t)0, k_hi);      // the tile's keys
-        const int64_t per = ((K + kKeys - 1) / kKeys + p.n_split - 1) / p.n_split * kKeys;
+        const int64_t per = MODE == kPrefix ? (int64_t)prefix_block_tiles((uint32_t)K, kKeys, p.n_split, p.split_cost) * kKeys
+                                            : ((K + kKeys - 1) / kKeys + p.n_split - 1) / p.n_split * kKeys;
         k_lo = min(K, split * per);
         k_hi = min(K, k_lo + per);
     }

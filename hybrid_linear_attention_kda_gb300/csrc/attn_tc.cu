@@ -357,7 +357,7 @@ __device__ bool find_item(const AttnTileLaunch& p, uint32_t block, Place& place,
     const int left = it.n - it.t0;                                         // tokens from the first one on
     auto tiles = [](int32_t keys) { return (int32_t)(((uint32_t)keys + kTile - 1) / kTile); };
     if (MODE == kPrefix) {
-        const int64_t per = (int64_t)(((uint32_t)tiles(K) + p.n_split - 1) / (uint32_t)p.n_split) * kTile;
+        const int64_t per = (int64_t)prefix_block_tiles(K, kTile, p.n_split, p.split_cost) * kTile;
         it.k_lo = (int32_t)min((int64_t)K, it.split * per);
         it.k_hi = it.all_see = (int32_t)min((int64_t)K, it.k_lo + per);
         it.n_keys0 = it.n_keys1 = tiles(it.k_hi - it.k_lo);

@@ -97,8 +97,9 @@ int decode_pieces(const kda_attn_decode_args& a) {
     const int64_t G = a.n_heads / a.n_kv_heads, rows = kda::decode_rows(a.dtype, (int)G);
     const int64_t tiles = ((int64_t)a.table_stride * a.block_size + kda::decode_tile(a.dtype, a.d) - 1) / kda::decode_tile(a.dtype, a.d);
     const int64_t units = (int64_t)a.n_seqs * a.n_kv_heads * ((G + rows - 1) / rows);
-    if (tiles >= kda::kDecodePieces * kda::kDecodeLeastTiles) return kda::kDecodePieces;
-    const int64_t pieces = (units * tiles / kda::kDecodeLeastTiles + kda::kDecodeWarps) / kda::kDecodeWarps * kda::kDecodeWarps;
+    const int least = kda::decode_least_tiles(tiles);
+    if (tiles >= (int64_t)kda::kDecodePieces * least) return kda::kDecodePieces;
+    const int64_t pieces = (units * tiles / least + kda::kDecodeWarps) / kda::kDecodeWarps * kda::kDecodeWarps;
     return (int)(pieces < kda::kDecodePieces ? pieces : kda::kDecodePieces);
 }
 

@@ -139,14 +139,20 @@ struct AttnDecodeLaunch {
     int4* open;                   // [n_pieces] the unit that begins in a piece and goes on
     int2* info;                   // [n_seqs] (shared positions, all positions), where there are groups
 };
-// Query heads of one unit.  fp32: up to four heads of a key/value head cost half of
-// eight in the kernel's arithmetic, which is what bounds it beyond two.
+// Query heads of one unit: bf16 the rows of a product.  fp32: arithmetic on rows that are
+// not there costs as much, so four where no more are needed (33 sequences of up to 2000
+// tokens, 4 key/value heads: four query heads each 38 us, 45 us in units of eight).
 constexpr int kDecodeRowsBf16 = 16;
 constexpr int decode_rows(int dtype, int G) { return dtype == KDA_BF16 ? kDecodeRowsBf16 : G <= 4 ? 4 : 8; }
-// Keys of a tile, and tiles of the shortest piece: a shorter one costs more in the
-// join than it saves.
+// Keys of a tile.
 constexpr int decode_tile(int dtype, int d) { return dtype == KDA_BF16 ? 16 : 1024 / d; }
-constexpr int kDecodeLeastTiles = 4;
+// Tiles of the shortest piece.  Pieces share the work of a few sequences, but every piece
+// of a unit is one more partial result to join, one by one: units of a few tiles are given
+// a worker each (4 sequences of up to 40 tokens: 10 us, 15 us with pieces of four), long
+// ones pieces of four (one sequence of 4000: 19 us, 35 us with pieces of one).
+__host__ __device__ constexpr int decode_least_tiles(int64_t unit_tiles) {
+    return unit_tiles < 16 ? 1 : unit_tiles < 48 ? 2 : 4;
+}
 constexpr int kDecodeWarps = 8, kDecodePieces = kDecodeWarps * 152;   // workers: eight warps on each of 152 SMs
 cudaError_t launch_decode_info(const AttnDecodeLaunch& p, cudaStream_t s);   // p.info, where there are groups
 cudaError_t launch_decode_simt(const AttnDecodeLaunch& p, cudaStream_t s);   // fp32

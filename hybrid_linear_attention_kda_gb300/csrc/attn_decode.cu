@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + R - 1) / R;
     __shared__ PieceStart at_[kWarps];
-    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kDecodeLeastTiles, at_);
+    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, at_);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
     if (piece >= line.pieces) {

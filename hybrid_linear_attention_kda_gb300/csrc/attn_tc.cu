@@ -253,6 +253,37 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// Writes 128 bytes at `byte` of each lane's row (none where row is NULL).  Four lanes trade
+// their rows' 32-byte pieces, so that together they write one row at a time: a store
+// instruction takes a cycle a line.  Lane x of the four puts piece x ^ y in place y; what
+// comes from lane x ^ y is that row's piece x.
+__device__ __forceinline__ void write_traded(uint32_t (&b)[4][8], char* row, int byte, int lane) {
+#pragma unroll
+    for (int bit = 1; bit < 4; bit <<= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (!(y & bit)) {
+                    const uint32_t lo = b[y][k], hi = b[y | bit][k];
+                    b[y][k] = up ? hi : lo;
+                    b[y | bit][k] = up ? lo : hi;
+                }
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (y > 0) b[y][k] = __shfl_xor_sync(0xffffffffu, b[y][k], y);
+        char* to = reinterpret_cast<char*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), y));
+        if (to)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + byte + 32 * (lane & 3)), "r"(b[y][0]),
+                         "r"(b[y][1]), "r"(b[y][2]), "r"(b[y][3]), "r"(b[y][4]), "r"(b[y][5]), "r"(b[y][6]), "r"(b[y][7])
+                         : "memory");
+    }
+}
+
 // A place in the ring of stages, as it moves from load to load: one warp's scalar
 // arithmetic between two MMAs is time that the tensor pipe waits.
 struct Ring {
@@ -877,49 +908,22 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.o_free[q]);
                 }
+                uint32_t b[4][8];
                 if constexpr (SPLIT) {
-                    float4* to = reinterpret_cast<float4*>(out) + x / 4;
-                    if (live)
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            to[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                                                __uint_as_float(o[4 * k + 3]));
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) b[k >> 3][k & 7] = o[32 * half + k];
+                        write_traded(b, out, 4 * x + 128 * half, lane);
+                    }
                 } else {
-                    uint32_t b[4][8];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         const float2 y = unpair2(mul2(pair2(o[2 * k], o[2 * k + 1]), inv2));
                         b[k >> 3][k & 7] = pack_bf16(y.x, y.y);
                     }
                     if (wide) {
-                        // Four lanes trade 32-byte pieces, so that together they write 128 bytes of
-                        // one row at a time: a store instruction takes a cycle a line.  Lane x of the
-                        // four puts piece x ^ y in place y; from lane x ^ y that is that row's piece x.
-#pragma unroll
-                        for (int bit = 1; bit < 4; bit <<= 1) {
-                            const bool up = lane & bit;
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    if (!(y & bit)) {
-                                        const uint32_t lo = b[y][k], hi = b[y | bit][k];
-                                        b[y][k] = up ? hi : lo;
-                                        b[y | bit][k] = up ? lo : hi;
-                                    }
-                        }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (y > 0) b[y][k] = __shfl_xor_sync(0xffffffffu, b[y][k], y);
-                            char* to = reinterpret_cast<char*>(__shfl_xor_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), y));
-                            if (to)
-                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * x + 32 * (lane & 3)),
-                                             "r"(b[y][0]), "r"(b[y][1]), "r"(b[y][2]), "r"(b[y][3]), "r"(b[y][4]), "r"(b[y][5]),
-                                             "r"(b[y][6]), "r"(b[y][7])
-                                             : "memory");
-                        }
+                        write_traded(b, out, 2 * x, lane);
                     } else if (live) {
 #pragma unroll
                         for (int y = 0; y < 8; ++y)

@@ -30,7 +30,13 @@
 // infinite or NaN v.  In the tiles that some row sees only a part of, warp 10
 // therefore zeroes the values of keys that no row sees, and replaces the non-finite
 // values of the others by zero and notes the first key of each column that held a
-// NaN, +inf or -inf; at the end, rows that see such a key get it added.
+// NaN, +inf or -inf; at the end, rows that see such a key get it added.  The notes are
+// those of one item.  Before they are made anew, warp 10 waits until every softmax warp
+// has counted all earlier items as read.  That wait ends whatever the roles have reached:
+// a softmax warp reads its notes once its products are done, and those of earlier items
+// need nothing of warp 10 that is not done before.  A barrier would not do: row tile 0
+// may be past the item by then (keys that only row tile 1 sees), and row tiles may be
+// two items behind, so that a phase's parity says neither.
 //
 // Bound by the tensor pipe where sequences are long: 4 d flops per (row, key) pair.
 // Measured on 4 x 8192 tokens, 32 query and 8 key/value heads, d = 128: 1.30 ms, 1690
@@ -99,11 +105,13 @@ template <int D> struct Misc {
     alignas(16) uint4 next_block;                                 // clusterlaunchcontrol's answer
     Item item[2];
     uint32_t tslot;
+    uint32_t items_read[kMmaWarp];                                // items whose notes each softmax warp is done with
     int32_t poison;                                               // the item that the notes below belong to
     int32_t first_nan[D], first_pos[D], first_neg[D];             // first key of a column that holds such a value
 };
 
 template <int D> constexpr size_t smem_bytes() { return Shape<D>::kMisc + sizeof(Misc<D>) + 1024; }
+static_assert(smem_bytes<64>() <= 227 * 1024 && smem_bytes<128>() <= 227 * 1024, "a thread block's shared memory");
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -192,6 +200,21 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return true;
     const uint32_t t0 = (uint32_t)clock();
     while (!mbar_test(bar, parity))
+        if ((uint32_t)clock() - t0 > kWaitCycles) return false;
+    return true;
+}
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+    uint32_t x;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(smem_u32(p)) : "memory");
+    return x;
+}
+__device__ __forceinline__ void store_release(uint32_t* p, uint32_t x) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(x) : "memory");
+}
+// Until a count has reached `least`, as long as wait().
+__device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t least) {
+    const uint32_t t0 = (uint32_t)clock();
+    while (load_acquire(p) < least)
         if ((uint32_t)clock() - t0 > kWaitCycles) return false;
     return true;
 }
@@ -456,6 +479,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         mbar_init(&ms.q_full, 1);
         mbar_init(&ms.q_free, 1);
         mbar_init(&ms.drained, 1);
+        for (int w = 0; w < kMmaWarp; ++w) ms.items_read[w] = 0;
         ms.poison = -1;
         fence_mbar_init();
     }
@@ -646,7 +670,6 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             // no barrier gets two phases ahead of its waits.
             Ring ring;
             bool ok = true;
-            uint32_t o_items[2] = {0, 0};                         // items before this one that each row tile takes part in
             Item it;
             for (uint32_t i = 0; ok && get_item(i, it); ++i) {
                 const int n_tiles = it.n_tiles, first_edge = it.edge;
@@ -682,9 +705,9 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         }
                         if (__any_sync(0xffffffffu, hit)) {
                             if (!noted) {
-                                // the notes may still be read for the item before
-                                for (int q = 0; q < 2 && ok; ++q)
-                                    if (o_items[q] > 0) ok = wait_all(&ms.o_free[q], (o_items[q] - 1) & 1);
+                                // the notes may still be read for earlier items
+                                ok = __all_sync(0xffffffffu, lane >= kMmaWarp || wait_count(&ms.items_read[lane], i));
+                                late |= !ok;
                                 if (!ok) break;
                                 for (int d = lane; d < D; d += 32) ms.first_nan[d] = ms.first_pos[d] = ms.first_neg[d] = INT_MAX;
                                 if (lane == 0) ms.poison = (int32_t)i;
@@ -709,7 +732,6 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                     }
                     if (lane == 0) mbar_arrive(&ms.empty[st]);
                 }
-                for (int q = 0; q < 2; ++q) o_items[q] += it.n_keys(q) > 0;
             }
         } else {
             // -------------------------------------------------------------- items
@@ -892,6 +914,8 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 for (int x = 0; x < D; x += 16) tmem_st16(tO(q) + lanes + x, zero);
                 tmem_wait_st();
             }
+            __syncwarp();
+            if (lane == 0) store_release(&ms.items_read[warp], i + 1);
             const float m2 = l == 0.f ? -CUDART_INF_F : m * c;
             char* out = SPLIT ? reinterpret_cast<char*>(p.part_o + at * D)
                               : reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.o) + row * a.o_stride + (int64_t)head * D);

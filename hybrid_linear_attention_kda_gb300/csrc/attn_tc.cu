@@ -106,7 +106,7 @@ template <int D> struct Misc {
     Item item[2];
     uint32_t tslot;
     uint32_t items_read[kMmaWarp];                                // items whose notes each softmax warp is done with
-    int32_t poison;                                               // the item that the notes below belong to
+    uint32_t poison;                                              // the item that the notes below belong to
     int32_t first_nan[D], first_pos[D], first_neg[D];             // first key of a column that holds such a value
 };
 
@@ -480,7 +480,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         mbar_init(&ms.q_free, 1);
         mbar_init(&ms.drained, 1);
         for (int w = 0; w < kMmaWarp; ++w) ms.items_read[w] = 0;
-        ms.poison = -1;
+        ms.poison = ~0u;
         fence_mbar_init();
     }
     fence_before_sync();
@@ -710,7 +710,10 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                                 late |= !ok;
                                 if (!ok) break;
                                 for (int d = lane; d < D; d += 32) ms.first_nan[d] = ms.first_pos[d] = ms.first_neg[d] = INT_MAX;
-                                if (lane == 0) ms.poison = (int32_t)i;
+                                __syncwarp();
+                                // the item's number last: row tile 0 reads it without waiting for key tiles
+                                // that it does not see, and must not take an earlier item's notes for these
+                                if (lane == 0) store_release(&ms.poison, i);
                                 noted = true;
                                 __syncwarp();
                             }
@@ -891,7 +894,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                 __syncwarp();
                 o_phase ^= 1;
                 fence_after_sync();
-                if (MODE != kPrefix && *(volatile int32_t*)&ms.poison == (int32_t)i) {
+                if (MODE != kPrefix && __shfl_sync(0xffffffffu, load_acquire(&ms.poison), 0) == i) {
 #pragma unroll 1
                     for (int x = 0; x < D; x += 16) {
                         uint32_t y[16];

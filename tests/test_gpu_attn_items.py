@@ -49,6 +49,20 @@ def test_values_that_only_the_second_row_tile_sees(kda, cuda_device, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_notes_of_earlier_items_are_forgotten(kda, cuda_device, d):
+    """In the same column throughout: items that hold a value at their first key, in turn with items that
+    hold another one only where the second row tile sees it, and with items that hold none."""
+    n, L, H = 120, 256, 8
+    lens = [L] * n
+    q, k, v = A.packed(37, lens, H, H, d, BF, cuda_device)
+    cu = A.cu_of(lens, cuda_device)
+    rng = np.random.RandomState(38)
+    key = lambda s: 0 if s % 2 else 128 + rng.randint(128)
+    marks = [(key(s), d - 1, KINDS[s // 2 % 3]) if s % 5 else None for s in range(n)]
+    _check(kda, lambda: kda.attn_prefill(q, k, v, cu, want_lse=True), lambda s, key: v[s * L + key], marks, lens, [0] * n, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_ragged_items(kda, cuda_device, d):
     """Items of one to several key tiles, with and without such values, at keys of both row tiles."""
     rng = np.random.RandomState(32)

@@ -38,6 +38,11 @@
 // may be past the item by then (keys that only row tile 1 sees), and row tiles may be
 // two items behind, so that a phase's parity says neither.
 //
+// The softmax warps' tensor-memory instructions are .sync.aligned: where a branch that goes
+// by the lane (a row's new maximum, a store of some rows, a wait) comes before one, a
+// __syncwarp() stands between.  The masks are selects, without a branch: a __syncwarp()
+// behind them made the compiler spill (4 x 8192 tokens 1.45 -> 1.51 ms).
+//
 // Bound by the tensor pipe where sequences are long: 4 d flops per (row, key) pair.
 // Measured on 4 x 8192 tokens, 32 query and 8 key/value heads, d = 128: 1.30 ms, 1690
 // TFLOP/s.  Items of few tiles are bound by the steps between them, and those by
@@ -860,6 +865,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                         m = mx;
                         const float2 lf = unpair2(l2);
                         l2 = pair2(__float_as_uint(lf.x * f), __float_as_uint(lf.y * f));
+                        __syncwarp();
                         // rare: rescale what was summed so far
 #pragma unroll 1
                         for (int x = j == 0 ? D : 0; x < D; x += 16) {
@@ -907,12 +913,14 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
                             if (seen > ms.first_nan[x + k] || (pos && neg)) add = CUDART_NAN_F;
                             y[k] = __float_as_uint(__uint_as_float(y[k]) + add);
                         }
+                        __syncwarp();
                         tmem_st16(tO(q) + lanes + x, y);
                     }
                     tmem_wait_st();
                 }
             } else {                                               // no keys: zeros
                 const uint32_t zero[16] = {};
+                __syncwarp();
 #pragma unroll 1
                 for (int x = 0; x < D; x += 16) tmem_st16(tO(q) + lanes + x, zero);
                 tmem_wait_st();
@@ -927,6 +935,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
 #pragma unroll 1
             for (int x = 0; x < D; x += 64) {
                 uint32_t o[64];
+                __syncwarp();
                 tmem_ld32(tO(q) + lanes + x, o);
                 tmem_ld32(tO(q) + lanes + x + 32, o + 32);
                 tmem_wait_ld();
@@ -968,6 +977,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         fence_before_sync();
     }
     if (late) flag(p.status, KDA_DEV_WAIT_TIMEOUT);
+    __syncwarp();
     __syncthreads();
     if (warp == kMmaWarp) {
         fence_after_sync();

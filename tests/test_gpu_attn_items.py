@@ -94,3 +94,22 @@ def test_resumed_items(kda, cuda_device, d, bs):
         marks.append((b - 1 - back, rng.randint(d), KINDS[rng.randint(3)]) if b and rng.randint(4) else None)
     _check(kda, lambda: kda.attn_prefill_paged(q, c.k, c.v, c.table, c.kv_lens, cu, want_lse=True),
            lambda s, key: c.v[int(c.table_np[s, key // bs]), :, key % bs], marks, new, [b - a for a, b in picks], d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_a_warp_that_go_separate_ways(kda, cuda_device, d):
+    """Rows move their maximum at different key tiles or never, end inside a warp, and lie on 16 bytes
+    only, so that each lane stores its own."""
+    lens = [300, 41, 129, 517, 77, 256, 3] * 8
+    H, H_kv = 4, 2
+    q, k, v = A.packed(39, lens, H, H_kv, d, BF, cuda_device)
+    T = sum(lens)
+    rng = np.random.RandomState(40)
+    q *= torch.from_numpy(rng.choice([0.0, 0.1, 1.0, 4.0], (T, H, 1))).to(BF).to(cuda_device)
+    k *= torch.from_numpy(rng.choice([0.1, 1.0, 6.0], (T, H_kv, 1), p=[0.5, 0.45, 0.05])).to(BF).to(cuda_device)
+    buf = torch.full((T * (H * d + 8) + 8,), 7.0, dtype=BF, device=cuda_device)
+    o = buf[8:].as_strided((T, H, d), (H * d + 8, d, 1))
+    _, lse = kda.attn_prefill(q, k, v, A.cu_of(lens, cuda_device), o=o, want_lse=True)
+    assert kda.kda_check_status() == 0
+    A.check(o, lse, A.split(q, lens), A.split(k, lens), A.split(v, lens), [0] * len(lens), d ** -0.5, BF)
+    assert (buf[:8] == 7).all() and (buf[8:].view(T, H * d + 8)[:, H * d:] == 7).all()

@@ -13,6 +13,8 @@ updates it in place for every token ("Kimi K3 Tech Intro", section 2.1):
 import ctypes
 import os
 
+from .attention_abi import KDA_DEV_BAD_GROUP, KDA_DEV_NO_BLOCKS, AttnDecodeArgs, AttnPrefillArgs, CachePlanArgs  # noqa: F401
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "libkda.so")
 
@@ -108,9 +110,9 @@ def load():
     lib.kda_snapshot_restore.argtypes = [vp, vp, i64, vp, i32, i32, i32, i32, vp]
     lib.kda_check_status.restype = ctypes.c_int
     lib.kda_check_status.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_uint32)]
-    from . import attention, prefix_cache
+    from . import attention_abi, prefix_cache
     prefix_cache.declare(lib)
-    attention.declare(lib)
+    attention_abi.declare(lib)
     _lib = lib
     return lib
 
@@ -411,13 +413,12 @@ def prefill(q, k, v, alpha, beta, cu_seqlens, total_tokens=None, *, start_pos=No
     return o, final_state
 
 
-_ATTENTION = ("KDA_DEV_NO_BLOCKS", "KDA_DEV_BAD_GROUP", "CachePlanArgs", "AttnPrefillArgs", "AttnDecodeArgs", "CachePlan",
-              "kda_cache_plan", "kda_cache_append", "kda_attn_prefill", "kda_attn_decode",
+_ATTENTION = ("CachePlan", "kda_cache_plan", "kda_cache_append", "kda_attn_prefill", "kda_attn_decode",
               "kda_attn_prefill_workspace_size", "kda_attn_decode_workspace_size", "cache_plan", "attn_prefill", "attn_prefill_paged", "attn_decode")
 
 
 def __getattr__(name):
-    """The attention side's names, from ``attention`` (which imports torch) on first use."""
+    """The attention side's functions, from ``attention`` (which imports torch) on first use."""
     if name in _ATTENTION:
         from . import attention
         globals().update({n: getattr(attention, n) for n in _ATTENTION})

@@ -116,8 +116,8 @@ def cache_plan(cached_lens, new_lens, block_table, free_blocks, free_begin, free
                max_tokens, cu_seqlens=None, kv_lens=None, slot_map=None, positions=None, stream=None):
     """The cache metadata of one step (``kda_cache_plan``).  cached_lens, new_lens int32 [n];
     block_table int32 [n, stride], completed in place; free_blocks int32 [n_free]; free_begin,
-    free_end int32 [1], two different tensors.  The outputs are allocated unless given.
-    Returns a ``CachePlan`` of cu_seqlens [n + 1], kv_lens [n], slot_map and positions
+    free_end int32 [1], two different tensors.  The outputs are allocated unless given, and may
+    not overlap the inputs (kv_lens is not cached_lens).  Returns a ``CachePlan`` of cu_seqlens [n + 1], kv_lens [n], slot_map and positions
     [max_tokens]."""
     if _elsewhere(stream, cached_lens):
         with _on(stream, cached_lens):

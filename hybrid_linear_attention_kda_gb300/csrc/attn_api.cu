@@ -89,6 +89,34 @@ kda_status_t check_scale(float scale) {
     return KDA_OK;
 }
 
+// An int32 array by name.
+struct IntArray {
+    const char* name;
+    const int32_t* at;
+    int64_t n;
+};
+
+// Every thread block of the plan reads all inputs while others write outputs.
+kda_status_t check_plan_overlap(const kda_cache_plan_args& a) {
+    const IntArray in[] = {{"cached_lens", a.cached_lens, a.n_seqs},
+                           {"new_lens", a.new_lens, a.n_seqs},
+                           {"free_blocks", a.free_blocks, a.n_free},
+                           {"free_begin", a.free_begin, 1}};
+    const IntArray out[] = {{"free_end", a.free_end, 1},
+                            {"block_table", a.block_table, (int64_t)a.n_seqs * a.table_stride},
+                            {"kv_lens", a.kv_lens, a.n_seqs},
+                            {"cu_seqlens", a.cu_seqlens, (int64_t)a.n_seqs + 1},
+                            {"slot_map", a.slot_map, a.max_tokens},
+                            {"positions", a.positions, a.max_tokens}};
+    for (const IntArray& x : in)
+        for (const IntArray& y : out) {
+            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.at), y0 = reinterpret_cast<uintptr_t>(y.at);
+            if (x.n > 0 && y.n > 0 && x0 < y0 + 4 * (uintptr_t)y.n && y0 < x0 + 4 * (uintptr_t)x.n)
+                return fail(KDA_ERR_INVALID_ARG, "%s overlaps %s", y.name, x.name);
+        }
+    return KDA_OK;
+}
+
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workers of the suffix kernel: all, or as many as the longest sequences that the
@@ -233,6 +261,7 @@ kda_status_t kda_cache_plan(const kda_cache_plan_args* args, void* stream) {
         KDA_TRY(check_int(a.slot_map, "slot_map"));
         KDA_TRY(check_int(a.positions, "positions"));
     }
+    KDA_TRY(check_plan_overlap(a));
     kda::CachePlanLaunch p{a, nullptr};
     KDA_TRY(kda::device_status_word(&p.status));
     const cudaError_t e = kda::launch_cache_plan(p, static_cast<cudaStream_t>(stream));

@@ -68,7 +68,9 @@ extern "C" {
  * max_tokens, so that the call can be replayed at a fixed size.
  *
  * free_begin and free_end are single device integers and may not be the same
- * one: every thread block reads *free_begin.
+ * one.  No output may overlap an input (the lengths, free_blocks, free_begin):
+ * thread blocks read all of these while others write.  Lengths are advanced by a
+ * copy of kv_lens behind the call.
  *
  * Device-visible errors.  A negative length counts as zero, and a length past
  * table_stride * block_size is cut there (KDA_DEV_BAD_SEQLENS); so are tokens

@@ -3,7 +3,7 @@ key/value cache's plan and append, prompt attention and decode attention.
 
 Argument marshalling only, as in the package itself; the header states layouts, masks and
 errors.  q, k and v may be views of a fused projection's output: the heads of one token are
-dense, the tokens evenly spaced.
+dense, the tokens evenly spaced.  All tensors are on the current device: the library launches there.
 """
 import collections
 import ctypes
@@ -66,6 +66,19 @@ def _tokens(x, name, dtype, shape, dev, index):
     return x.data_ptr(), stride
 
 
+def _current_device():
+    return torch.cuda.current_device()
+
+
+if hasattr(torch._C, "_cuda_getDevice"):                    # without the check that CUDA is up: a tensor is on it
+    _current_device = torch._C._cuda_getDevice
+
+
+def _not_current(index, name):
+    """The library launches on the current device and sets that one's status word."""
+    raise ValueError(f"{name} is on cuda:{index}, which is not the current device (cuda:{_current_device()})")
+
+
 def _first(x, name):
     """(shape, dtype, its code, device, device index, address, stride) of the tensor that the
     others have to match."""
@@ -75,6 +88,8 @@ def _first(x, name):
         raise TypeError(f"{name} must be {_FLOATS[0]} or {_FLOATS[1]} (got {dtype})")
     dev, index = x.device, x.get_device()
     ptr, stride = _tokens(x, name, dtype, shape, dev, index)
+    if index != _current_device():
+        _not_current(index, name)
     return shape, dtype, _CODES[dtype], dev, index, ptr, stride
 
 
@@ -132,6 +147,8 @@ def cache_plan(cached_lens, new_lens, block_table, free_blocks, free_begin, free
         raise ValueError(f"max_tokens must be >= 0 (got {T})")
     dev, ix = cached_lens.device, cached_lens.get_device()
     a0 = _dev(cached_lens, "cached_lens", _I32, (n,), None, ix if ix >= 0 else None)
+    if ix != _current_device():
+        _not_current(ix, "cached_lens")
     a1 = _dev(new_lens, "new_lens", _I32, (n,), dev, ix)
     a2 = _dev(free_blocks, "free_blocks", _I32, (n_free,), dev, ix)
     a3 = _dev(free_begin, "free_begin", _I32, (1,), dev, ix)

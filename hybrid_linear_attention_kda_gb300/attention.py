@@ -45,7 +45,7 @@ def _tokens(x, name, dtype, shape, dev, index):
     if type(x) is _Tensor and x.dtype is dtype and x.shape == shape and x.get_device() == index and index >= 0:
         stride, inner, last = x.stride()
         if last == 1 and inner == d and stride >= heads * d:
-            return x.data_ptr(), stride
+            return x.data_ptr(), stride if T > 1 else heads * d         # between tokens: of one, of no account
     if not isinstance(x, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor (got {type(x).__name__})")
     if x.dtype is not dtype:

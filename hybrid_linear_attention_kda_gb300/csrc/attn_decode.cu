@@ -60,8 +60,9 @@ __global__ void __launch_bounds__(kInfoThreads) decode_info_kernel(const __grid_
 constexpr int kWarps = kDecodeWarps, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 // The maximum that weights refer to is the first tile's, and is moved when a weight
-// passes kMostWeight; kLeastMaximum until a row has seen a score above -inf.
-constexpr float kMostWeight = 1024.f, kLeastMaximum = -1e30f;
+// passes kMostWeight; kLeastMaximum, the least finite number, until a row has seen a score
+// above -inf: of any score above it the weight is infinite then, and moves it.
+constexpr float kMostWeight = 1024.f, kLeastMaximum = -3.402823466e38f;
 
 // A tile holds 4 KB of keys and 4 KB of values.  The 16-byte pieces of key j lie at
 // piece ^ (j * lanes per key) of its row, so that eight lanes of a score (two or four

@@ -72,9 +72,10 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMostWeight = 1024.f;         // of a row's tile, before the maximum moves
-// The maximum of a row that has seen only scores of -inf: the first score above it
-// gives an infinite weight, which moves it.
-constexpr float kLeastMaximum = -1e30f;
+// The maximum of a row that has seen only scores of -inf, before or after the scale: the
+// first score above it gives an infinite weight, which moves it.  Near the least finite
+// number, so that no score lies below; times the scale it stays finite.
+constexpr float kLeastMaximum = -3e38f;
 constexpr uint32_t kTmemCols = 512;           // S0 0, S1 128, O0 256, O1 384
 
 enum Mode { kPacked, kPaged, kPrefix };
@@ -792,7 +793,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         const int r_token = r / G, g = r % G;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         // a scale of 0 becomes the least normal number, so that a hidden score of -inf stays one
-        const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f), least = kLeastMaximum / fmaxf(c, 1.f);
         // Rows that begin on 32 bytes are traded and written in whole sectors, others in 16-byte
         // pieces (720 x 64 tokens, 32/8 heads, d = 128: 190 us, and 254 us).
         const bool wide = !SPLIT && ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)(a.o_stride * 2)) & 31u) == 0;
@@ -809,7 +810,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
             int tile_sees = max(0, (MODE == kPrefix ? it.k_hi : min(it.k_hi, it.first + it.t0 + q * tokens + 1)) - it.k_lo);
             if (__any_sync(0xffffffffu, !live)) tile_sees = 0;
             const int n = it.n_keys(q);
-            float m = kLeastMaximum;
+            float m = least;
             uint64_t l2 = pair2(0.f);
             for (int j = 0; j < n; ++j) {
                 pass(ok, &ms.s_full[q], phase);

@@ -31,7 +31,7 @@
  *  - q, k, v, o and the caches share one element type.  bf16: products on the
  *    tensor cores with fp32 accumulation, the softmax in fp32, its weights
  *    rounded to bf16 for the product with v (their sum is taken before that
- *    rounding).  fp32: fp32 throughout.
+ *    rounding), for scores |scale * q . k| up to 2^27.  fp32: fp32 throughout.
  *  - Positions that a mask hides never reach a result, whatever they hold: NaN
  *    or infinities in later tokens, other sequences, or the unwritten tail of a
  *    block change nothing.  A query row that sees no key gives zeros, and -inf

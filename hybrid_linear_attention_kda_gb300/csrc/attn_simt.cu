@@ -12,8 +12,8 @@
 // every so manieth key tile each, whose results are joined at the end: the chain of
 // key tiles gets as much shorter.  K is padded by 16 bytes a row, so that the 16
 // threads of a row group read distinct banks; the weights reuse K's place.  Bound by
-// the FP32 pipe and the shared-memory reads that feed it: 8 x 2000 tokens, 16 heads, d =
-// 128 take 3.5 ms, 37 TFLOP/s.  One prompt of 512, 2 heads, d = 64 takes 20 us, 47 us with
+// the FP32 pipe and the shared-memory reads that feed it (eight 16-byte reads for 64
+// products): 8 x 2000 tokens, 16/4 heads, d = 128 take 3.5 ms, 37 TFLOP/s.  One prompt of 512, 2 heads, d = 64 takes 20 us, 47 us with
 // one group.
 #include <math_constants.h>
 

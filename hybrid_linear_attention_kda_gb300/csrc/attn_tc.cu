@@ -44,12 +44,15 @@
 // behind them made the compiler spill (4 x 8192 tokens 1.45 -> 1.51 ms).
 //
 // Bound by the tensor pipe where sequences are long: 4 d flops per (row, key) pair.
-// Measured on 4 x 8192 tokens, 32 query and 8 key/value heads, d = 128: 1.30 ms, 1690
-// TFLOP/s.  Items of few tiles are bound by the steps between them, and those by
+// Measured on 4 x 8192 tokens, 32 query and 8 key/value heads, d = 128: 1.44 ms, 1530
+// TFLOP/s in a loop, under the power limit (1.33 ms in its first milliseconds).  With d =
+// 64 and 16/2 heads 0.50 ms, 1100 TFLOP/s: P lies in S's place, so that a row tile's next
+// scores wait for its last product, and two row tiles are too few to hide that chain at
+// half the arithmetic.  Items of few tiles are bound by the steps between them, and those by
 // fetching instructions: straight code that is not in the 32 KB of instruction cache
 // costs 6 cycles an instruction, and a jump a trip to L2.  So what is rarely executed
 // is kept in loops, and what every item executes in one place: 2880 items of one or two
-// tiles (180 x 256 tokens, 16 query and 2 key/value heads, d = 64) take 93 us, and took 112
+// tiles (180 x 256 tokens, 16 query and 2 key/value heads, d = 64) take 95 us, and took 112
 // us with the weights, the rescaling and the hidden values' repair unrolled wherever needed.
 #include <cuda.h>
 #include <math_constants.h>
@@ -339,7 +342,7 @@ struct Place {
 // warp; later indexes mostly lie further on, so the search goes on where the last one
 // ended, mostly without a load.  Long items come first, so that the blocks end together:
 // the tiles of one sequence last first, and up to 32 sequences by their positions (8
-// prompts of 1 to 1024 tokens behind 256 to 4096: 124 -> 108 us; among more, the order
+// prompts of 1 to 1024 tokens behind 256 to 4096: 116 us, 127 us unsorted; among more, the order
 // makes no difference that was worth sorting).  Sequences are not interleaved: their keys
 // stay in L2.  SPLIT: the keys of a tile are cut into n_split blocks, an item each.
 template <int MODE, bool SPLIT>
@@ -795,7 +798,7 @@ attn_tc_kernel(const __grid_constant__ AttnTileLaunch p, const __grid_constant__
         // a scale of 0 becomes the least normal number, so that a hidden score of -inf stays one
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f), least = kLeastMaximum / fmaxf(c, 1.f);
         // Rows that begin on 32 bytes are traded and written in whole sectors, others in 16-byte
-        // pieces (720 x 64 tokens, 32/8 heads, d = 128: 190 us, and 254 us).
+        // pieces (720 x 64 tokens, 32/8 heads, d = 128: 200 us, and 259 us).
         const bool wide = !SPLIT && ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)(a.o_stride * 2)) & 31u) == 0;
         uint32_t phase = 0, o_phase = 0;                          // of the tiles, of the items with tiles
         bool ok = true;

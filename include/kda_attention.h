@@ -126,6 +126,11 @@ kda_status_t kda_cache_append(int64_t n_tokens, int32_t n_kv_heads, int32_t d, i
  * one past total_tokens, or a kv_len outside [0, table_stride * block_size], sets
  * KDA_DEV_BAD_SEQLENS and skips the sequence; a table entry outside the cache
  * sets KDA_DEV_BAD_SLOT, and that sequence's outputs are unspecified.
+ *
+ * Where the rows are too many to be cut, one thread block walks all keys of its rows,
+ * and its waits run out after about a second: in bf16 that is some 2^26 keys, beyond
+ * which KDA_DEV_WAIT_TIMEOUT is set and outputs are unspecified.  The same holds for
+ * a shared prefix of kda_attn_decode that is not cut.
  */
 typedef struct kda_attn_prefill_args {
     int32_t n_seqs;

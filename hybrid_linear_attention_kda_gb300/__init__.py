@@ -13,7 +13,8 @@ updates it in place for every token ("Kimi K3 Tech Intro", section 2.1):
 import ctypes
 import os
 
-from .attention_abi import KDA_DEV_BAD_GROUP, KDA_DEV_NO_BLOCKS, AttnDecodeArgs, AttnPrefillArgs, CachePlanArgs  # noqa: F401
+from .attention_abi import (KDA_DEV_BAD_GROUP, KDA_DEV_BAD_POSITION, KDA_DEV_NO_BLOCKS, AttnDecodeArgs,  # noqa: F401
+                            AttnPrefillArgs, CacheAppendRopeArgs, CachePlanArgs, QkRopeArgs)
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "libkda.so")
@@ -416,11 +417,17 @@ def prefill(q, k, v, alpha, beta, cu_seqlens, total_tokens=None, *, start_pos=No
 _ATTENTION = ("CachePlan", "kda_cache_plan", "kda_cache_append", "kda_attn_prefill", "kda_attn_decode",
               "kda_attn_prefill_workspace_size", "kda_attn_decode_workspace_size", "cache_plan", "attn_prefill", "attn_prefill_paged", "attn_decode")
 
+_ROPE = ("rope_turns", "kda_qk_norm_rope", "qk_norm_rope", "kda_cache_append_rope", "cache_append_rope")
+
 
 def __getattr__(name):
-    """The attention side's functions, from ``attention`` (which imports torch) on first use."""
+    """The attention side's functions, from the modules that hold them (which import torch) on first use."""
     if name in _ATTENTION:
         from . import attention
         globals().update({n: getattr(attention, n) for n in _ATTENTION})
+        return globals()[name]
+    if name in _ROPE:
+        from . import rope
+        globals().update({n: getattr(rope, n) for n in _ROPE})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,9 +1,9 @@
-"""The C interface of the softmax-attention side (``include/kda_attention.h``): its argument blocks,
-status bits and signatures.  Without torch, so that loading the library needs none.
+"""The C interface of the softmax-attention side (``include/kda_attention.h``, ``kda_rope.h``): its argument
+blocks, status bits and signatures.  Without torch, so that loading the library needs none.
 """
 import ctypes
 
-KDA_DEV_NO_BLOCKS, KDA_DEV_BAD_GROUP = 0x40, 0x80
+KDA_DEV_NO_BLOCKS, KDA_DEV_BAD_GROUP, KDA_DEV_BAD_POSITION = 0x40, 0x80, 0x100
 
 
 class CachePlanArgs(ctypes.Structure):
@@ -47,6 +47,28 @@ class AttnDecodeArgs(ctypes.Structure):
     ]
 
 
+class QkRopeArgs(ctypes.Structure):
+    """Mirror of ``kda_qk_rope_args``."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("reserved0", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("turns", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+    ]
+
+
+class CacheAppendRopeArgs(ctypes.Structure):
+    """Mirror of ``kda_cache_append_rope_args``."""
+    _fields_ = [
+        ("qk", QkRopeArgs), ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64), ("slot_map", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("n_blocks", ctypes.c_int64),
+        ("block_size", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+    ]
+
+
 def declare(lib):
     """Set the ctypes signatures of the entry points."""
     vp, i32, i64, P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER
@@ -62,3 +84,7 @@ def declare(lib):
     lib.kda_attn_decode_workspace_size.argtypes = [P(AttnDecodeArgs)]
     lib.kda_attn_decode.restype = ctypes.c_int
     lib.kda_attn_decode.argtypes = [P(AttnDecodeArgs), vp]
+    for name, block in (("kda_qk_norm_rope", QkRopeArgs), ("kda_cache_append_rope", CacheAppendRopeArgs)):
+        entry = getattr(lib, name)
+        entry.restype = ctypes.c_int
+        entry.argtypes = [P(block), vp]

@@ -14,7 +14,8 @@ import ctypes
 import os
 
 from .attention_abi import (KDA_DEV_BAD_GROUP, KDA_DEV_BAD_POSITION, KDA_DEV_NO_BLOCKS, AttnDecodeArgs,  # noqa: F401
-                            AttnPrefillArgs, CacheAppendRopeArgs, CachePlanArgs, QkRopeArgs)
+                            AttnDecodeQ4Args, AttnPrefillArgs, CacheAppendQ4Args, CacheAppendRopeArgs, CachePlanArgs,
+                            CacheQ4, CacheUnpackQ4Args, QkRopeArgs)
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "libkda.so")
@@ -418,16 +419,17 @@ _ATTENTION = ("CachePlan", "kda_cache_plan", "kda_cache_append", "kda_attn_prefi
               "kda_attn_prefill_workspace_size", "kda_attn_decode_workspace_size", "cache_plan", "attn_prefill", "attn_prefill_paged", "attn_decode")
 
 _ROPE = ("rope_turns", "kda_qk_norm_rope", "qk_norm_rope", "kda_cache_append_rope", "cache_append_rope")
+_Q4 = ("Q4Cache", "q4_cache", "kda_cache_append_q4", "cache_append_q4", "kda_cache_unpack_q4", "cache_unpack_q4",
+       "kda_attn_decode_q4", "kda_attn_decode_q4_workspace_size", "attn_decode_q4")
+_LAZY = {"attention": _ATTENTION, "rope": _ROPE, "cache_q4": _Q4}
 
 
 def __getattr__(name):
     """The attention side's functions, from the modules that hold them (which import torch) on first use."""
-    if name in _ATTENTION:
-        from . import attention
-        globals().update({n: getattr(attention, n) for n in _ATTENTION})
-        return globals()[name]
-    if name in _ROPE:
-        from . import rope
-        globals().update({n: getattr(rope, n) for n in _ROPE})
-        return globals()[name]
+    for module, names in _LAZY.items():
+        if name in names:
+            from importlib import import_module
+            held = import_module("." + module, __name__)
+            globals().update({n: getattr(held, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

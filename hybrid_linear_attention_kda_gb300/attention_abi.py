@@ -1,5 +1,5 @@
-"""The C interface of the softmax-attention side (``include/kda_attention.h``, ``kda_rope.h``): its argument
-blocks, status bits and signatures.  Without torch, so that loading the library needs none.
+"""The C interface of the softmax-attention side (``include/kda_attention.h``, ``kda_rope.h``,
+``kda_cache_q4.h``): its argument blocks, status bits and signatures.  Without torch, so that loading the library needs none.
 """
 import ctypes
 
@@ -69,6 +69,42 @@ class CacheAppendRopeArgs(ctypes.Structure):
     ]
 
 
+class CacheQ4(ctypes.Structure):
+    """Mirror of ``kda_cache_q4``."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p), ("n_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+    ]
+
+
+class CacheAppendQ4Args(ctypes.Structure):
+    """Mirror of ``kda_cache_append_q4_args``."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("k_out_stride", ctypes.c_int64), ("v_out_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("slot_map", ctypes.c_void_p),
+        ("cache", CacheQ4),
+    ]
+
+
+class CacheUnpackQ4Args(ctypes.Structure):
+    """Mirror of ``kda_cache_unpack_q4_args``."""
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("cache", CacheQ4), ("block_table", ctypes.c_void_p), ("to_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int32), ("to_stride", ctypes.c_int32), ("first", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("n_blocks", ctypes.c_int64),
+    ]
+
+
+class AttnDecodeQ4Args(ctypes.Structure):
+    """Mirror of ``kda_attn_decode_q4_args``."""
+    _fields_ = [("base", AttnDecodeArgs), ("cache", CacheQ4)]
+
+
 def declare(lib):
     """Set the ctypes signatures of the entry points."""
     vp, i32, i64, P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER
@@ -84,7 +120,11 @@ def declare(lib):
     lib.kda_attn_decode_workspace_size.argtypes = [P(AttnDecodeArgs)]
     lib.kda_attn_decode.restype = ctypes.c_int
     lib.kda_attn_decode.argtypes = [P(AttnDecodeArgs), vp]
-    for name, block in (("kda_qk_norm_rope", QkRopeArgs), ("kda_cache_append_rope", CacheAppendRopeArgs)):
+    lib.kda_attn_decode_q4_workspace_size.restype = ctypes.c_size_t
+    lib.kda_attn_decode_q4_workspace_size.argtypes = [P(AttnDecodeQ4Args)]
+    for name, block in (("kda_qk_norm_rope", QkRopeArgs), ("kda_cache_append_rope", CacheAppendRopeArgs),
+                        ("kda_cache_append_q4", CacheAppendQ4Args), ("kda_cache_unpack_q4", CacheUnpackQ4Args),
+                        ("kda_attn_decode_q4", AttnDecodeQ4Args)):
         entry = getattr(lib, name)
         entry.restype = ctypes.c_int
         entry.argtypes = [P(block), vp]

@@ -1,0 +1,39 @@
+// Launches of the 4-bit cache (not part of the C ABI).
+#pragma once
+
+#include "attn_common.cuh"
+#include "kda_cache_q4.h"
+
+namespace kda {
+
+constexpr int kQ4Group = 64;                                // channels that share a scale
+__host__ __device__ constexpr int q4_code_bytes(int d) { return d / 2; }                  // of a head's vector
+__host__ __device__ constexpr int q4_scale_bytes(int d) { return d / kQ4Group * 4; }
+
+struct CacheAppendQ4Launch {
+    kda_cache_append_q4_args a;
+    uint32_t* status;
+};
+cudaError_t launch_append_q4(const CacheAppendQ4Launch& p, cudaStream_t s);
+
+struct CacheUnpackQ4Launch {
+    kda_cache_unpack_q4_args a;
+    uint32_t* status;
+};
+cudaError_t launch_unpack_q4(const CacheUnpackQ4Launch& p, cudaStream_t s);
+
+// Decode attention over the 4-bit cache; `base` as for the full-width cache, with its k_cache,
+// v_cache and n_blocks those of the shared prefixes.
+struct AttnDecodeQ4Launch {
+    AttnDecodeLaunch base;
+    kda_cache_q4 cache;
+};
+constexpr int kQ4Keys = 16;                                 // keys of a tile
+// Products of eight columns a unit takes: one, or two where a key/value head's query heads do
+// not fit in one (fp32: two columns a head).
+__host__ __device__ constexpr int q4_columns(int dtype, int G) { return G <= (dtype == KDA_BF16 ? 8 : 4) ? 1 : 2; }
+__host__ __device__ constexpr int q4_rows(int dtype, int G) { return q4_columns(dtype, G) * (dtype == KDA_BF16 ? 8 : 4); }
+__host__ __device__ constexpr int q4_warps(int columns) { return columns == 1 ? 16 : 8; }   // of a thread block, one an SM
+cudaError_t launch_decode_q4(const AttnDecodeQ4Launch& p, cudaStream_t s);
+
+}  // namespace kda

@@ -1,4 +1,4 @@
-// Decode attention over the 4-bit cache.  The division of work (a line of tiles of 16 keys,
+// Decode attention over the 4-bit cache.  The division of work (a line of tiles of 32 keys,
 // cut into equal pieces, a warp each, and the join) is attn_decode.cuh's.
 //
 // With codes n, and (s, m) of each key's group of 64 channels,
@@ -15,10 +15,13 @@
 // K: a code in an fp16 number's lowest bits is that number: the subnormals are n 2^-24, exact
 // operands like any other.  A word's eight codes take four masks and a shift: at bits 4..7
 // a code counts 16-fold, which q's side makes up for.  q is scaled by a power of two for the
-// range of fp16.  V: 128 + n is 0x4300 | n in bf16, less 136; two keys' words are interleaved
-// first, since the products add up over keys.  Weights times scales are bf16, as their range
-// has no bound.
+// range of fp16.  V: the products add up over keys, so that a byte of codes has to meet the
+// same byte of the next key: ldmatrix transposes bytes, a permutation puts 0x64 behind each,
+// which makes 1024 + byte of it, and one fp16 instruction n - 8 of each of its codes.  A
+// product's rows are the keys in the order in which that hands them out.  Weights times scales are rounded to fp16: 11 bits, counted from the largest so far
+// of each head and group (a power of two, moved like the weights' own maximum).
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "attn_decode.cuh"
 #include "cache_q4.cuh"
@@ -29,15 +32,20 @@ using namespace decode;
 
 constexpr int kKeys = kQ4Keys;
 constexpr float kMaxGrowth = 8.f;        // log2 of how far weights may exceed 1 before their maximum moves
+constexpr float kMostWeight = 0x1p15f;   // times scale, in units: below fp16's largest
 
-// Per warp: a ring of tiles, each 16 keys' codes and scales of K and of V.
+// Per warp: a ring of tiles, each two halves of 16 keys, which may lie in two pages; codes
+// of K, codes of V, scales of K, scales of V.
+constexpr int kHalf = kKeys / 2;
 template <int D, int WARPS> struct Q4Smem {
     static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / kQ4Group * 4, kTile = 2 * (kCodes + kScales);
-    static constexpr int kFit = 216 * 1024 / (WARPS * kTile), kStages = kFit < 16 ? kFit : 16;
-    static constexpr int kBytes = WARPS * kStages * kTile;
+    static constexpr int kStages = 222 * 1024 / (WARPS * kTile), kBytes = WARPS * kStages * kTile;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+}
 // `bytes` of 16 bytes global -> shared, zeros behind them.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes) : "memory");
@@ -55,15 +63,30 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
 }
+// The scale pairs of one key.
+template <int NG> __device__ __forceinline__ void load_scales(uint32_t (&scale)[2], uint32_t at) {
+    if (NG == 2) {
+        const uint2 v = lds64(at);
+        scale[0] = v.x, scale[1] = v.y;
+    } else {
+        scale[0] = scale[1] = lds32(at);
+    }
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// The first product of a sum.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 // Transpose of an 8 x 8 matrix of 16-bit values, two a lane.
 __device__ __forceinline__ uint32_t transpose(uint32_t x) {
@@ -76,10 +99,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -87,11 +106,28 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 __device__ __forceinline__ float low_of(uint32_t x) { return __uint_as_float(x << 16); }             // bf16 pairs
 __device__ __forceinline__ float high_of(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-// n - 8 in bf16 for the codes at bits 0..3 of both halves of x.
-__device__ __forceinline__ uint32_t centred(uint32_t x) {
-    const uint32_t y = (x & 0x000F000Fu) | 0x43004300u, middle = 0x43084308u;          // 128 + n, 136
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&middle));
-    return *reinterpret_cast<const uint32_t*>(&v);
+// Two 16 x 16 blocks of bytes, transposed: r[2 i + h] holds column lane / 4 + 8 h of block i,
+// rows 4 (lane % 4) .. + 3.  Lanes name the blocks' rows, 16 bytes each.
+__device__ __forceinline__ void ldsm_bytes(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+// n - 8 in fp16 for the lower and the upper codes of two bytes of x (0 and 1, or 2 and 3).  With
+// a byte c, 0x6400 | c is 1024 + c; without its lower code but 8 in its place, 1024 + 16 n + 8.
+template <int PICK> __device__ __forceinline__ void centred(uint32_t x, uint32_t& lower, uint32_t& upper) {
+    const uint32_t both = __byte_perm(x, 0x64u, PICK == 0 ? 0x4140 : 0x4342);
+    const uint32_t rest = (both & 0xFFF0FFF0u) | 0x00080008u, by = 0x2C002C00u, middle = 0xD488D488u;      // 1 / 16, -72.5
+    const __half2 h = *reinterpret_cast<const __half2*>(&both), r = *reinterpret_cast<const __half2*>(&rest);
+    const __half2 lo = __hsub2(h, r), hi = __hfma2(r, *reinterpret_cast<const __half2*>(&by), *reinterpret_cast<const __half2*>(&middle));
+    lower = *reinterpret_cast<const uint32_t*>(&lo), upper = *reinterpret_cast<const uint32_t*>(&hi);
+}
+
+// x as the sum of three bf16 numbers: the i-th, nothing where i is 3.
+__device__ __forceinline__ float third(float x, int i) {
+    const float a = __bfloat162float(__float2bfloat16_rn(x)), b = __bfloat162float(__float2bfloat16_rn(x - a));
+    return i == 0 ? a : i == 1 ? b : i == 2 ? __bfloat162float(__float2bfloat16_rn(x - a - b)) : 0.f;
 }
 
 // Sixteen channels of q.
@@ -111,6 +147,23 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* q, float (&x)[16]) {
         for (int k = 0; k < 4; ++k) x[8 * i + 2 * k] = low_of(w[k]), x[8 * i + 2 * k + 1] = high_of(w[k]);
     }
 }
+
+__device__ __forceinline__ void write2(float* to, float x, float y) { *reinterpret_cast<float2*>(to) = make_float2(x, y); }
+__device__ __forceinline__ void write2(__nv_bfloat16* to, float x, float y) { *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(x, y); }
+
+// By how many powers of two the unit of a head's and group's weights is to move, so that the
+// tile's largest weight, `most` * 2^10, lies at 2^6 .. 2^7 of it: then weights have 11 bits
+// down to 2^-20 of the largest and may grow by 2^8.  Upwards only where the sums so far have
+// shrunk (by `shrunk`; 0: there were none), and not by so much that they could leave fp32's
+// range.
+__device__ __forceinline__ int unit_up(float most, float shrunk, float unit) {
+    if (!(most > 0.f)) return 0;
+    const int at = (int)(__float_as_uint(unit) >> 23) - 127;
+    int up = 6 - 10 - ((int)(__float_as_uint(most) >> 23) - 127) - at;
+    if (shrunk != 0.f) up = min(up, shrunk == 1.f ? 0 : 40 + 126 - (int)(__float_as_uint(shrunk) >> 23));
+    return max(-120 - at, min(120 - at, up));                        // the unit and its inverse stay normal
+}
+__device__ __forceinline__ float two_to(int i) { return __uint_as_float((uint32_t)(i + 127) << 23); }
 
 // A unit's query heads are the columns of NT products of eight: all heads' own (bf16), or
 // four heads twice, for both parts (fp32).
@@ -138,45 +191,64 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     Cursor c = start(at_[warp], line, piece, a.n_kv_heads * blocks, kKeys);
 
     // ------------------------------------------------------------------ copies
-    // The copies' own place on the line, kStages - 1 tiles ahead.  A group's 32 bytes of codes,
-    // unit u = key * NG + g, lie at u ^ (u / 4 % 4): what eight lanes of a product read together
-    // is in eight banks' worth of different places.
+    // The copies' own place on the line, kStages - 1 tiles ahead: cursor f at the first tile of
+    // a run within one unit, f_run tiles of it to come, key f_key next.  Sixteen lanes copy a
+    // half of the tile.  A group's 32 bytes of codes, unit u = key * NG + g of its half, lie at
+    // u ^ (u / 4 % 4): what eight lanes of a product read together is in eight banks' worth of
+    // different places.
     Cursor f = c;
     const uint32_t ring = smem_u32(smem_raw) + (uint32_t)(warp * kStages * S::kTile);
-    int32_t next_block = 0;                              // table entry of the place f
-    const int page_shift = __ffs(a.block_size) - 1;
-    auto look_up = [&]() {
-        const int64_t key = f.info.x + f.k * kKeys;
-        next_block = f.left > 0 && key < f.info.y ? a.block_table[(int64_t)f.s * a.table_stride + (key >> page_shift)] : -2;
-    };
+    const int page_shift = __ffs(a.block_size) - 1, half = lane >> 4, l16 = lane & 15;
+    int f_run = (int)f.run(), f_key = f.info.x + (int)f.k * kKeys + half * kHalf, f_head = f.u / blocks;
+    const int32_t* f_row = a.block_table + (int64_t)f.s * a.table_stride;
+    int32_t next_block = 0;                              // this half's table entry at f_key
+    // places in shared memory: piece y = 16 i + l16 of a half's codes, and one piece of its scales
+    constexpr int kPieces = S::kScales / 2 / 16, kPieceKeys = 4 / NG;
+    const int scale_piece = l16 % kPieces, scale_is_v = l16 / kPieces;
+    const uint32_t code0 = ring + half * (S::kCodes / 2) + (l16 >> 3) * 128 + ((l16 & 7) ^ (l16 >> 3) * (NG == 2 ? 1 : 5)) * 16;
+    const uint32_t scale_to = ring + 2 * S::kCodes + scale_is_v * S::kScales + half * (S::kScales / 2) + scale_piece * 16;
+    auto code_to = [&](uint32_t tile, int i) { return ((code0 + tile) ^ (NG == 2 ? (2 * i & 3) * 16 : 0)) + i * 256; };
+    const uint8_t* k_from = static_cast<const uint8_t*>(cache.k_codes) + l16 * 16;
+    const uint8_t* v_from = static_cast<const uint8_t*>(cache.v_codes) + l16 * 16;
+    const uint8_t* scale_from = static_cast<const uint8_t*>(scale_is_v ? cache.v_scales : cache.k_scales) + scale_piece * 16;
+    auto look_up = [&]() { next_block = f_run > 0 && f_key < f.info.y ? f_row[f_key >> page_shift] : -2; };
     auto fetch = [&](int stage) {
-        if (f.left > 0) {
-            const int64_t key = f.info.x + f.k * kKeys;
-            int live = (int)max((int64_t)0, min((int64_t)kKeys, f.info.y - key));     // keys that exist
+        if (f_run > 0) {
+            int live = min(kHalf, f.info.y - f_key);                         // keys of the half that exist
             if (live > 0 && (next_block < 0 || next_block >= cache.n_blocks)) {
                 flag(p.status, KDA_DEV_BAD_SLOT);
                 live = 0;
             }
-            const int hk = blocks == 1 ? f.u : f.u / blocks;
-            const int64_t row = live > 0 ? ((int64_t)next_block * a.n_kv_heads + hk) * a.block_size + (key & (a.block_size - 1)) : 0;
-            const uint32_t to = ring + (uint32_t)(stage * S::kTile);
-            const uint8_t* kc = static_cast<const uint8_t*>(cache.k_codes) + row * (D / 2);
-            const uint8_t* vc = static_cast<const uint8_t*>(cache.v_codes) + row * (D / 2);
+            // (rows are below 2^31; a half lies in one page, so that those of missing keys may be named too)
+            const uint32_t row = live > 0 ? ((uint32_t)next_block * a.n_kv_heads + f_head) * a.block_size + (f_key & (a.block_size - 1)) : 0u;
+            const uint32_t to = (uint32_t)(stage * S::kTile);
+            const uint8_t* kc = k_from + (uint64_t)row * (D / 2);
+            const uint8_t* vc = v_from + (uint64_t)row * (D / 2);
+            const uint8_t* sc_from = scale_from + (uint64_t)row * (NG * 4);
+            if (__all_sync(0xffffffffu, live == kHalf)) {
 #pragma unroll
-            for (int i = 0; i < S::kCodes / 16 / 32; ++i) {
-                const int y = i * 32 + lane, u = y >> 1, bytes = u / NG < live ? 16 : 0;
-                const uint32_t dst = to + (uint32_t)((u ^ (u >> 2 & 3)) * 32 + (y & 1) * 16);
-                const int from = bytes ? y * 16 : 0;
-                copy16(dst, kc + from, bytes);
-                copy16(dst + S::kCodes, vc + from, bytes);
+                for (int i = 0; i < S::kCodes / 2 / 256; ++i) {
+                    copy16(code_to(to, i), kc + i * 256);
+                    copy16(code_to(to, i) + S::kCodes, vc + i * 256);
+                }
+                if (l16 < 2 * kPieces) copy16(scale_to + to, sc_from);
+            } else {
+#pragma unroll
+                for (int i = 0; i < S::kCodes / 2 / 256; ++i) {
+                    const int bytes = (i * 16 + l16) / (2 * NG) < live ? 16 : 0;
+                    copy16(code_to(to, i), kc + i * 256, bytes);
+                    copy16(code_to(to, i) + S::kCodes, vc + i * 256, bytes);
+                }
+                if (l16 < 2 * kPieces) copy16(scale_to + to, sc_from, max(0, min(16, (live - scale_piece * kPieceKeys) * NG * 4)));
             }
-            constexpr int kPieces = S::kScales / 16, kPieceKeys = 4 / NG;        // 16-byte pieces of the scales
-            if (lane < 2 * kPieces) {
-                const int y = lane % kPieces, bytes = max(0, min(16, (live - y * kPieceKeys) * NG * 4));
-                const uint8_t* from = static_cast<const uint8_t*>(lane < kPieces ? cache.k_scales : cache.v_scales) + row * (NG * 4) + (bytes ? y * 16 : 0);
-                copy16(to + 2 * S::kCodes + lane * 16, from, bytes);
+            f_key += kKeys;
+            if (--f_run == 0) {
+                f.next_unit(p, kKeys);
+                if (f.left > 0) {
+                    f_run = (int)f.run(), f_key = f.info.x + half * kHalf, f_head = f.u / blocks;
+                    f_row = a.block_table + (int64_t)f.s * a.table_stride;
+                }
             }
-            f.step(p, kKeys);
             look_up();
         }
         copy_commit();
@@ -189,6 +261,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     // Lane (n, t) of a product's operands: rows n and n + 8, columns 2 t and one more.
     const int n = lane >> 2, t = lane & 3;
     const float sc = a.scale * kLog2e;
+    // Row n + 8 r of a half's products is key own_key + 2 r.  The lane's eight bytes of its K codes
+    // of group g lie at k_at(r, g), the 16 bytes that it names to ldmatrix at v0 ^ 32 g.  (The
+    // tile starts at a multiple of 128 bytes, so that places are sums and exclusive ors.)
+    const int own_key = 4 * (n >> 1) + (n & 1), v_key = lane & 15, v_line = v_key * NG >> 2;
+    const uint32_t k0 = ring + (NG == 2 ? (n >> 1) * 256 + (((n & 1) * 4 + (t >> 1)) ^ (n & 2)) * 16
+                                        : (n >> 1) * 128 + (((n & 1) * 2 + (t >> 1)) ^ (n >> 1 & 1) * 5) * 16) + (t & 1) * 8;
+    const uint32_t v0 = ring + S::kCodes + v_line * 128 + ((v_key * 2 * NG + (lane >> 4) & 7) ^ (NG == 2 ? v_line & 3 : (v_line & 1) * 5)) * 16;
+    const uint32_t s0 = ring + 2 * S::kCodes + own_key * NG * 4;
+    auto k_at = [](uint32_t k, int r, int g) { return NG == 2 ? (k ^ (g * 32 + r * 16)) + r * 128 : k ^ r * 64; };
     int stage = 0;
     while (c.left > 0) {
         const int64_t k_first = c.k, k_last = c.k + c.run();
@@ -200,7 +281,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         // q of column n, 16 channels of each group from 64 g + 16 t, as the operands that meet
         // a word's codes: (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16.
         uint32_t q[NT][NG][2][4];
-        float qsum[NT][2][NG], unscale[NT][2];           // of heads 2 t and 2 t + 1
+        uint32_t qsum[NT];                               // of column n, part t of three, both groups, times scale log2 e
+        float unscale[NT][2];                            // of heads 2 t and 2 t + 1, times that too
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * kColumns + n % kColumns;
@@ -246,93 +328,105 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                unscale[nt][e] = __shfl_sync(0xffffffffu, undo, 4 * (2 * t + e));
-#pragma unroll
-                for (int g = 0; g < NG; ++g) qsum[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * t + e)) * sc;
-            }
+            for (int e = 0; e < 2; ++e) unscale[nt][e] = __shfl_sync(0xffffffffu, undo, 4 * (2 * t + e)) * 0x1p24f * sc;
+            const float lower = third(sum[0] * sc, t), upper = NG == 2 ? third(sum[NG - 1] * sc, t) : 0.f;
+            qsum[nt] = __float_as_uint(lower) >> 16 | (__float_as_uint(upper) & 0xFFFF0000u);
         }
 
-        float o[NT][NG * 4][4], m[NT][2], l[NT][2], low[NT][2][NG];      // low: sum of p (m + 8 s)
+        // o: sum of weights times codes, in units of 1 / unit; low: sum of p (m + 8 s)
+        float o[NT][NG * 4][4], m[NT][2], l[NT][2], low[NT][2][NG], unit[NT][2][NG];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < NG * 4; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[nt][e] = -CUDART_INF_F, l[nt][e] = 0.f;
+                m[nt][e] = -FLT_MAX, l[nt][e] = 0.f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) low[nt][e][g] = 0.f;
+                for (int g = 0; g < NG; ++g) low[nt][e][g] = 0.f, unit[nt][e][g] = 1.f;
             }
         }
 
-        for (int64_t kt = k_first; kt < k_last; ++kt) {
+        int live = info.y - (info.x + (int)k_first * kKeys);                 // keys from this tile on
+        for (int kt = (int)(k_last - k_first); kt > 0; --kt, live -= kKeys) {
             copy_wait<kStages - 2>();
             __syncwarp();                                // the tile is there, and the stage before it is read
             fetch(stage == 0 ? kStages - 1 : stage - 1);
-            const uint32_t kb = ring + (uint32_t)(stage * S::kTile), vb = kb + S::kCodes, sb = vb + S::kCodes;
+            const uint32_t tile = (uint32_t)(stage * S::kTile), kb = k0 + tile, vb = v0 + tile, sb = s0 + tile;
             stage = stage == kStages - 1 ? 0 : stage + 1;
-            const int live = (int)max((int64_t)0, min((int64_t)kKeys, info.y - (info.x + kt * kKeys)));
 
-            // scores of keys n and n + 8 (r), heads 2 t + e
-            float x[NT][2][2] = {};
+            // scores of keys own_key + 2 (r % 2) of both halves, heads 2 t + e
+            float x[NT][4][2];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                uint2 w[2];
-                uint32_t scale[2];
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t scale[2][2];                    // (s, m) of both keys' groups
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int u = (n + 8 * r) * NG + g;
-                    w[r] = lds64(kb + (uint32_t)((u ^ (u >> 2 & 3)) * 32 + t * 8));
-                    scale[r] = lds32(sb + (uint32_t)u * 4);
+                for (int r = 0; r < 2; ++r) load_scales<NG>(scale[r], sb + hf * (S::kScales / 2) + r * (8 * NG));
+                float y[NT][4];                          // sum of s (q . n)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    uint2 w[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) w[r] = lds64(k_at(kb, r, g) + hf * (S::kCodes / 2));
+                    float acc[NT][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w0 = h ? w[0].y : w[0].x, w1 = h ? w[1].y : w[1].x, v0 = w0 >> 8, v1 = w1 >> 8;
+                        const uint32_t a0 = w0 & 0x000F000Fu, a1 = w1 & 0x000F000Fu, a2 = w0 & 0x00F000F0u, a3 = w1 & 0x00F000F0u;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (h == 0) mma_f16_first(acc[nt], a0, a1, a2, a3, q[nt][g][h][0], q[nt][g][h][1]);
+                            else mma_f16(acc[nt], a0, a1, a2, a3, q[nt][g][h][0], q[nt][g][h][1]);
+                            mma_f16(acc[nt], v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u, q[nt][g][h][2], q[nt][g][h][3]);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float step = low_of(scale[k >> 1][g]);
+                            y[nt][k] = g == 0 ? acc[nt][k] * step : fmaf(acc[nt][k], step, y[nt][k]);
+                        }
                 }
-                float acc[NT][4] = {};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t w0 = h ? w[0].y : w[0].x, w1 = h ? w[1].y : w[1].x, v0 = w0 >> 8, v1 = w1 >> 8;
+                for (int nt = 0; nt < NT; ++nt) {
+                    float base[4];                       // sum of m (sum q)
+                    mma_bf16_k8(base, __byte_perm(scale[0][0], scale[0][NG - 1], 0x7632), __byte_perm(scale[1][0], scale[1][NG - 1], 0x7632), qsum[nt]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(acc[nt], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, q[nt][g][h][0], q[nt][g][h][1]);
-                        mma_f16(acc[nt], v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u, q[nt][g][h][2], q[nt][g][h][3]);
+                    for (int k = 0; k < 4; ++k) {
+                        if (kTwoParts) y[nt][k] += __shfl_xor_sync(0xffffffffu, y[nt][k], 2);
+                        x[nt][2 * hf + (k >> 1)][k & 1] = fmaf(y[nt][k], unscale[nt][k & 1], base[k]);
                     }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float y = acc[nt][2 * r + e];
-                            if (kTwoParts) y += __shfl_xor_sync(0xffffffffu, y, 2);
-                            y = y * 0x1p24f * unscale[nt][e] * sc;
-                            x[nt][r][e] += fmaf(y, low_of(scale[r]), high_of(scale[r]) * qsum[nt][e][g]);
-                        }
             }
             if (live < kKeys) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        if (n + 8 * r >= live) x[nt][r][0] = x[nt][r][1] = -CUDART_INF_F;
+                    for (int r = 0; r < 4; ++r)
+                        if (own_key + 2 * (r & 1) + kHalf * (r >> 1) >= live) x[nt][r][0] = x[nt][r][1] = -CUDART_INF_F;
             }
             bool grow = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float mx = fmaxf(x[nt][0][e], x[nt][1][e]);
-                    grow |= mx - m[nt][e] > kMaxGrowth;              // (false for -inf less -inf)
+                    const float mx = fmaxf(fmaxf(x[nt][0][e], x[nt][1][e]), fmaxf(x[nt][2][e], x[nt][3][e]));
+                    grow |= mx - m[nt][e] > kMaxGrowth;
                 }
-            if (__any_sync(0xffffffffu, grow)) {
+            const bool grown = __any_sync(0xffffffffu, grow);
+            float shrunk[NT][2];                         // what the sums so far were multiplied by
+            if (grown) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(x[nt][0][e], x[nt][1][e]);
+                        float mx = fmaxf(fmaxf(x[nt][0][e], x[nt][1][e]), fmaxf(x[nt][2][e], x[nt][3][e]));
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                         mx = fmaxf(m[nt][e], mx);
-                        const float w = m[nt][e] == -CUDART_INF_F ? 0.f : ex2(m[nt][e] - mx);
+                        const float w = m[nt][e] == -FLT_MAX ? 0.f : ex2(m[nt][e] - mx);
+                        shrunk[nt][e] = w;
                         m[nt][e] = mx;
                         l[nt][e] *= w;
 #pragma unroll
@@ -348,59 +442,102 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float off = m[nt][e] == -CUDART_INF_F ? 0.f : m[nt][e];
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        x[nt][r][e] = ex2(x[nt][r][e] - off);
+                    for (int r = 0; r < 4; ++r) {
+                        x[nt][r][e] = ex2(x[nt][r][e] - m[nt][e]);
                         l[nt][e] += x[nt][r][e];
                     }
+            // weights times scales, in units, as fp16 pairs of two heads; a sum of them says whether
+            // one might leave fp16's range
+            uint32_t w[NT][NG][4];
+            __half2 total = __float2half2_rn(0.f);
+            auto weigh = [&](int nt, int g, int r, float step) {
+                float y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    y[e] = x[nt][r][e] * (step * unit[nt][e][g]);
+                    if (kTwoParts) {
+                        const float hi = __half2float(__float2half_rn(y[e]));
+                        y[e] = t < 2 ? hi : y[e] - hi;
+                    }
                 }
+                w[nt][g][r] = pack_half(y[0], y[1]);
+            };
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                uint32_t b[NT][2];                       // weights times scales, turned to heads n, keys 2 t, 2 t + 1 (+ 8)
+            for (int r = 0; r < 4; ++r) {
+                uint32_t scale[2];
+                load_scales<NG>(scale, sb + S::kScales + (r >> 1) * (S::kScales / 2) + (r & 1) * (8 * NG));
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t scale = lds32(sb + S::kScales + (uint32_t)((n + 8 * r) * NG + g) * 4);
-                    const float step = low_of(scale), mid = fmaf(8.f, step, high_of(scale));
+                for (int g = 0; g < NG; ++g) {
+                    const float step = low_of(scale[g]), mid = fmaf(8.f, step, high_of(scale[g]));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float w[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            low[nt][e][g] = fmaf(x[nt][r][e], mid, low[nt][e][g]);
-                            w[e] = x[nt][r][e] * step;
-                            if (kTwoParts) {
-                                const float hi = __bfloat162float(__float2bfloat16_rn(w[e]));
-                                w[e] = t < 2 ? hi : w[e] - hi;
-                            }
-                        }
-                        b[nt][r] = transpose(pack(w[0], w[1]));
+                        for (int e = 0; e < 2; ++e) low[nt][e][g] = fmaf(x[nt][r][e], mid, low[nt][e][g]);
+                        weigh(nt, g, r, step);
+                        total = __hadd2(total, *reinterpret_cast<const __half2*>(&w[nt][g][r]));
                     }
-                }
-                uint32_t v[2][2];                        // channels 64 g + 8 n .. of keys 2 t, 2 t + 1 (+ 8)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int u = (2 * t + e + 8 * r) * NG + g;
-                        v[r][e] = lds32(vb + (uint32_t)((u ^ (u >> 2 & 3)) * 32 + n * 4));
-                    }
-                const uint32_t a0 = __byte_perm(v[0][0], v[0][1], 0x5410), a1 = __byte_perm(v[0][0], v[0][1], 0x7632);   // channels 0-3, 4-7
-                const uint32_t c0 = __byte_perm(v[1][0], v[1][1], 0x5410), c1 = __byte_perm(v[1][0], v[1][1], 0x7632);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t y = i < 2 ? a0 : a1, z = i < 2 ? c0 : c1;
-                    const int at = 8 * (i & 1);
-                    const uint32_t f0 = centred(y >> at), f1 = centred(y >> (at + 4)), f2 = centred(z >> at), f3 = centred(z >> (at + 4));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
                 }
             }
+            const bool fits = __low2float(total) <= kMostWeight && __high2float(total) <= kMostWeight;
+            if (grown || __any_sync(0xffffffffu, !fits)) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float step[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        uint32_t scale[2];
+                        load_scales<NG>(scale, sb + S::kScales + (r >> 1) * (S::kScales / 2) + (r & 1) * (8 * NG));
+                        step[r] = low_of(scale[g]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float most = 0.f;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) most = fmaxf(most, x[nt][r][e] * 0x1p-10f * step[r]);
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                            const int up = unit_up(most, grown ? shrunk[nt][e] : 1.f, unit[nt][e][g]);
+                            const float by = two_to(up / 2), by2 = two_to(up - up / 2);
+                            unit[nt][e][g] = unit[nt][e][g] * by * by2;
+#pragma unroll
+                            for (int i = 4 * g; i < 4 * g + 4; ++i) {
+                                o[nt][i][e] = o[nt][i][e] * by * by2;
+                                o[nt][i][2 + e] = o[nt][i][2 + e] * by * by2;
+                            }
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) weigh(nt, g, r, step[r]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    uint32_t b[NT][2];                   // turned to heads n, rows 2 t, 2 t + 1 (+ 8)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) b[nt][r] = transpose(w[nt][g][2 * hf + r]);
+                    uint32_t v[4];                       // channels 64 g + 16 i + 2 n and the next, of four keys
+                    ldsm_bytes(v, (vb ^ g * 32) + hf * (S::kCodes / 2));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t f0, f1, f2, f3;
+                        centred<0>(v[i], f0, f1);
+                        centred<1>(v[i], f2, f3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                    }
+                }
             __syncwarp();                                // all lanes have read the stage
         }
 
-        // Lane (n, t) has channels 64 g + 8 n .. of heads 2 t + e; both parts' lanes the same.
+        // Lane (n, t) has channels 16 i + 2 n and the next of heads 2 t + e; both parts' lanes the same.
         const bool whole = k_first == 0 && k_last == c.T;
         const int n_pre = whole ? prefix_parts(p, info.x) : 0;
         if (n_pre > 0) griddep_wait();                   // the prefix's results
@@ -409,20 +546,23 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float lt = l[nt][e], mt = m[nt][e], y[NG][8];
+                float lt = l[nt][e], mt = m[nt][e], y[NG * 4][2];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     float base = low[nt][e][g];
+                    const float by = 1.f / unit[nt][e][g];
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) base += __shfl_xor_sync(0xffffffffu, base, off);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[g][i] = o[nt][g * 4 + i / 2][(i & 1) * 2 + e];
-                        if (kTwoParts) y[g][i] += __shfl_xor_sync(0xffffffffu, y[g][i], 2);
-                        y[g][i] += base;
-                    }
+                    for (int i = 4 * g; i < 4 * g + 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            y[i][k] = o[nt][i][2 * k + e] * by;
+                            if (kTwoParts) y[i][k] += __shfl_xor_sync(0xffffffffu, y[i][k], 2);
+                            y[i][k] += base;
+                        }
                 }
                 const int rr = nt * kColumns + (kTwoParts ? (2 * t + e) & 3 : 2 * t + e), head = head0 + rr;
                 if (rr >= rows || (kTwoParts && t >= 2)) continue;
@@ -433,40 +573,22 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                     float w, w2;
                     join(mt, lt, ml.x, ml.y, w, w2);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g)
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const float4 v = *reinterpret_cast<const float4*>(p.pre_o + pr * D + g * kQ4Group + 8 * n + k);
-                            y[g][k] = y[g][k] * w + v.x * w2;
-                            y[g][k + 1] = y[g][k + 1] * w + v.y * w2;
-                            y[g][k + 2] = y[g][k + 2] * w + v.z * w2;
-                            y[g][k + 3] = y[g][k + 3] * w + v.w * w2;
-                        }
+                    for (int k = 0; k < NG * 4; ++k) {
+                        const float2 v = *reinterpret_cast<const float2*>(p.pre_o + pr * D + 16 * k + 2 * n);
+                        y[k][0] = y[k][0] * w + v.x * w2;
+                        y[k][1] = y[k][1] * w + v.y * w2;
+                    }
                 }
                 if (whole) {
                     const float inv = lt == 0.f ? 0.f : 1.f / lt;
-                    T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + 8 * n;
+                    T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + 2 * n;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        if (kTwoParts) {
-#pragma unroll
-                            for (int k = 0; k < 8; k += 4)
-                                *reinterpret_cast<float4*>(out + g * kQ4Group + k) =
-                                    make_float4(y[g][k] * inv, y[g][k + 1] * inv, y[g][k + 2] * inv, y[g][k + 3] * inv);
-                        } else {
-                            *reinterpret_cast<uint4*>(out + g * kQ4Group) =
-                                make_uint4(pack(y[g][0] * inv, y[g][1] * inv), pack(y[g][2] * inv, y[g][3] * inv),
-                                           pack(y[g][4] * inv, y[g][5] * inv), pack(y[g][6] * inv, y[g][7] * inv));
-                        }
-                    }
+                    for (int k = 0; k < NG * 4; ++k) write2(out + 16 * k, y[k][0] * inv, y[k][1] * inv);
                     if (n == 0) write_lse(a, s, head, mt, lt);
                 } else {
-                    float* out = p.part_o + (slot * kRows + rr) * D + 8 * n;
+                    float* out = p.part_o + (slot * kRows + rr) * D + 2 * n;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g)
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4)
-                            *reinterpret_cast<float4*>(out + g * kQ4Group + k) = make_float4(y[g][k], y[g][k + 1], y[g][k + 2], y[g][k + 3]);
+                    for (int k = 0; k < NG * 4; ++k) write2(out + 16 * k, y[k][0], y[k][1]);
                     if (n == 0) p.part_ml[slot * kRows + rr] = make_float2(mt, lt);
                 }
             }

@@ -28,12 +28,12 @@ struct AttnDecodeQ4Launch {
     AttnDecodeLaunch base;
     kda_cache_q4 cache;
 };
-constexpr int kQ4Keys = 16;                                 // keys of a tile
+constexpr int kQ4Keys = 32;                                 // keys of a tile
 // Products of eight columns a unit takes: one, or two where a key/value head's query heads do
 // not fit in one (fp32: two columns a head).
 __host__ __device__ constexpr int q4_columns(int dtype, int G) { return G <= (dtype == KDA_BF16 ? 8 : 4) ? 1 : 2; }
 __host__ __device__ constexpr int q4_rows(int dtype, int G) { return q4_columns(dtype, G) * (dtype == KDA_BF16 ? 8 : 4); }
-__host__ __device__ constexpr int q4_warps(int columns) { return columns == 1 ? 16 : 8; }   // of a thread block, one an SM
+__host__ __device__ constexpr int q4_warps(int columns) { return columns == 1 ? 12 : 8; }   // of a thread block, one an SM
 cudaError_t launch_decode_q4(const AttnDecodeQ4Launch& p, cudaStream_t s);
 
 }  // namespace kda

@@ -97,7 +97,8 @@ struct Cursor {
 };
 
 // The pieces of a thread block of NT threads with PIECES workers: fills at[] for
-// them (the caller's shared memory) and returns the line.  Thread i counts the tiles
+// them (the caller's shared memory) and returns the line.  Every unit that has tiles takes
+// `pad` more places on the line than it has.  Thread i counts the tiles
 // of its share of the sequences, one block scan gives the line's length, and the
 // thread whose share holds a piece's first tile walks it again.
 struct PieceStart {
@@ -106,13 +107,17 @@ struct PieceStart {
     int64_t rel;           // tiles past the first of s
 };
 template <int NT, int PIECES>
-__device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, PieceStart* at) {
+__device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys, PieceStart* at, int pad = 0) {
+    auto places = [&](int2 info) {
+        const int64_t t = seq_tiles(info, tile_keys);
+        return t > 0 ? t + pad : t;
+    };
     __shared__ int64_t scan_buf[NT / 32];
     const int32_t n = p.a.n_seqs;
     const int32_t share = (n + NT - 1) / NT, s0 = min(n, (int32_t)threadIdx.x * share), s1 = min(n, s0 + share);
     int64_t mine = 0;
 #pragma unroll 4
-    for (int32_t s = s0; s < s1; ++s) mine += seq_tiles(seq_info(p, s), tile_keys);
+    for (int32_t s = s0; s < s1; ++s) mine += places(seq_info(p, s));
     int64_t total;
     const int64_t before = block_scan<NT>(mine, scan_buf, &total) - mine;
     const Line line(total * units, p.n_pieces, decode_least_tiles(divide(total, n)));
@@ -124,7 +129,7 @@ __device__ Line find_pieces(const AttnDecodeLaunch& p, int units, int tile_keys,
         int64_t x = before;
         for (int32_t s = s0;; ++s) {
             const int2 info = seq_info(p, s);
-            const int64_t t = seq_tiles(info, tile_keys);
+            const int64_t t = places(info);
             if (begin < (x + t) * units) {
                 at[i] = PieceStart{s, info, begin - x * units};
                 break;
@@ -184,7 +189,7 @@ __device__ __forceinline__ void write_lse(const kda_attn_decode_args& a, int32_t
 }
 
 // (m, l, o) of one row as a warp holds it, D / 32 columns a lane, and partial results
-// added to it.  They come from L2, a microsecond away: four are asked for at a time.
+// added to it.  They come from L2, a microsecond away: kAtOnce are asked for at a time.
 template <int D> struct RowSum {
     static constexpr int kCols = D / 32;
     float m, l, o[kCols];
@@ -201,8 +206,7 @@ template <int D> struct RowSum {
         for (int e = 0; e < kCols; ++e) o[e] = o[e] * w + x[e] * w2;
     }
     // Parts from .. to - 1 in turn; where(i, ml, o) names the i-th one's place.
-    template <typename Where> __device__ __forceinline__ void add_parts(int64_t from, int64_t to, int lane, Where where) {
-        constexpr int kAtOnce = 4;
+    template <int kAtOnce = 4, typename Where> __device__ __forceinline__ void add_parts(int64_t from, int64_t to, int lane, Where where) {
         for (int64_t i = from; i < to; i += kAtOnce) {
             float2 ml[kAtOnce];
             alignas(8) float x[kAtOnce][kCols];

@@ -53,6 +53,19 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// All of a half tile that is this lane's: every 16th piece of its codes, alternately from c0 and
+// c1 on, and one of its scales.
+template <int D>
+__device__ __forceinline__ void copy_half(uint32_t c0, uint32_t c1, uint32_t sc, const uint8_t* k, const uint8_t* v, const uint8_t* from, int l16) {
+    constexpr int kCodes = kKeys * D / 2;
+#pragma unroll
+    for (int i = 0; i < kCodes / 512; ++i) {
+        copy16((i & 1 ? c1 : c0) + (i & ~1) * 256, k + i * 256);
+        copy16((i & 1 ? c1 : c0) + (i & ~1) * 256 + kCodes, v + i * 256);
+    }
+    if (D == 128 || l16 < 8) copy16(sc, from);
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
@@ -165,6 +178,37 @@ __device__ __forceinline__ int unit_up(float most, float shrunk, float unit) {
 }
 __device__ __forceinline__ float two_to(int i) { return __uint_as_float((uint32_t)(i + 127) << 23); }
 
+// A worker's place on the line: unit u of sequence s at tile k of its T.  A unit takes some
+// places more than it has tiles (q4_pad), for the time that its beginning and end take; a piece
+// that ends among those holds the unit to its end, one that starts there starts with the next.
+struct Place {
+    int64_t left;      // of the piece from here on
+    int32_t s, u, units;
+    int32_t k, T;
+    int2 info;
+
+    __device__ __forceinline__ int run() const { return (int)min((int64_t)(T - k), left); }
+    __device__ __forceinline__ bool whole() const { return k == 0 && left >= T; }
+    __device__ __forceinline__ void next_unit(const AttnDecodeLaunch& p, int pad) {
+        left -= T + pad - k;
+        k = 0;
+        if (++u < units || left <= 0) return;
+        u = 0;
+        do {
+            info = seq_info(p, ++s);
+            T = (int)seq_tiles(info, kKeys);
+        } while (T == 0);
+    }
+    __device__ __forceinline__ Place() {}
+    __device__ __forceinline__ Place(const AttnDecodeLaunch& p, const PieceStart& at, int64_t length, int units_, int pad) {
+        left = length, s = at.s, units = units_, info = at.info;
+        T = (int)seq_tiles(info, kKeys);
+        u = (int32_t)divide(at.rel, T + pad);
+        k = (int32_t)(at.rel - (int64_t)u * (T + pad));
+        if (k >= T) next_unit(p, pad);
+    }
+};
+
 // A unit's query heads are the columns of NT products of eight: all heads' own (bf16), or
 // four heads twice, for both parts (fp32).
 template <typename T, int D, int NT, int WARPS>
@@ -180,15 +224,23 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
     __shared__ PieceStart at_[WARPS];
-    const Line line = find_pieces<32 * WARPS, WARPS>(p, a.n_kv_heads * blocks, kKeys, at_);
+    const int pad = q4_pad(a);
+    const Line line = find_pieces<32 * WARPS, WARPS>(p, a.n_kv_heads * blocks, kKeys, at_, pad);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * WARPS + warp;
-    if (piece >= line.pieces) {
+    Place first;
+    first.left = 0;
+    if (piece < line.pieces) first = Place(p, at_[warp], line.begin(piece + 1) - line.begin(piece), a.n_kv_heads * blocks, pad);
+    if (first.left <= 0) {
         if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
         finish_empty<T, D>(p, piece, lane);
         return;
     }
-    Cursor c = start(at_[warp], line, piece, a.n_kv_heads * blocks, kKeys);
+    // The places on the line are looked at where units begin and end: they wait in shared memory
+    // meanwhile, which leaves the registers to the tiles.
+    __shared__ Place here[WARPS], ahead[WARPS];
+    here[warp] = ahead[warp] = first;
+    __syncwarp();
 
     // ------------------------------------------------------------------ copies
     // The copies' own place on the line, kStages - 1 tiles ahead: cursor f at the first tile of
@@ -196,60 +248,62 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     // half of the tile.  A group's 32 bytes of codes, unit u = key * NG + g of its half, lie at
     // u ^ (u / 4 % 4): what eight lanes of a product read together is in eight banks' worth of
     // different places.
-    Cursor f = c;
     const uint32_t ring = smem_u32(smem_raw) + (uint32_t)(warp * kStages * S::kTile);
     const int page_shift = __ffs(a.block_size) - 1, half = lane >> 4, l16 = lane & 15;
-    int f_run = (int)f.run(), f_key = f.info.x + (int)f.k * kKeys + half * kHalf, f_head = f.u / blocks;
-    const int32_t* f_row = a.block_table + (int64_t)f.s * a.table_stride;
+    const int page_mask = a.block_size - 1;
+    const uint32_t page_rows = (uint32_t)(a.n_kv_heads * a.block_size), n_blocks = (uint32_t)cache.n_blocks;
+    int f_run, f_key, f_end;
+    uint32_t f_head_row;
+    const int32_t* f_row;
+    auto enter = [&](const Place& f) {
+        f_run = f.run(), f_key = f.info.x + f.k * kKeys + half * kHalf, f_end = f.info.y;
+        f_head_row = (uint32_t)(f.u / blocks * a.block_size);
+        f_row = a.block_table + (int64_t)f.s * a.table_stride;
+    };
+    enter(ahead[warp]);
     int32_t next_block = 0;                              // this half's table entry at f_key
     // places in shared memory: piece y = 16 i + l16 of a half's codes, and one piece of its scales
     constexpr int kPieces = S::kScales / 2 / 16, kPieceKeys = 4 / NG;
     const int scale_piece = l16 % kPieces, scale_is_v = l16 / kPieces;
     const uint32_t code0 = ring + half * (S::kCodes / 2) + (l16 >> 3) * 128 + ((l16 & 7) ^ (l16 >> 3) * (NG == 2 ? 1 : 5)) * 16;
     const uint32_t scale_to = ring + 2 * S::kCodes + scale_is_v * S::kScales + half * (S::kScales / 2) + scale_piece * 16;
-    auto code_to = [&](uint32_t tile, int i) { return ((code0 + tile) ^ (NG == 2 ? (2 * i & 3) * 16 : 0)) + i * 256; };
+    auto code_to = [&](uint32_t tile, int i) { return ((code0 + tile) ^ (NG == 2 ? 32 * i : 0)) + i * 256; };     // i: 0, 1; then 512 on
     const uint8_t* k_from = static_cast<const uint8_t*>(cache.k_codes) + l16 * 16;
     const uint8_t* v_from = static_cast<const uint8_t*>(cache.v_codes) + l16 * 16;
     const uint8_t* scale_from = static_cast<const uint8_t*>(scale_is_v ? cache.v_scales : cache.k_scales) + scale_piece * 16;
-    auto look_up = [&]() { next_block = f_run > 0 && f_key < f.info.y ? f_row[f_key >> page_shift] : -2; };
+    auto look_up = [&]() { if (f_key < f_end) next_block = f_row[f_key >> page_shift]; };
     auto fetch = [&](int stage) {
         if (f_run > 0) {
-            int live = min(kHalf, f.info.y - f_key);                         // keys of the half that exist
-            if (live > 0 && (next_block < 0 || next_block >= cache.n_blocks)) {
-                flag(p.status, KDA_DEV_BAD_SLOT);
-                live = 0;
-            }
-            // (rows are below 2^31; a half lies in one page, so that those of missing keys may be named too)
-            const uint32_t row = live > 0 ? ((uint32_t)next_block * a.n_kv_heads + f_head) * a.block_size + (f_key & (a.block_size - 1)) : 0u;
             const uint32_t to = (uint32_t)(stage * S::kTile);
-            const uint8_t* kc = k_from + (uint64_t)row * (D / 2);
-            const uint8_t* vc = v_from + (uint64_t)row * (D / 2);
-            const uint8_t* sc_from = scale_from + (uint64_t)row * (NG * 4);
-            if (__all_sync(0xffffffffu, live == kHalf)) {
-#pragma unroll
-                for (int i = 0; i < S::kCodes / 2 / 256; ++i) {
-                    copy16(code_to(to, i), kc + i * 256);
-                    copy16(code_to(to, i) + S::kCodes, vc + i * 256);
-                }
-                if (l16 < 2 * kPieces) copy16(scale_to + to, sc_from);
+            const int live = f_end - f_key;                                  // keys from here on
+            const bool known = (uint32_t)next_block < n_blocks;
+            // (rows are below 2^31; a half lies in one page, so that those of missing keys may be named too)
+            const uint32_t row = (uint32_t)next_block * page_rows + (f_head_row + (f_key & page_mask));
+            if (__all_sync(0xffffffffu, known && live >= kHalf)) {
+                copy_half<D>(code_to(to, 0), code_to(to, 1), scale_to + to, k_from + (uint64_t)row * (D / 2), v_from + (uint64_t)row * (D / 2),
+                             scale_from + (uint64_t)row * (NG * 4), l16);
             } else {
+                if (live > 0 && !known) flag(p.status, KDA_DEV_BAD_SLOT);
+                const int have = known ? max(0, min(kHalf, live)) : 0;
+                const uint64_t from = have > 0 ? row : 0;
 #pragma unroll
                 for (int i = 0; i < S::kCodes / 2 / 256; ++i) {
-                    const int bytes = (i * 16 + l16) / (2 * NG) < live ? 16 : 0;
-                    copy16(code_to(to, i), kc + i * 256, bytes);
-                    copy16(code_to(to, i) + S::kCodes, vc + i * 256, bytes);
+                    const int bytes = (i * 16 + l16) / (2 * NG) < have ? 16 : 0;
+                    copy16(code_to(to, i & 1) + (i & ~1) * 256, k_from + from * (D / 2) + i * 256, bytes);
+                    copy16(code_to(to, i & 1) + (i & ~1) * 256 + S::kCodes, v_from + from * (D / 2) + i * 256, bytes);
                 }
-                if (l16 < 2 * kPieces) copy16(scale_to + to, sc_from, max(0, min(16, (live - scale_piece * kPieceKeys) * NG * 4)));
+                if (l16 < 2 * kPieces) copy16(scale_to + to, scale_from + from * (NG * 4), max(0, min(16, (have - scale_piece * kPieceKeys) * NG * 4)));
             }
             f_key += kKeys;
             if (--f_run == 0) {
-                f.next_unit(p, kKeys);
-                if (f.left > 0) {
-                    f_run = (int)f.run(), f_key = f.info.x + half * kHalf, f_head = f.u / blocks;
-                    f_row = a.block_table + (int64_t)f.s * a.table_stride;
-                }
+                Place f = ahead[warp];
+                f.next_unit(p, pad);
+                __syncwarp();
+                ahead[warp] = f;
+                __syncwarp();
+                if (f.left > 0) enter(f);
             }
-            look_up();
+            if (f_run > 0) look_up();
         }
         copy_commit();
     };
@@ -271,12 +325,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     const uint32_t s0 = ring + 2 * S::kCodes + own_key * NG * 4;
     auto k_at = [](uint32_t k, int r, int g) { return NG == 2 ? (k ^ (g * 32 + r * 16)) + r * 128 : k ^ r * 64; };
     int stage = 0;
-    while (c.left > 0) {
-        const int64_t k_first = c.k, k_last = c.k + c.run();
-        const int32_t s = c.s;
-        const int hk = c.u / blocks, rb = c.u % blocks;
-        const int head0 = hk * G + rb * kRows, rows = min(kRows, G - rb * kRows);
-        const int2 info = c.info;
+    bool more = true;
+    while (more) {
+        int kt, live;                                    // tiles of the unit in this piece, keys from the first one on
+        const Place c = here[warp];
+        kt = c.run(), live = c.info.y - (c.info.x + c.k * kKeys);
 
         // q of column n, 16 channels of each group from 64 g + 16 t, as the operands that meet
         // a word's codes: (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16.
@@ -286,15 +339,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * kColumns + n % kColumns;
-            const bool live = r < rows;
-            const T* qs = static_cast<const T*>(a.q) + s * a.q_stride + (int64_t)(head0 + (live ? r : 0)) * D + 16 * t;
+            const bool is_row = r < min(kRows, G - c.u % blocks * kRows);
+            const T* qs = static_cast<const T*>(a.q) + c.s * a.q_stride + (int64_t)(c.u / blocks * G + c.u % blocks * kRows + (is_row ? r : 0)) * D + 16 * t;
             float x[NG][16], most = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 load16(qs + g * kQ4Group, x[g]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    x[g][e] = live ? x[g][e] : 0.f;
+                    x[g][e] = is_row ? x[g][e] : 0.f;
                     most = fmaxf(most, fabsf(x[g][e]));
                 }
             }
@@ -347,8 +400,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
             }
         }
 
-        int live = info.y - (info.x + (int)k_first * kKeys);                 // keys from this tile on
-        for (int kt = (int)(k_last - k_first); kt > 0; --kt, live -= kKeys) {
+        for (; kt > 0; --kt, live -= kKeys) {
             copy_wait<kStages - 2>();
             __syncwarp();                                // the tile is there, and the stage before it is read
             fetch(stage == 0 ? kStages - 1 : stage - 1);
@@ -538,10 +590,13 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         }
 
         // Lane (n, t) has channels 16 i + 2 n and the next of heads 2 t + e; both parts' lanes the same.
-        const bool whole = k_first == 0 && k_last == c.T;
-        const int n_pre = whole ? prefix_parts(p, info.x) : 0;
+        Place done = here[warp];
+        const int32_t s = done.s;
+        const int head0 = done.u / blocks * G + done.u % blocks * kRows, rows = min(kRows, G - done.u % blocks * kRows);
+        const bool whole = done.whole();
+        const int n_pre = whole ? prefix_parts(p, done.info.x) : 0;
         if (n_pre > 0) griddep_wait();                   // the prefix's results
-        const int64_t slot = part_slot(piece, k_first == 0);
+        const int64_t slot = part_slot(piece, done.k == 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -592,12 +647,118 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                     if (n == 0) p.part_ml[slot * kRows + rr] = make_float2(mt, lt);
                 }
             }
+        const int64_t at = line.begin(piece + 1) - done.left;                // of tile done.k
+        const bool goes_on = done.k == 0 && !whole;      // begins here and ends in a later piece: the join's
+        const int4 note = goes_on ? make_int4(s, done.u, (int)line.piece_of(at + done.T - 1), prefix_parts(p, done.info.x)) : make_int4(-1, 0, 0, 0);
+        done.next_unit(p, pad);
+        more = done.left > 0;
+        if (lane == 0 && !more) p.open[piece] = note;
         __syncwarp();
-        if (lane == 0 && c.left == c.run()) p.open[piece] = open_unit(p, c, piece, line);
-        c.next_unit(p, kKeys);
+        here[warp] = done;
+        __syncwarp();
     }
     copy_wait<0>();
     finish_empty<T, D>(p, piece, lane);
+}
+
+// The join of units that several pieces share, as join_kernel does it: parts in the order of the
+// prefix's blocks and then the pieces.  A row is one warp's where units have few parts (narrow),
+// the warps of a row's block then share them where there are many: every thread block counts
+// the open units itself and takes its share of their rows.
+struct OpenRow {
+    int4 open;            // sequence, unit, last piece, prefix parts
+    int64_t c0;           // the piece in which the unit begins
+    int r, head;          // row of the unit, query head
+    int64_t parts;
+    __device__ __forceinline__ OpenRow(const AttnDecodeLaunch& p, int64_t c, int row, int unit_rows) : open(p.open[c]), c0(c), r(row) {
+        const int G = p.a.n_heads / p.a.n_kv_heads, blocks = (G + unit_rows - 1) / unit_rows;
+        const int rb = open.y % blocks;
+        head = r < G - rb * unit_rows ? open.y / blocks * G + rb * unit_rows + r : -1;
+        parts = open.w + open.z - c0 + 1;
+    }
+};
+template <typename T, int D, int ROWS, int kAtOnce>
+__device__ __forceinline__ void add_row(const AttnDecodeLaunch& p, const OpenRow& x, RowSum<D>& sum, int64_t from, int64_t to, int lane) {
+    sum.template add_parts<kAtOnce>(from, to, lane, [&](int64_t i, const float2*& ml, const float*& o) {
+        if (i < x.open.w) {
+            const int64_t at = prefix_row(p, (int)i, x.open.x, x.head);
+            ml = p.pre_ml + at;
+            o = p.pre_o + at * D;
+        } else {
+            const int64_t at = part_slot(x.c0 + i - x.open.w, i == x.open.w) * ROWS + x.r;
+            ml = p.part_ml + at;
+            o = p.part_o + at * D;
+        }
+    });
+}
+
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBlocks = 304;
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) join_narrow_kernel(const __grid_constant__ AttnDecodeLaunch p, int unit_rows) {
+    griddep_wait();
+    const int64_t x = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5), c = x / unit_rows;
+    if (c >= p.n_pieces || p.open[c].x < 0) return;
+    const int lane = threadIdx.x & 31;
+    const OpenRow row(p, c, (int)(x - c * unit_rows), ROWS);
+    if (row.head < 0) return;
+    RowSum<D> sum;
+    add_row<T, D, ROWS, 4>(p, row, sum, 0, row.parts, lane);
+    sum.template write<T>(p.a, row.open.x, row.head, lane);
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) join_wide_kernel(const __grid_constant__ AttnDecodeLaunch p, int unit_rows) {
+    constexpr int kCols = D / 32;
+    __shared__ int32_t scan_buf[kJoinWarps], s_piece;
+    __shared__ float s_o[kJoinWarps][D];
+    __shared__ float2 s_ml[kJoinWarps];
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int share = (p.n_pieces + kJoinThreads - 1) / kJoinThreads, lo = min(p.n_pieces, tid * share), hi = min(p.n_pieces, lo + share);
+    int32_t mine = 0, total;
+    for (int c = lo; c < hi; ++c) mine += p.open[c].x >= 0;
+    const int32_t before = block_scan<kJoinThreads>(mine, scan_buf, &total) - mine;
+    for (int64_t i = blockIdx.x; i < (int64_t)total * unit_rows; i += gridDim.x) {
+        const int32_t unit = (int32_t)(i / unit_rows);
+        __syncthreads();                                 // s_piece and the last row's parts are read
+        if (unit >= before && unit < before + mine) {
+            int c = lo - 1;
+            for (int32_t left = unit - before; left >= 0; --left)
+                while (p.open[++c].x < 0) {}
+            s_piece = c;
+        }
+        __syncthreads();
+        const OpenRow row(p, s_piece, (int)(i - (int64_t)unit * unit_rows), ROWS);
+        if (row.head < 0) continue;                      // (all threads alike)
+        RowSum<D> sum;
+        const int64_t per = (row.parts + kJoinWarps - 1) / kJoinWarps;
+        add_row<T, D, ROWS, 8>(p, row, sum, min(row.parts, warp * per), min(row.parts, (warp + 1) * per), lane);
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) s_o[warp][lane * kCols + e] = sum.o[e];
+        if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kJoinWarps; ++w) {
+                float x[kCols];
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) x[e] = s_o[w][lane * kCols + e];
+                sum.add(s_ml[w], x);
+            }
+            sum.template write<T>(p.a, row.open.x, row.head, lane);
+        }
+    }
+}
+
+template <typename T, int D, int ROWS>
+cudaError_t launch_q4_join(const AttnDecodeLaunch& p, cudaStream_t s) {
+    const int G = p.a.n_heads / p.a.n_kv_heads, unit_rows = G < ROWS ? G : ROWS;
+    const int64_t units = (int64_t)p.a.n_seqs * p.a.n_kv_heads * ((G + ROWS - 1) / ROWS);
+    note_launch();
+    if (p.n_pieces >= 16 * units)
+        return launch_overlapped(join_wide_kernel<T, D, ROWS>, dim3(kJoinBlocks), dim3(kJoinThreads), 0, s, p, unit_rows);
+    const int64_t rows = (int64_t)p.n_pieces * unit_rows;
+    return launch_overlapped(join_narrow_kernel<T, D, ROWS>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinThreads), 0, s, p, unit_rows);
 }
 
 template <typename T, int D, int NT>
@@ -608,7 +769,7 @@ cudaError_t launch_t(const AttnDecodeQ4Launch& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     note_launch();
     e = launch_overlapped(decode_q4_kernel<T, D, NT, WARPS>, dim3(p.base.n_pieces / WARPS), dim3(32 * WARPS), kBytes, s, p);
-    return e == cudaSuccess ? launch_join<T, D, kRows>(p.base, s) : e;
+    return e == cudaSuccess ? launch_q4_join<T, D, kRows>(p.base, s) : e;
 }
 template <typename T, int D>
 cudaError_t launch_d(const AttnDecodeQ4Launch& p, cudaStream_t s) {

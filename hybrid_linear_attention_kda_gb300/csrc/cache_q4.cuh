@@ -34,6 +34,7 @@ constexpr int kQ4Keys = 32;                                 // keys of a tile
 __host__ __device__ constexpr int q4_columns(int dtype, int G) { return G <= (dtype == KDA_BF16 ? 8 : 4) ? 1 : 2; }
 __host__ __device__ constexpr int q4_rows(int dtype, int G) { return q4_columns(dtype, G) * (dtype == KDA_BF16 ? 8 : 4); }
 __host__ __device__ constexpr int q4_warps(int columns) { return columns == 1 ? 12 : 8; }   // of a thread block, one an SM
+__host__ __device__ constexpr int q4_pad(const kda_attn_decode_args& a) { return a.n_groups > 0 ? 4 : 2; }
 cudaError_t launch_decode_q4(const AttnDecodeQ4Launch& p, cudaStream_t s);
 
 }  // namespace kda

@@ -47,78 +47,129 @@ template <> struct Eight<float> {
     }
 };
 
+// The values of a word's codes, as T, each rounded once.  Codes become numbers as the low bits of
+// 2^23, or of 128 in bf16, less that; bf16's are formed four apart and put in order.
+__device__ __forceinline__ void values_of(uint32_t w, uint32_t scale, Eight<float>& out) {
+    const float step = __uint_as_float(scale << 16), low = __uint_as_float(scale & 0xFFFF0000u);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(__uint_as_float((w >> 4 * e & 15u) | 0x4B000000u) - 8388608.f, step, low);
+    out.close(v);
+}
+__device__ __forceinline__ void values_of(uint32_t w, uint32_t scale, Eight<__nv_bfloat16>& out) {
+    const uint32_t steps = __byte_perm(scale, scale, 0x1010), lows = __byte_perm(scale, scale, 0x3232), none = 0x43004300u;
+    uint32_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {                            // channels e and e + 4
+        const uint32_t n = (w >> 4 * e & 0x000F000Fu) | none;
+        const __nv_bfloat162 r = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&n), *reinterpret_cast<const __nv_bfloat162*>(&none)),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&steps), *reinterpret_cast<const __nv_bfloat162*>(&lows));
+        v[e] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    out.r = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+// The smallest and the largest of a lane's eight channels, NaN where one is.  bf16 in pairs.
+__device__ __forceinline__ void range_of(const Eight<float>&, const float (&x)[8], float& lo, float& hi) {
+    lo = hi = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) lo = min_nan(lo, x[e]), hi = max_nan(hi, x[e]);
+}
+__device__ __forceinline__ void range_of(const Eight<__nv_bfloat16>& v, const float (&)[8], float& lo, float& hi) {
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v.r);
+    const __nv_bfloat162 a = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
+    const __nv_bfloat162 b = __hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3]));
+    lo = min_nan(__low2float(a), __high2float(a)), hi = max_nan(__low2float(b), __high2float(b));
+}
+
 constexpr int kAppendVecs = 2;
+constexpr float kMagic = 12582912.f;     // 1.5 * 2^23: adding it rounds to integers, which its low bits then hold
 
 // A thread takes eight channels, eight lanes a group.  A thread block takes whole tokens (k
-// and v, all heads): block_tokens of them.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ CacheAppendQ4Launch p, int32_t block_tokens) {
+// and v, all heads): block_tokens of them; `row_magic` divides by a token's pieces of one
+// tensor, as ceil(2^40 / row_vecs).
+//
+// The definition's quotient is the correctly rounded one.  A product with 1 / s is within 2^-18
+// of it, and rounds to the same integer unless it lies that near the middle of two: those lanes
+// divide.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ CacheAppendQ4Launch p, int32_t block_tokens, uint64_t row_magic) {
+    constexpr uint32_t kHeadVecs = D / 8;
     griddep_wait();
     const kda_cache_append_q4_args& a = p.a;
-    const uint32_t head_vecs = (uint32_t)a.d / 8, row_vecs = head_vecs * (uint32_t)a.n_kv_heads, page = (uint32_t)a.cache.block_size;
-    const int64_t t0 = (int64_t)blockIdx.x * block_tokens, n_slots = a.cache.n_blocks * a.cache.block_size;
+    const uint32_t row_vecs = kHeadVecs * (uint32_t)a.n_kv_heads;
+    const int shift = __ffs(a.cache.block_size) - 1;
+    const int64_t t0 = (int64_t)blockIdx.x * block_tokens, n_slots = a.cache.n_blocks << shift;
     const uint32_t n = 2 * row_vecs * (uint32_t)min((int64_t)block_tokens, a.n_tokens - t0);
-    const int lane = threadIdx.x & 31;
     for (uint32_t base = 0; base < n; base += kThreads * kAppendVecs) {
         Eight<T> in[kAppendVecs];
         int32_t slot[kAppendVecs];
+        uint32_t half[kAppendVecs], y[kAppendVecs];      // 2 * token, or that + 1 for v; piece of the token's row
 #pragma unroll
         for (int m = 0; m < kAppendVecs; ++m) {
             const uint32_t i = base + m * kThreads + threadIdx.x;
             in[m] = Eight<T>{};
             slot[m] = -1;
+            half[m] = (uint32_t)(i * row_magic >> 40), y[m] = i - half[m] * row_vecs;
             if (i >= n) continue;
-            const uint32_t half = i / row_vecs, x = i - half * row_vecs;     // half: 2 * token, or that + 1 for v
-            const int64_t t = t0 + (half >> 1);
+            const int64_t t = t0 + (half[m] >> 1);
             slot[m] = a.slot_map[t];
-            const T* from = static_cast<const T*>(half & 1 ? a.v : a.k) + t * (half & 1 ? a.v_stride : a.k_stride) + x * 8;
-            in[m] = *reinterpret_cast<const Eight<T>*>(from);
+            in[m] = *reinterpret_cast<const Eight<T>*>(static_cast<const T*>(half[m] & 1 ? a.v : a.k) + t * (half[m] & 1 ? a.v_stride : a.k_stride) + y[m] * 8);
         }
 #pragma unroll
         for (int m = 0; m < kAppendVecs; ++m) {
-            const uint32_t i = base + m * kThreads + threadIdx.x;
-            float x[8];
+            float x[8], lo, hi;
             in[m].open(x);
-            float lo = x[0], hi = x[0];
-            bool odd = false;                                // something is not finite
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
-                odd |= !(fabsf(x[e]) <= FLT_MAX);
-            }
+            range_of(in[m], x, lo, hi);
 #pragma unroll
             for (int off = 1; off < 8; off <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+                lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+                hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
             }
-            const uint32_t odd_lanes = __ballot_sync(0xffffffffu, odd) >> (lane & 24) & 0xFFu;
             float low = bf16_down(lo), step = bf16_up(__fdiv_rn(__fsub_rn(hi, low), 15.f));
-            const bool fine = !odd_lanes && low >= -FLT_MAX && __fsub_rn(hi, low) <= FLT_MAX && step <= FLT_MAX;
+            const bool fine = fabsf(low) <= FLT_MAX && __fsub_rn(hi, low) <= FLT_MAX && step <= FLT_MAX;      // (no, with a NaN)
             if (!fine) low = CUDART_NAN_F, step = 0.f;
-            uint32_t codes = 0;
+            float c[8], most = 0.f;                      // codes; how far from its integer a quotient is
+            float by;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(step));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                uint32_t code = 0;
-                if (step > 0.f) code = min(__float2uint_rn(__fdiv_rn(__fsub_rn(x[e], low), step)), 15u);
-                codes |= code << (4 * e);
-                x[e] = fmaf((float)code, step, low);
+                const float t = __fsub_rn(x[e], low);
+                c[e] = fmaf(t, by, kMagic) - kMagic;
+                most = fmaxf(most, fabsf(fmaf(t, by, -c[e])));
             }
+            // (a tiny step's inverse is not a number to go by; nor is there a middle to be near without one)
+            if (!(most <= 0.5f - 0x1p-16f) || !(step >= 0x1p-100f)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) c[e] = step > 0.f ? fminf(rintf(__fdiv_rn(__fsub_rn(x[e], low), step)), 15.f) : 0.f;
+            }
+            // four codes fit a float's integers
+            const float c03 = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]) + kMagic, c47 = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]) + kMagic;
+            const uint32_t codes = __byte_perm(__float_as_uint(c03), __float_as_uint(c47), 0x5410);
             if (slot[m] < 0 || slot[m] >= n_slots) {
                 if (slot[m] != -1) flag(p.status, KDA_DEV_BAD_SLOT);
                 continue;
             }
-            const uint32_t half = i / row_vecs, y = i - half * row_vecs, h = y / head_vecs, e = y - h * head_vecs;
-            const bool is_v = half & 1;
-            const uint32_t block = (uint32_t)slot[m] / page, off = (uint32_t)slot[m] - block * page;
-            const int64_t row = ((int64_t)block * a.n_kv_heads + h) * page + off;
-            static_cast<uint32_t*>(is_v ? a.cache.v_codes : a.cache.k_codes)[row * head_vecs + e] = codes;
-            if (e % 8 == 0)
-                static_cast<uint32_t*>(is_v ? a.cache.v_scales : a.cache.k_scales)[row * (head_vecs / 8) + e / 8] =
-                    __float_as_uint(step) >> 16 | (__float_as_uint(low) & 0xFFFF0000u);
+            const bool is_v = half[m] & 1;
+            const uint32_t h = y[m] / kHeadVecs, e = y[m] % kHeadVecs;
+            const int64_t row = (((int64_t)(slot[m] >> shift) * a.n_kv_heads + h) << shift) + (slot[m] & (a.cache.block_size - 1));
+            static_cast<uint32_t*>(is_v ? a.cache.v_codes : a.cache.k_codes)[row * kHeadVecs + e] = codes;
+            const uint32_t scale = __float_as_uint(step) >> 16 | (__float_as_uint(low) & 0xFFFF0000u);
+            if (e % 8 == 0) static_cast<uint32_t*>(is_v ? a.cache.v_scales : a.cache.k_scales)[row * (kHeadVecs / 8) + e / 8] = scale;
             void* out = is_v ? a.v_out : a.k_out;
             if (out) {
-                in[m].close(x);
-                *reinterpret_cast<Eight<T>*>(static_cast<T*>(out) + (t0 + (half >> 1)) * (is_v ? a.v_out_stride : a.k_out_stride) + y * 8) = in[m];
+                values_of(codes, scale, in[m]);
+                *reinterpret_cast<Eight<T>*>(static_cast<T*>(out) + (t0 + (half[m] >> 1)) * (is_v ? a.v_out_stride : a.k_out_stride) + y[m] * 8) = in[m];
             }
         }
     }
@@ -127,16 +178,6 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
 // ------------------------------------------------------------------ read-back
 
 constexpr int kWarps = kThreads / 32, kRows = 16;           // an item: 16 positions of one head
-
-// Eight values of codes w, as T.
-template <typename T> __device__ __forceinline__ void write_eight(T* to, uint32_t w, float step, float low) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf((float)(w >> (4 * e) & 15u), step, low);
-    Eight<T> v;
-    v.close(x);
-    *reinterpret_cast<Eight<T>*>(to) = v;
-}
 
 // Items in the order of sequences, positions, heads, dealt to the warps in turn, so that all
 // warps work side by side whatever the lengths are.  Every thread block runs the (short)
@@ -207,10 +248,9 @@ __global__ void __launch_bounds__(kThreads) unpack_q4_kernel(const __grid_consta
                 for (int k = 0; k < kSteps; ++k) {
                     const int32_t pos = pos0 + own_row + k * kAtOnce;
                     if (pos < r.x || pos >= r.y) continue;
-                    const float step = __uint_as_float(scale[v][k] << 16), low = __uint_as_float(scale[v][k] & 0xFFFF0000u);
-                    T* out = static_cast<T*>(v ? a.v_cache : a.k_cache) + (dst + k * kAtOnce) * D + own * 16;
-                    write_eight(out, codes[v][k].x, step, low);
-                    write_eight(out + 8, codes[v][k].y, step, low);
+                    Eight<T>* out = reinterpret_cast<Eight<T>*>(static_cast<T*>(v ? a.v_cache : a.k_cache) + (dst + k * kAtOnce) * D + own * 16);
+                    values_of(codes[v][k].x, scale[v][k], out[0]);
+                    values_of(codes[v][k].y, scale[v][k], out[1]);
                 }
         }
         base += total;
@@ -232,9 +272,12 @@ cudaError_t launch_append_q4(const CacheAppendQ4Launch& p, cudaStream_t s) {
     const int32_t fit = kThreads * kAppendVecs / (2 * p.a.n_kv_heads * (p.a.d / 8));
     const int32_t block_tokens = fit > 1 && p.a.n_tokens > 2 * 152 * (int64_t)fit ? fit : 1;
     const dim3 grid((unsigned)((p.a.n_tokens + block_tokens - 1) / block_tokens));
+    const uint64_t row_vecs = (uint64_t)p.a.n_kv_heads * (p.a.d / 8), magic = ((1ull << 40) + row_vecs - 1) / row_vecs;
+    const bool wide = p.a.d == 128;
     note_launch();
-    return p.a.dtype == KDA_BF16 ? launch_overlapped(append_q4_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, p, block_tokens)
-                                 : launch_overlapped(append_q4_kernel<float>, grid, dim3(kThreads), 0, s, p, block_tokens);
+    if (p.a.dtype == KDA_BF16)
+        return launch_overlapped(wide ? append_q4_kernel<__nv_bfloat16, 128> : append_q4_kernel<__nv_bfloat16, 64>, grid, dim3(kThreads), 0, s, p, block_tokens, magic);
+    return launch_overlapped(wide ? append_q4_kernel<float, 128> : append_q4_kernel<float, 64>, grid, dim3(kThreads), 0, s, p, block_tokens, magic);
 }
 
 cudaError_t launch_unpack_q4(const CacheUnpackQ4Launch& p, cudaStream_t s) {

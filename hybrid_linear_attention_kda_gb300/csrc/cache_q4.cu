@@ -79,98 +79,120 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
-// The smallest and the largest of a lane's eight channels, NaN where one is.  bf16 in pairs.
+// The smallest and the largest of a group, eight lanes' channels; NaN where one is.  bf16 in
+// pairs, and the lanes' as (smallest, - largest).
 __device__ __forceinline__ void range_of(const Eight<float>&, const float (&x)[8], float& lo, float& hi) {
     lo = hi = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) lo = min_nan(lo, x[e]), hi = max_nan(hi, x[e]);
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    }
 }
 __device__ __forceinline__ void range_of(const Eight<__nv_bfloat16>& v, const float (&)[8], float& lo, float& hi) {
     const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v.r);
     const __nv_bfloat162 a = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
     const __nv_bfloat162 b = __hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3]));
-    lo = min_nan(__low2float(a), __high2float(a)), hi = max_nan(__low2float(b), __high2float(b));
+    const uint32_t ab = *reinterpret_cast<const uint32_t*>(&a), bb = *reinterpret_cast<const uint32_t*>(&b) ^ 0x80008000u;
+    uint32_t p = __byte_perm(ab, bb, 0x5410), q = __byte_perm(ab, bb, 0x7632);
+    __nv_bfloat162 m = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&p), *reinterpret_cast<const __nv_bfloat162*>(&q));
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) m = __hmin2_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+    lo = __low2float(m), hi = -__high2float(m);
 }
 
-constexpr int kAppendVecs = 2;
 constexpr float kMagic = 12582912.f;     // 1.5 * 2^23: adding it rounds to integers, which its low bits then hold
 
-// A thread takes eight channels, eight lanes a group.  A thread block takes whole tokens (k
-// and v, all heads): block_tokens of them; `row_magic` divides by a token's pieces of one
-// tensor, as ceil(2^40 / row_vecs).
+// Codes and (s, m) of a group, of which this lane has eight channels: `v` is what they are in
+// memory.
 //
 // The definition's quotient is the correctly rounded one.  A product with 1 / s is within 2^-18
-// of it, and rounds to the same integer unless it lies that near the middle of two: those lanes
-// divide.
+// of it, and rounds to the same integer unless it lies that near the middle of two.  Those lanes
+// look at what is left of x: it lies in the middle (common in bf16: the even code is taken), or
+// clearly to one side, or they divide.
+template <typename T> __device__ __forceinline__ uint32_t encode(const Eight<T>& v, uint32_t& scale) {
+    float x[8], lo, hi;
+    v.open(x);
+    range_of(v, x, lo, hi);
+    float low = sizeof(T) == 2 ? lo : bf16_down(lo), step = bf16_up(__fdiv_rn(__fsub_rn(hi, low), 15.f)), by;
+    const bool fine = fabsf(low) <= FLT_MAX && __fsub_rn(hi, low) <= FLT_MAX && step <= FLT_MAX;      // (no, with a NaN)
+    if (!fine) low = CUDART_NAN_F, step = 0.f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(step));
+    float c[8], most = 0.f;                                  // codes; how far from its integer a quotient is
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = __fsub_rn(x[e], low);
+        c[e] = fmaf(x[e], by, kMagic) - kMagic;
+        most = fmaxf(most, fabsf(fmaf(x[e], by, -c[e])));
+    }
+    // (a tiny step's inverse is not a number to go by; nor is there a middle to be near without one)
+    if (!(most <= 0.5f - 0x1p-16f) || !(step >= 0x1p-100f)) {
+        bool divide = !(step >= 0x1p-100f);
+        const float half = 0.5f * step, near = step * 0x1p-18f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float rest = fmaf(-c[e], step, x[e]), past = fabsf(rest) - half;           // both exact
+            divide |= past != 0.f && fabsf(past) < near;
+            const bool odd = __float_as_uint(c[e] + kMagic) & 1u;
+            if (odd ? past >= 0.f : past > 0.f) c[e] += copysignf(1.f, rest);
+        }
+        if (divide) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = step > 0.f ? fminf(rintf(__fdiv_rn(x[e], step)), 15.f) : 0.f;
+        }
+    }
+    scale = __float_as_uint(step) >> 16 | (__float_as_uint(low) & 0xFFFF0000u);
+    // four codes fit a float's integers
+    const float c03 = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]) + kMagic, c47 = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]) + kMagic;
+    return __byte_perm(__float_as_uint(c03), __float_as_uint(c47), 0x5410);
+}
+
+// A thread takes eight channels of a key and the same of its value, eight lanes a group.  A
+// thread block takes whole tokens, all heads: block_tokens of them; `row_magic` divides by a
+// token's pieces of one tensor, as ceil(2^20 / row_vecs) where a block has several tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ CacheAppendQ4Launch p, int32_t block_tokens, uint64_t row_magic) {
+__global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ CacheAppendQ4Launch p, uint32_t block_tokens, uint32_t row_magic) {
     constexpr uint32_t kHeadVecs = D / 8;
     griddep_wait();
     const kda_cache_append_q4_args& a = p.a;
     const uint32_t row_vecs = kHeadVecs * (uint32_t)a.n_kv_heads;
     const int shift = __ffs(a.cache.block_size) - 1;
     const int64_t t0 = (int64_t)blockIdx.x * block_tokens, n_slots = a.cache.n_blocks << shift;
-    const uint32_t n = 2 * row_vecs * (uint32_t)min((int64_t)block_tokens, a.n_tokens - t0);
-    for (uint32_t base = 0; base < n; base += kThreads * kAppendVecs) {
-        Eight<T> in[kAppendVecs];
-        int32_t slot[kAppendVecs];
-        uint32_t half[kAppendVecs], y[kAppendVecs];      // 2 * token, or that + 1 for v; piece of the token's row
-#pragma unroll
-        for (int m = 0; m < kAppendVecs; ++m) {
-            const uint32_t i = base + m * kThreads + threadIdx.x;
-            in[m] = Eight<T>{};
-            slot[m] = -1;
-            half[m] = (uint32_t)(i * row_magic >> 40), y[m] = i - half[m] * row_vecs;
-            if (i >= n) continue;
-            const int64_t t = t0 + (half[m] >> 1);
-            slot[m] = a.slot_map[t];
-            in[m] = *reinterpret_cast<const Eight<T>*>(static_cast<const T*>(half[m] & 1 ? a.v : a.k) + t * (half[m] & 1 ? a.v_stride : a.k_stride) + y[m] * 8);
+    const uint32_t n = row_vecs * (uint32_t)min((int64_t)block_tokens, a.n_tokens - t0);
+    for (uint32_t base = 0; base < n; base += kThreads) {
+        const uint32_t i = base + threadIdx.x, token = block_tokens == 1 ? 0 : i * row_magic >> 20, y = i - token * row_vecs;
+        const int64_t t = t0 + token;
+        Eight<T> k{}, v{};
+        int32_t slot = -1;
+        if (i < n) {
+            slot = a.slot_map[t];
+            k = *reinterpret_cast<const Eight<T>*>(static_cast<const T*>(a.k) + t * a.k_stride + y * 8);
+            v = *reinterpret_cast<const Eight<T>*>(static_cast<const T*>(a.v) + t * a.v_stride + y * 8);
         }
-#pragma unroll
-        for (int m = 0; m < kAppendVecs; ++m) {
-            float x[8], lo, hi;
-            in[m].open(x);
-            range_of(in[m], x, lo, hi);
-#pragma unroll
-            for (int off = 1; off < 8; off <<= 1) {
-                lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-                hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-            }
-            float low = bf16_down(lo), step = bf16_up(__fdiv_rn(__fsub_rn(hi, low), 15.f));
-            const bool fine = fabsf(low) <= FLT_MAX && __fsub_rn(hi, low) <= FLT_MAX && step <= FLT_MAX;      // (no, with a NaN)
-            if (!fine) low = CUDART_NAN_F, step = 0.f;
-            float c[8], most = 0.f;                      // codes; how far from its integer a quotient is
-            float by;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(step));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float t = __fsub_rn(x[e], low);
-                c[e] = fmaf(t, by, kMagic) - kMagic;
-                most = fmaxf(most, fabsf(fmaf(t, by, -c[e])));
-            }
-            // (a tiny step's inverse is not a number to go by; nor is there a middle to be near without one)
-            if (!(most <= 0.5f - 0x1p-16f) || !(step >= 0x1p-100f)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) c[e] = step > 0.f ? fminf(rintf(__fdiv_rn(__fsub_rn(x[e], low), step)), 15.f) : 0.f;
-            }
-            // four codes fit a float's integers
-            const float c03 = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]) + kMagic, c47 = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]) + kMagic;
-            const uint32_t codes = __byte_perm(__float_as_uint(c03), __float_as_uint(c47), 0x5410);
-            if (slot[m] < 0 || slot[m] >= n_slots) {
-                if (slot[m] != -1) flag(p.status, KDA_DEV_BAD_SLOT);
-                continue;
-            }
-            const bool is_v = half[m] & 1;
-            const uint32_t h = y[m] / kHeadVecs, e = y[m] % kHeadVecs;
-            const int64_t row = (((int64_t)(slot[m] >> shift) * a.n_kv_heads + h) << shift) + (slot[m] & (a.cache.block_size - 1));
-            static_cast<uint32_t*>(is_v ? a.cache.v_codes : a.cache.k_codes)[row * kHeadVecs + e] = codes;
-            const uint32_t scale = __float_as_uint(step) >> 16 | (__float_as_uint(low) & 0xFFFF0000u);
-            if (e % 8 == 0) static_cast<uint32_t*>(is_v ? a.cache.v_scales : a.cache.k_scales)[row * (kHeadVecs / 8) + e / 8] = scale;
-            void* out = is_v ? a.v_out : a.k_out;
-            if (out) {
-                values_of(codes, scale, in[m]);
-                *reinterpret_cast<Eight<T>*>(static_cast<T*>(out) + (t0 + (half[m] >> 1)) * (is_v ? a.v_out_stride : a.k_out_stride) + y[m] * 8) = in[m];
-            }
+        uint32_t k_scale, v_scale;
+        const uint32_t k_codes = encode(k, k_scale), v_codes = encode(v, v_scale);
+        if (slot < 0 || slot >= n_slots) {
+            if (slot != -1) flag(p.status, KDA_DEV_BAD_SLOT);
+            continue;
+        }
+        const uint32_t h = y / kHeadVecs, e = y % kHeadVecs;
+        // (rows are below 2^31)
+        const uint64_t row = (uint32_t)(((slot >> shift) * a.n_kv_heads + h) << shift) + (slot & (a.cache.block_size - 1));
+        static_cast<uint32_t*>(a.cache.k_codes)[row * kHeadVecs + e] = k_codes;
+        static_cast<uint32_t*>(a.cache.v_codes)[row * kHeadVecs + e] = v_codes;
+        if (e % 8 == 0) {
+            static_cast<uint32_t*>(a.cache.k_scales)[row * (kHeadVecs / 8) + e / 8] = k_scale;
+            static_cast<uint32_t*>(a.cache.v_scales)[row * (kHeadVecs / 8) + e / 8] = v_scale;
+        }
+        if (a.k_out) {
+            values_of(k_codes, k_scale, k);
+            *reinterpret_cast<Eight<T>*>(static_cast<T*>(a.k_out) + t * a.k_out_stride + y * 8) = k;
+        }
+        if (a.v_out) {
+            values_of(v_codes, v_scale, v);
+            *reinterpret_cast<Eight<T>*>(static_cast<T*>(a.v_out) + t * a.v_out_stride + y * 8) = v;
         }
     }
 }
@@ -178,6 +200,27 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
 // ------------------------------------------------------------------ read-back
 
 constexpr int kWarps = kThreads / 32, kRows = 16;           // an item: 16 positions of one head
+
+// A lane's sixteen channels in stores of whole 32-byte sectors (two of 16 bytes each: 240 us for
+// 24 sequences of up to 16384 tokens, 8 heads, d = 128; so: 200 us).
+__device__ __forceinline__ void store32(void* to, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                 "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ void write_sixteen(__nv_bfloat16* to, uint2 codes, uint32_t scale) {
+    Eight<__nv_bfloat16> x, y;
+    values_of(codes.x, scale, x);
+    values_of(codes.y, scale, y);
+    store32(to, x.r, y.r);
+}
+__device__ __forceinline__ void write_sixteen(float* to, uint2 codes, uint32_t scale) {
+    Eight<float> x;
+    values_of(codes.x, scale, x);
+    store32(to, reinterpret_cast<const uint4*>(x.r)[0], reinterpret_cast<const uint4*>(x.r)[1]);
+    values_of(codes.y, scale, x);
+    store32(to + 8, reinterpret_cast<const uint4*>(x.r)[0], reinterpret_cast<const uint4*>(x.r)[1]);
+}
 
 // Items in the order of sequences, positions, heads, dealt to the warps in turn, so that all
 // warps work side by side whatever the lengths are.  Every thread block runs the (short)
@@ -248,9 +291,7 @@ __global__ void __launch_bounds__(kThreads) unpack_q4_kernel(const __grid_consta
                 for (int k = 0; k < kSteps; ++k) {
                     const int32_t pos = pos0 + own_row + k * kAtOnce;
                     if (pos < r.x || pos >= r.y) continue;
-                    Eight<T>* out = reinterpret_cast<Eight<T>*>(static_cast<T*>(v ? a.v_cache : a.k_cache) + (dst + k * kAtOnce) * D + own * 16);
-                    values_of(codes[v][k].x, scale[v][k], out[0]);
-                    values_of(codes[v][k].y, scale[v][k], out[1]);
+                    write_sixteen(static_cast<T*>(v ? a.v_cache : a.k_cache) + (dst + k * kAtOnce) * D + own * 16, codes[v][k], scale[v][k]);
                 }
         }
         base += total;
@@ -269,10 +310,10 @@ cudaError_t launch_unpack_t(const CacheUnpackQ4Launch& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append_q4(const CacheAppendQ4Launch& p, cudaStream_t s) {
-    const int32_t fit = kThreads * kAppendVecs / (2 * p.a.n_kv_heads * (p.a.d / 8));
-    const int32_t block_tokens = fit > 1 && p.a.n_tokens > 2 * 152 * (int64_t)fit ? fit : 1;
+    const uint32_t row_vecs = (uint32_t)p.a.n_kv_heads * (p.a.d / 8), fit = kThreads / row_vecs;
+    // few tokens are spread over the SMs, one to a block
+    const uint32_t block_tokens = fit > 1 && p.a.n_tokens > 2 * 152 * (int64_t)fit ? fit : 1, magic = ((1u << 20) + row_vecs - 1) / row_vecs;
     const dim3 grid((unsigned)((p.a.n_tokens + block_tokens - 1) / block_tokens));
-    const uint64_t row_vecs = (uint64_t)p.a.n_kv_heads * (p.a.d / 8), magic = ((1ull << 40) + row_vecs - 1) / row_vecs;
     const bool wide = p.a.d == 128;
     note_launch();
     if (p.a.dtype == KDA_BF16)

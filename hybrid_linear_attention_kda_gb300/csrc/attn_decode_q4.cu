@@ -143,23 +143,25 @@ __device__ __forceinline__ float third(float x, int i) {
     return i == 0 ? a : i == 1 ? b : i == 2 ? __bfloat162float(__float2bfloat16_rn(x - a - b)) : 0.f;
 }
 
-// Sixteen channels of q.
-__device__ __forceinline__ void load16(const float* q, float (&x)[16]) {
+// Sixteen channels of q as they lie in memory.
+template <typename T> struct Raw16 {
+    uint4 r[sizeof(T)];
+    __device__ __forceinline__ void load(const T* q) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(q)[i];
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        for (int i = 0; i < (int)sizeof(T); ++i) r[i] = reinterpret_cast<const uint4*>(q)[i];
     }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* q, float (&x)[16]) {
+    __device__ __forceinline__ void open(float (&x)[16]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(q)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < (int)sizeof(T); ++i) {
+            const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[8 * i + 2 * k] = low_of(w[k]), x[8 * i + 2 * k + 1] = high_of(w[k]);
+            for (int k = 0; k < 4; ++k) {
+                if (sizeof(T) == 4) x[4 * i + k] = __uint_as_float(w[k]);
+                else x[(8 * i + 2 * k) & 15] = low_of(w[k]), x[(8 * i + 2 * k + 1) & 15] = high_of(w[k]);
+            }
+        }
     }
-}
+};
 
 __device__ __forceinline__ void write2(float* to, float x, float y) { *reinterpret_cast<float2*>(to) = make_float2(x, y); }
 __device__ __forceinline__ void write2(__nv_bfloat16* to, float x, float y) { *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(x, y); }
@@ -255,13 +257,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     int f_run, f_key, f_end;
     uint32_t f_head_row;
     const int32_t* f_row;
-    auto enter = [&](const Place& f) {
-        f_run = f.run(), f_key = f.info.x + f.k * kKeys + half * kHalf, f_end = f.info.y;
-        f_head_row = (uint32_t)(f.u / blocks * a.block_size);
-        f_row = a.block_table + (int64_t)f.s * a.table_stride;
-    };
-    enter(ahead[warp]);
-    int32_t next_block = 0;                              // this half's table entry at f_key
+    // Table entries of this half's tiles, a lane each: sixteen from the present batch's first on, and
+    // the sixteen behind them.
+    int32_t entries = -1, entries_on = -1;
+    int f_tile = 0;                                      // of the batch
     // places in shared memory: piece y = 16 i + l16 of a half's codes, and one piece of its scales
     constexpr int kPieces = S::kScales / 2 / 16, kPieceKeys = 4 / NG;
     const int scale_piece = l16 % kPieces, scale_is_v = l16 / kPieces;
@@ -271,11 +270,22 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     const uint8_t* k_from = static_cast<const uint8_t*>(cache.k_codes) + l16 * 16;
     const uint8_t* v_from = static_cast<const uint8_t*>(cache.v_codes) + l16 * 16;
     const uint8_t* scale_from = static_cast<const uint8_t*>(scale_is_v ? cache.v_scales : cache.k_scales) + scale_piece * 16;
-    auto look_up = [&]() { if (f_key < f_end) next_block = f_row[f_key >> page_shift]; };
+    auto look_up = [&](int ahead_by) {
+        const uint32_t key = (uint32_t)f_key + (uint32_t)((ahead_by + l16) * kKeys);
+        return key < (uint32_t)f_end ? f_row[key >> page_shift] : -1;
+    };
+    auto enter = [&](const Place& f) {
+        f_run = f.run(), f_key = f.info.x + f.k * kKeys + half * kHalf, f_end = f.info.y;
+        f_head_row = (uint32_t)(f.u / blocks * a.block_size);
+        f_row = a.block_table + (int64_t)f.s * a.table_stride;
+        f_tile = 0, entries = look_up(0), entries_on = look_up(16);
+    };
+    enter(ahead[warp]);
     auto fetch = [&](int stage) {
         if (f_run > 0) {
             const uint32_t to = (uint32_t)(stage * S::kTile);
             const int live = f_end - f_key;                                  // keys from here on
+            const int32_t next_block = __shfl_sync(0xffffffffu, entries, (lane & 16) | f_tile);
             const bool known = (uint32_t)next_block < n_blocks;
             // (rows are below 2^31; a half lies in one page, so that those of missing keys may be named too)
             const uint32_t row = (uint32_t)next_block * page_rows + (f_head_row + (f_key & page_mask));
@@ -302,14 +312,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 ahead[warp] = f;
                 __syncwarp();
                 if (f.left > 0) enter(f);
+            } else if (++f_tile == 16) {
+                f_tile = 0, entries = entries_on, entries_on = look_up(16);
             }
-            if (f_run > 0) look_up();
         }
         copy_commit();
     };
-    look_up();
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
     // ------------------------------------------------------------------ units
     // Lane (n, t) of a product's operands: rows n and n + 8, columns 2 t and one more.
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     const uint32_t s0 = ring + 2 * S::kCodes + own_key * NG * 4;
     auto k_at = [](uint32_t k, int r, int g) { return NG == 2 ? (k ^ (g * 32 + r * 16)) + r * 128 : k ^ r * 64; };
     int stage = 0;
-    bool more = true;
+    bool more = true, begun = false;
     while (more) {
         int kt, live;                                    // tiles of the unit in this piece, keys from the first one on
         const Place c = here[warp];
@@ -333,6 +341,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 
         // q of column n, 16 channels of each group from 64 g + 16 t, as the operands that meet
         // a word's codes: (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16.
+        Raw16<T> raw[NT][NG];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = min(nt * kColumns + n % kColumns, min(kRows, G - c.u % blocks * kRows) - 1);
+            const T* qs = static_cast<const T*>(a.q) + c.s * a.q_stride + (int64_t)(c.u / blocks * G + c.u % blocks * kRows + r) * D + 16 * t;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) raw[nt][g].load(qs + g * kQ4Group);
+        }
+        if (!begun) {                                    // the first copies, while q is on its way
+            begun = true;
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) fetch(i);
+        }
         uint32_t q[NT][NG][2][4];
         uint32_t qsum[NT];                               // of column n, part t of three, both groups, times scale log2 e
         float unscale[NT][2];                            // of heads 2 t and 2 t + 1, times that too
@@ -340,11 +361,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * kColumns + n % kColumns;
             const bool is_row = r < min(kRows, G - c.u % blocks * kRows);
-            const T* qs = static_cast<const T*>(a.q) + c.s * a.q_stride + (int64_t)(c.u / blocks * G + c.u % blocks * kRows + (is_row ? r : 0)) * D + 16 * t;
             float x[NG][16], most = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                load16(qs + g * kQ4Group, x[g]);
+                raw[nt][g].open(x[g]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     x[g][e] = is_row ? x[g][e] : 0.f;

@@ -49,7 +49,6 @@ __device__ __forceinline__ void turn(int32_t position, uint64_t turns, float& c,
     if (quarter >= 2) s = -s;
 }
 
-constexpr int kAtOnce = 4;        // loads of a lane's rows under way
 
 // What a lane makes of its pairs in all rows of one kind: with the weights w and its token's
 // angles, (x0, x1) -> ((w0 c) x0 - (w1 s) x1, (w0 s) x0 + (w1 c) x1), times the row's norm.
@@ -61,17 +60,20 @@ template <bool kHalves> __device__ __forceinline__ constexpr int first_of(int i)
 template <bool kHalves> __device__ __forceinline__ constexpr int second_of(int i) { return kHalves ? 4 + i : 2 * i + 1; }
 
 // Rows lo .. hi - 1 of one kind; from and to are the lane's places in row 0, kRows rows a warp.
+// Rows of a lane under way: 64 bytes.
+template <typename T> constexpr int kAtOnce = 8 / (int)sizeof(T);
+
 template <typename T, int D, bool kHalves>
 __device__ __forceinline__ void turn_rows(const T* from, T* to, int64_t from_row, int64_t to_row, int lo, int hi, int c0, int c1, bool turned,
                                           const Turn& t, bool norm, float eps) {
     using P = Piece<T>;
     using Raw = typename P::Raw;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-    for (int b = lo; b < hi; b += kRows * kAtOnce) {     // (the same for all lanes)
+    for (int b = lo; b < hi; b += kRows * kAtOnce<T>) {     // (the same for all lanes)
         const int r0 = b + (threadIdx.x & 31) / kLanes;
-        Raw raw[kAtOnce][2];
+        Raw raw[kAtOnce<T>][2];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
+        for (int u = 0; u < kAtOnce<T>; ++u) {
             raw[u][0] = raw[u][1] = Raw{};
             if (r0 + u * kRows < hi) {
                 const T* x = from + (r0 + u * kRows) * from_row;
@@ -80,7 +82,7 @@ __device__ __forceinline__ void turn_rows(const T* from, T* to, int64_t from_row
             }
         }
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
+        for (int u = 0; u < kAtOnce<T>; ++u) {
             float x[8], y[8], inv = 1.f;
             P::open(raw[u][0], x);
             P::open(raw[u][1], x + 4);
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 template <typename T, int D, bool kAppend>
 cudaError_t launch_t(const RopeLaunch& p, cudaStream_t s) {
-    constexpr int kBatch = kAtOnce * (32 / (D / 8));
+    constexpr int kBatch = kAtOnce<T> * (32 / (D / 8));
     const int n_rows = p.a.n_heads + (kAppend ? 2 : 1) * p.a.n_kv_heads, batches = (n_rows + kBatch - 1) / kBatch;
     // a token's rows are spread over warps until the GPU has 32 of them an SM
     int64_t parts = (152 * 32 + p.a.n_tokens - 1) / p.a.n_tokens;

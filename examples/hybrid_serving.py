@@ -24,13 +24,15 @@ UNIT = 256          # a KDA prefill resumes at a multiple of this many tokens
 
 
 class HybridStack:
-    """``pattern`` gives each layer's kind: "k" is KDA, "a" softmax attention.  Random weights;
-    the projections are plain matrix products, and there are no feed-forward layers."""
+    """``pattern`` gives each layer's kind: "k" is KDA, "a" softmax attention, with norms of its
+    queries and keys and a position rotation if ``rope``.  Random weights; the projections are
+    plain matrix products, and there are no feed-forward layers."""
 
-    def __init__(self, pattern="kkka", heads=8, kv_heads=2, d=128, dtype=torch.bfloat16, device="cuda", seed=0):
+    def __init__(self, pattern="kkka", heads=8, kv_heads=2, d=128, dtype=torch.bfloat16, device="cuda", seed=0, rope=False):
         gen = torch.Generator(device).manual_seed(seed)
         self.pattern, self.H, self.H_kv, self.d, self.dtype, self.device = pattern, heads, kv_heads, d, dtype, device
         self.width = heads * d
+        self.turns = kda.rope_turns([10000.0 ** (-2 * i / d) for i in range(d // 2)], device) if rope else None
 
         def weight(rows, cols):
             return (torch.randn(rows, cols, generator=gen, device=device) * rows ** -0.5).to(dtype)
@@ -43,7 +45,16 @@ class HybridStack:
                     weight(self.width, heads)
             else:
                 w["qkv"] = weight(self.width, (heads + 2 * kv_heads) * d)
+                if rope:
+                    w["q_weight"], w["k_weight"] = (1 + 0.1 * torch.randn(d, generator=gen, device=device) for _ in range(2))
             self.layers.append(w)
+
+    def turned(self, i, q, k, positions):
+        """Layer i's queries and keys, normed and rotated in place."""
+        if self.turns is not None:
+            kda.qk_norm_rope(q, k, positions, self.turns, q_weight=self.layers[i]["q_weight"],
+                             k_weight=self.layers[i]["k_weight"], q_out=q, k_out=k)
+        return q, k
 
     def forward(self, x, kda_layer, attn_layer):
         """x [T, width] through the stack.  kda_layer(i, q, k, v, alpha, beta) and attn_layer(i,
@@ -68,14 +79,20 @@ class HybridStack:
 class Server:
     """The requests' caches and states: per attention layer one pair of paged caches, per KDA
     layer one state pool (slot s for request s, the last slot for the shared prompt), and one
-    block table and free list for all layers."""
+    block table and free list for all layers.
 
-    def __init__(self, net, n, capacity, block_size=64):
-        self.net, self.n, self.block_size = net, n, block_size
+    With ``four_bit`` the pair of caches holds the shared prompt, in its first ``shared_blocks``
+    blocks, and behind them, while prompts run, the values of the 4-bit cache's blocks."""
+
+    def __init__(self, net, n, capacity, block_size=64, four_bit=False, prefix=0):
+        self.net, self.n, self.block_size, self.four_bit = net, n, block_size, four_bit
         stride = -(-capacity // block_size)
         self.n_blocks = (n + 1) * stride
+        self.shared_blocks = prefix // block_size if four_bit else 0
         dev = net.device
-        shape = (self.n_blocks, net.H_kv, block_size, net.d)
+        self.q4 = {i: kda.q4_cache(self.n_blocks, net.H_kv, block_size, net.d, dev)
+                   for i, kind in enumerate(net.pattern) if kind == "a" and four_bit}
+        shape = (self.shared_blocks + self.n_blocks, net.H_kv, block_size, net.d)
         self.caches = {i: (torch.empty(shape, dtype=net.dtype, device=dev), torch.empty(shape, dtype=net.dtype, device=dev))
                        for i, kind in enumerate(net.pattern) if kind == "a"}
         self.pools = {i: torch.zeros(n + 1, net.H, net.d, net.d, device=dev)
@@ -101,13 +118,19 @@ class Server:
         """The shared prompt, x [a multiple of UNIT, width]."""
         T = x.shape[0]
         table, zero = self.table[:1].clone(), torch.zeros(1, dtype=torch.int32, device=x.device)
-        plan = self.plan(table, zero, zero + T, T)
+        if self.four_bit:                                  # the prompt has blocks of its own
+            blocks = torch.arange(self.shared_blocks, dtype=torch.int32, device=x.device)
+            plan = kda.cache_plan(zero, zero + T, table, blocks, zero.clone(), zero.clone(), block_size=self.block_size,
+                                  n_blocks=self.shared_blocks, max_tokens=T)
+        else:
+            plan = self.plan(table, zero, zero + T, T)
 
         def kda_layer(i, q, k, v, alpha, beta):
             o, self.pools[i][self.n:] = kda.prefill(q, k, v, alpha, beta, plan.cu_seqlens, T)
             return o
 
         def attn_layer(i, q, k, v):
+            q, k = self.net.turned(i, q, k, plan.positions)
             kda.kda_cache_append(k, v, plan.slot_map, *self.caches[i])
             return kda.attn_prefill(q, k, v, plan.cu_seqlens)[0]
 
@@ -130,13 +153,35 @@ class Server:
                                                     init_slot=shared, pool=self.pools[i])
             return o
 
+        table, slots = self.table, plan.slot_map
+        if self.four_bit:                                  # the wide caches' own numbers, behind the prompt's blocks
+            own = torch.arange(table.shape[1], device=x.device) >= self.shared_blocks
+            table = torch.where(own & (table >= 0), table + self.shared_blocks, table)
+            slots = torch.where(slots >= 0, slots + self.shared_blocks * self.block_size, slots)
+
         def attn_layer(i, q, k, v):
-            kda.kda_cache_append(k, v, plan.slot_map, *self.caches[i])
-            return kda.attn_prefill_paged(q, *self.caches[i], self.table, plan.kv_lens, plan.cu_seqlens)[0]
+            q, k = self.net.turned(i, q, k, plan.positions)
+            if self.four_bit:
+                k, v = kda.cache_append_q4(k, v, plan.slot_map, self.q4[i], k_out=k, v_out=v)
+            kda.kda_cache_append(k, v, slots, *self.caches[i])
+            return kda.attn_prefill_paged(q, *self.caches[i], table, plan.kv_lens, plan.cu_seqlens)[0]
 
         y = self.net.forward(x, kda_layer, attn_layer)
         self.lens.copy_(plan.kv_lens)
         return y
+
+    def more_prompts(self, x, new_lens):
+        """Further turns: more tokens for the requests, behind what they hold.  With ``four_bit``, what
+        their attention has to see of that is read back into the wide caches first."""
+        if "k" in self.net.pattern:
+            raise ValueError(f"a KDA layer resumes at multiples of {UNIT} tokens only")
+        if self.four_bit:
+            own = torch.arange(self.table.shape[1], device=x.device) >= self.shared_blocks
+            wide = torch.where(own & (self.table >= 0), self.table + self.shared_blocks, self.table)
+            first = torch.full_like(self.lens, self.prefix)
+            for i, cache in self.q4.items():
+                kda.cache_unpack_q4(cache, self.table, self.lens, *self.caches[i], wide, first=first)
+        return self.prompts(x, new_lens)
 
     def step(self, x):
         """One new token per request, x [n, width].  Only device work of fixed sizes, so that it
@@ -149,9 +194,19 @@ class Server:
             return o
 
         def attn_layer(i, q, k, v):
-            kda.kda_cache_append(k, v, plan.slot_map, *self.caches[i])
-            return kda.attn_decode(q, *self.caches[i], self.table, plan.kv_lens, group_start=self.group_start,
-                                   prefix_lens=self.prefix_lens)[0]
+            shared = dict(group_start=self.group_start, prefix_lens=self.prefix_lens)
+            if self.four_bit:
+                q, k = self.net.turned(i, q, k, plan.positions)
+                kda.cache_append_q4(k, v, plan.slot_map, self.q4[i])
+                k_prefix, v_prefix = (c[:self.shared_blocks] for c in self.caches[i])
+                return kda.attn_decode_q4(q, self.q4[i], self.table, plan.kv_lens, k_prefix=k_prefix, v_prefix=v_prefix, **shared)[0]
+            if self.net.turns is not None:
+                w = self.net.layers[i]
+                q = kda.cache_append_rope(k, v, plan.positions, self.net.turns, plan.slot_map, *self.caches[i], q=q,
+                                          q_weight=w["q_weight"], k_weight=w["k_weight"])
+            else:
+                kda.kda_cache_append(k, v, plan.slot_map, *self.caches[i])
+            return kda.attn_decode(q, *self.caches[i], self.table, plan.kv_lens, **shared)[0]
 
         y = self.net.forward(x, kda_layer, attn_layer)
         self.lens.copy_(plan.kv_lens)
@@ -176,13 +231,26 @@ class Server:
         return [self.lens, self.free_begin, self.free_end, self.table, *self.pools.values()]
 
 
-def recompute(net, x, cu_seqlens):
-    """The stack over whole packed sequences, from their first tokens."""
-    return net.forward(x, lambda i, q, k, v, a, b: kda.prefill(q, k, v, a, b, cu_seqlens, x.shape[0], want_final=False)[0],
-                       lambda i, q, k, v: kda.attn_prefill(q, k, v, cu_seqlens)[0])
+def recompute(net, x, cu_seqlens, prefix=0, four_bit=False):
+    """The stack over whole packed sequences, from their first tokens; with ``four_bit``, tokens
+    behind the first ``prefix`` of each have the keys and values that a 4-bit cache stands for."""
+    T = x.shape[0]
+    at = torch.arange(T, dtype=torch.int32, device=x.device)
+    positions = at - cu_seqlens[torch.searchsorted(cu_seqlens, at, right=True) - 1]
+    if four_bit:
+        cache = kda.q4_cache(-(-T // 256), net.H_kv, 256, net.d, x.device)
+        slots = torch.where(positions >= prefix, at, -1)
+
+    def attn_layer(i, q, k, v):
+        q, k = net.turned(i, q, k, positions)
+        if four_bit:
+            kda.cache_append_q4(k, v, slots, cache, k_out=k, v_out=v)
+        return kda.attn_prefill(q, k, v, cu_seqlens)[0]
+
+    return net.forward(x, lambda i, q, k, v, a, b: kda.prefill(q, k, v, a, b, cu_seqlens, T, want_final=False)[0], attn_layer)
 
 
-def serve(net, n=8, prefix=2 * UNIT, longest=300, steps=16, block_size=64, seed=1):
+def serve(net, n=8, prefix=2 * UNIT, longest=300, steps=16, block_size=64, seed=1, four_bit=False):
     """Serve ``n`` requests.  The input of a decode step is the last output, normalised, as a
     stand-in for sampling and embedding.  Returns (all inputs, all outputs, cu_seqlens) of the
     requests' full sequences, packed, and the milliseconds of one decode step."""
@@ -190,7 +258,7 @@ def serve(net, n=8, prefix=2 * UNIT, longest=300, steps=16, block_size=64, seed=
     lens = torch.randint(1, longest + 1, (n,), generator=gen, device=net.device, dtype=torch.int32)
     own = torch.randn(int(lens.sum()), net.width, generator=gen, device=net.device).to(net.dtype)
     system = torch.randn(prefix, net.width, generator=gen, device=net.device).to(net.dtype)
-    server = Server(net, n, prefix + longest + steps, block_size)
+    server = Server(net, n, prefix + longest + steps, block_size, four_bit, prefix)
     shared = server.start(system)
     hidden = server.prompts(own, lens)
     ends = lens.cumsum(0)
@@ -229,16 +297,19 @@ def main():
     ap.add_argument("--prefix", type=int, default=2 * UNIT, help=f"tokens of the system prompt, a multiple of {UNIT}")
     ap.add_argument("--longest", type=int, default=300, help="longest prompt of a request")
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--rope", action="store_true", help="norms of queries and keys, and a position rotation")
+    ap.add_argument("--cache", choices=("full", "4bit"), default="full", help="the requests' own tokens in the attention layers")
     ap.add_argument("--check", action="store_true")
     a = ap.parse_args()
     dtype = torch.bfloat16 if a.dtype == "bf16" else torch.float32
     with torch.no_grad():
-        net = HybridStack(a.pattern, a.heads, a.kv_heads, dtype=dtype)
-        x, y, cu, ms = serve(net, a.requests, a.prefix, a.longest, a.steps)
+        net = HybridStack(a.pattern, a.heads, a.kv_heads, dtype=dtype, rope=a.rope)
+        four_bit = a.cache == "4bit"
+        x, y, cu, ms = serve(net, a.requests, a.prefix, a.longest, a.steps, four_bit=four_bit)
         print(f"{a.requests} requests behind {a.prefix} shared tokens, layers {a.pattern}: {ms:.3f} ms a decode step, "
               f"{a.requests / ms * 1e3:.0f} tokens/s")
         if a.check:
-            want = recompute(net, x, cu)
+            want = recompute(net, x, cu, a.prefix, four_bit)
             err = (y.double() - want.double()).norm() / want.double().norm()
             print(f"relative distance to the recomputed hidden states: {err:.2e}")
 

@@ -15,7 +15,8 @@
 // K: a code in an fp16 number's lowest bits is that number: the subnormals are n 2^-24, exact
 // operands like any other.  A word's eight codes take four masks and a shift: at bits 4..7
 // a code counts 16-fold, which q's side makes up for.  q is scaled by a power of two for the
-// range of fp16.  V: the products add up over keys, so that a byte of codes has to meet the
+// range of fp16.  (fp32 takes centred codes here too, and q's sum times m + 8 s: what the tensor
+// cores cut off of larger sums would be more than fp32 loses.)  V: the products add up over keys, so that a byte of codes has to meet the
 // same byte of the next key: ldmatrix transposes bytes, a permutation puts 0x64 behind each,
 // which makes 1024 + byte of it, and one fp16 instruction n - 8 of each of its codes.  A
 // product's rows are the keys in the order in which that hands them out.  Weights times scales are rounded to fp16: 11 bits, counted from the largest so far
@@ -137,6 +138,18 @@ template <int PICK> __device__ __forceinline__ void centred(uint32_t x, uint32_t
     lower = *reinterpret_cast<const uint32_t*>(&lo), upper = *reinterpret_cast<const uint32_t*>(&hi);
 }
 
+// n - 8 in fp16 for the codes at bits 0..3, and at bits 4..7, of both halves of x.
+__device__ __forceinline__ uint32_t centred_low(uint32_t x) {
+    const uint32_t y = (x & 0x000F000Fu) | 0x64006400u, middle = 0x64086408u;                              // 1024 + n, 1032
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&middle));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t centred_high(uint32_t x) {
+    const uint32_t y = (x & 0x00F000F0u) | 0x64006400u, by = 0x2C002C00u, middle = 0xD480D480u;            // 1024 + 16 n, 1 / 16, -72
+    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&y), *reinterpret_cast<const __half2*>(&by), *reinterpret_cast<const __half2*>(&middle));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // x as the sum of three bf16 numbers: the i-th, nothing where i is 3.
 __device__ __forceinline__ float third(float x, int i) {
     const float a = __bfloat162float(__float2bfloat16_rn(x)), b = __bfloat162float(__float2bfloat16_rn(x - a));
@@ -217,6 +230,7 @@ template <typename T, int D, int NT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_constant__ AttnDecodeQ4Launch launch) {
     using S = Q4Smem<D, WARPS>;
     constexpr bool kTwoParts = sizeof(T) == 4;
+    constexpr float kUpper = kTwoParts ? 1.f : 0.0625f;  // what q's channels take that meet codes which count 16-fold
     constexpr int NG = D / kQ4Group, kStages = S::kStages, kColumns = kTwoParts ? 4 : 8, kRows = NT * kColumns;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const AttnDecodeLaunch& p = launch.base;
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         }
         uint32_t q[NT][NG][2][4];
         uint32_t qsum[NT];                               // of column n, part t of three, both groups, times scale log2 e
-        float unscale[NT][2];                            // of heads 2 t and 2 t + 1, times that too
+        float unscale[NT][2], sums[NT][2][NG];           // of heads 2 t and 2 t + 1, times that too; sums: fp32 only
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * kColumns + n % kColumns;
@@ -395,13 +409,19 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 for (int w = 0; w < 2; ++w) {
                     const float* y = &x[g][8 * w];
                     q[nt][g][w][0] = pack_half(y[0], y[4]);
-                    q[nt][g][w][1] = pack_half(y[1] * 0.0625f, y[5] * 0.0625f);
+                    q[nt][g][w][1] = pack_half(y[1] * kUpper, y[5] * kUpper);
                     q[nt][g][w][2] = pack_half(y[2], y[6]);
-                    q[nt][g][w][3] = pack_half(y[3] * 0.0625f, y[7] * 0.0625f);
+                    q[nt][g][w][3] = pack_half(y[3] * kUpper, y[7] * kUpper);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) unscale[nt][e] = __shfl_sync(0xffffffffu, undo, 4 * (2 * t + e)) * 0x1p24f * sc;
+            for (int e = 0; e < 2; ++e) {
+                unscale[nt][e] = __shfl_sync(0xffffffffu, undo, 4 * (2 * t + e)) * (kTwoParts ? 1.f : 0x1p24f) * sc;
+                if (kTwoParts) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) sums[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * t + e)) * sc;
+                }
+            }
             const float lower = third(sum[0] * sc, t), upper = NG == 2 ? third(sum[NG - 1] * sc, t) : 0.f;
             qsum[nt] = __float_as_uint(lower) >> 16 | (__float_as_uint(upper) & 0xFFFF0000u);
         }
@@ -444,6 +464,20 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t w0 = h ? w[0].y : w[0].x, w1 = h ? w[1].y : w[1].x, v0 = w0 >> 8, v1 = w1 >> 8;
+                        if (kTwoParts) {                 // fp32: centred codes, and each product's sum rounded to the others'
+                            const uint32_t f[2][4] = {{centred_low(w0), centred_low(w1), centred_high(w0), centred_high(w1)},
+                                                      {centred_low(v0), centred_low(v1), centred_high(v0), centred_high(v1)}};
+#pragma unroll
+                            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float part[4];
+                                    mma_f16_first(part, f[z][0], f[z][1], f[z][2], f[z][3], q[nt][g][h][2 * z], q[nt][g][h][2 * z + 1]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) acc[nt][k] = h == 0 && z == 0 ? part[k] : acc[nt][k] + part[k];
+                                }
+                            continue;
+                        }
                         const uint32_t a0 = w0 & 0x000F000Fu, a1 = w1 & 0x000F000Fu, a2 = w0 & 0x00F000F0u, a3 = w1 & 0x00F000F0u;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -462,8 +496,16 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float base[4];                       // sum of m (sum q)
-                    mma_bf16_k8(base, __byte_perm(scale[0][0], scale[0][NG - 1], 0x7632), __byte_perm(scale[1][0], scale[1][NG - 1], 0x7632), qsum[nt]);
+                    float base[4] = {};                  // sum of m (sum q), or of (m + 8 s) (sum q) where the codes are centred
+                    if (kTwoParts) {
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                base[k] = fmaf(fmaf(8.f, low_of(scale[k >> 1][g]), high_of(scale[k >> 1][g])), sums[nt][k & 1][g], base[k]);
+                    } else {
+                        mma_bf16_k8(base, __byte_perm(scale[0][0], scale[0][NG - 1], 0x7632), __byte_perm(scale[1][0], scale[1][NG - 1], 0x7632), qsum[nt]);
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (kTwoParts) y[nt][k] += __shfl_xor_sync(0xffffffffu, y[nt][k], 2);
@@ -586,10 +628,13 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                     }
                 }
             }
+            // The tensor cores cut what they add up off rather than round it, which over many tiles
+            // would cost fp32 its last bits: there a tile's sum is formed alone, and added to o.
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+            for (int g = 0; g < NG; ++g) {
+                float tile_o[NT][4][4];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
+                for (int hf = 0; hf < 2; ++hf) {
                     uint32_t b[NT][2];                   // turned to heads n, rows 2 t, 2 t + 1 (+ 8)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -603,9 +648,22 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                         centred<0>(v[i], f0, f1);
                         centred<1>(v[i], f2, f3);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (!kTwoParts) mma_f16(o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                            else if (hf == 0) mma_f16_first(tile_o[nt][i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                            else mma_f16(tile_o[nt][i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                        }
                     }
                 }
+                if (kTwoParts) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[nt][g * 4 + i][k] += tile_o[nt][i][k];
+                }
+            }
             __syncwarp();                                // all lanes have read the stage
         }
 

@@ -630,11 +630,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
             }
             // The tensor cores cut what they add up off rather than round it, which over many tiles
             // would cost fp32 its last bits: there a tile's sum is formed alone, and added to o.
+            float tile_o[NT][NG * 4][4];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float tile_o[NT][4][4];
+            for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                for (int g = 0; g < NG; ++g) {
                     uint32_t b[NT][2];                   // turned to heads n, rows 2 t, 2 t + 1 (+ 8)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -650,19 +650,18 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if (!kTwoParts) mma_f16(o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
-                            else if (hf == 0) mma_f16_first(tile_o[nt][i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
-                            else mma_f16(tile_o[nt][i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                            else if (hf == 0) mma_f16_first(tile_o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
+                            else mma_f16(tile_o[nt][g * 4 + i], f0, f1, f2, f3, b[nt][0], b[nt][1]);
                         }
                     }
                 }
-                if (kTwoParts) {
+            if (kTwoParts) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < NG * 4; ++i)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) o[nt][g * 4 + i][k] += tile_o[nt][i][k];
-                }
+                        for (int k = 0; k < 4; ++k) o[nt][i][k] += tile_o[nt][i][k];
             }
             __syncwarp();                                // all lanes have read the stage
         }

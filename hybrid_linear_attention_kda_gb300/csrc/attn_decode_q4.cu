@@ -67,15 +67,12 @@ __device__ __forceinline__ void copy_half(uint32_t c0, uint32_t c1, uint32_t sc,
     if (D == 128 || l16 < 8) copy16(sc, from);
 }
 
+// (What cp.async brings is there after its wait, which these loads do not pass.)
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
+    return *reinterpret_cast<const uint32_t*>(__cvta_shared_to_generic(at));
 }
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
-    return v;
+    return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(at));
 }
 // The scale pairs of one key.
 template <int NG> __device__ __forceinline__ void load_scales(uint32_t (&scale)[2], uint32_t at) {
@@ -87,18 +84,18 @@ template <int NG> __device__ __forceinline__ void load_scales(uint32_t (&scale)[
     }
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // The first product of a sum.
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
@@ -674,13 +671,14 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         const int n_pre = whole ? prefix_parts(p, done.info.x) : 0;
         if (n_pre > 0) griddep_wait();                   // the prefix's results
         const int64_t slot = part_slot(piece, done.k == 0);
+        float y[NT][2][NG * 4][2];
+        int head_of[NT][2];                              // -1: nothing of this lane's to write
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float lt = l[nt][e], mt = m[nt][e], y[NG * 4][2];
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, off);
+                for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     float base = low[nt][e][g];
@@ -691,37 +689,55 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                     for (int i = 4 * g; i < 4 * g + 4; ++i)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            y[i][k] = o[nt][i][2 * k + e] * by;
-                            if (kTwoParts) y[i][k] += __shfl_xor_sync(0xffffffffu, y[i][k], 2);
-                            y[i][k] += base;
+                            float& z = y[nt][e][i][k];
+                            z = o[nt][i][2 * k + e] * by;
+                            if (kTwoParts) z += __shfl_xor_sync(0xffffffffu, z, 2);
+                            z += base;
                         }
                 }
-                const int rr = nt * kColumns + (kTwoParts ? (2 * t + e) & 3 : 2 * t + e), head = head0 + rr;
-                if (rr >= rows || (kTwoParts && t >= 2)) continue;
-#pragma unroll 2
-                for (int i = 0; i < n_pre; ++i) {
-                    const int64_t pr = prefix_row(p, i, s, head);
-                    const float2 ml = p.pre_ml[pr];
+                const int rr = nt * kColumns + ((2 * t + e) & (kColumns - 1));
+                head_of[nt][e] = rr < rows && (!kTwoParts || t < 2) ? head0 + rr : -1;
+            }
+        for (int i = 0; i < n_pre; ++i)                  // all heads' loads of a part together
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 ml[2], v[2][NG * 4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int64_t pr = prefix_row(p, i, s, max(head_of[nt][e], 0));
+                    ml[e] = load_now2(p.pre_ml + pr);
+#pragma unroll
+                    for (int k = 0; k < NG * 4; ++k) v[e][k] = load_now2(p.pre_o + pr * D + 16 * k + 2 * n);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
                     float w, w2;
-                    join(mt, lt, ml.x, ml.y, w, w2);
+                    join(m[nt][e], l[nt][e], ml[e].x, ml[e].y, w, w2);
 #pragma unroll
                     for (int k = 0; k < NG * 4; ++k) {
-                        const float2 v = *reinterpret_cast<const float2*>(p.pre_o + pr * D + 16 * k + 2 * n);
-                        y[k][0] = y[k][0] * w + v.x * w2;
-                        y[k][1] = y[k][1] * w + v.y * w2;
+                        y[nt][e][k][0] = y[nt][e][k][0] * w + v[e][k].x * w2;
+                        y[nt][e][k][1] = y[nt][e][k][1] * w + v[e][k].y * w2;
                     }
                 }
+            }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int head = head_of[nt][e];
+                if (head < 0) continue;
                 if (whole) {
-                    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+                    const float inv = l[nt][e] == 0.f ? 0.f : 1.f / l[nt][e];
                     T* out = static_cast<T*>(a.o) + s * a.o_stride + (int64_t)head * D + 2 * n;
 #pragma unroll
-                    for (int k = 0; k < NG * 4; ++k) write2(out + 16 * k, y[k][0] * inv, y[k][1] * inv);
-                    if (n == 0) write_lse(a, s, head, mt, lt);
+                    for (int k = 0; k < NG * 4; ++k) write2(out + 16 * k, y[nt][e][k][0] * inv, y[nt][e][k][1] * inv);
+                    if (n == 0) write_lse(a, s, head, m[nt][e], l[nt][e]);
                 } else {
-                    float* out = p.part_o + (slot * kRows + rr) * D + 2 * n;
+                    const int64_t row = slot * kRows + (head - head0);
+                    float* out = p.part_o + row * D + 2 * n;
 #pragma unroll
-                    for (int k = 0; k < NG * 4; ++k) write2(out + 16 * k, y[k][0], y[k][1]);
-                    if (n == 0) p.part_ml[slot * kRows + rr] = make_float2(mt, lt);
+                    for (int k = 0; k < NG * 4; ++k) write2(out + 16 * k, y[nt][e][k][0], y[nt][e][k][1]);
+                    if (n == 0) p.part_ml[row] = make_float2(m[nt][e], l[nt][e]);
                 }
             }
         const int64_t at = line.begin(piece + 1) - done.left;                // of tile done.k

@@ -122,7 +122,11 @@ def attn_decode_q4(q, cache, block_table, kv_lens, *, k_prefix=None, v_prefix=No
     [n_blocks, H_kv, block_size, d] come together: the groups of consecutive sequences whose first positions are shared, and
     where those positions are (their entries of block_table are blocks of k_prefix).  The rest as for ``attn_decode``.
     Returns (o, lse or None)."""
-    if len({x is None for x in (k_prefix, v_prefix, group_start, prefix_lens)}) > 1:
+    if group_start is None:
+        apart = k_prefix is not None or v_prefix is not None or prefix_lens is not None
+    else:
+        apart = k_prefix is None or v_prefix is None or prefix_lens is None
+    if apart:
         raise ValueError("k_prefix, v_prefix, group_start and prefix_lens come together")
     if _elsewhere(stream, q):
         with _on(stream, q):

@@ -191,7 +191,7 @@ __device__ __forceinline__ int unit_up(float most, float shrunk, float unit) {
 __device__ __forceinline__ float two_to(int i) { return __uint_as_float((uint32_t)(i + 127) << 23); }
 
 // A worker's place on the line: unit u of sequence s at tile k of its T.  A unit takes some
-// places more than it has tiles (q4_pad), for the time that its beginning and end take; a piece
+// places more than it has tiles (kQ4Pad), for the time that its beginning and end take; a piece
 // that ends among those holds the unit to its end, one that starts there starts with the next.
 struct Place {
     int64_t left;      // of the piece from here on
@@ -201,8 +201,8 @@ struct Place {
 
     __device__ __forceinline__ int run() const { return (int)min((int64_t)(T - k), left); }
     __device__ __forceinline__ bool whole() const { return k == 0 && left >= T; }
-    __device__ __forceinline__ void next_unit(const AttnDecodeLaunch& p, int pad) {
-        left -= T + pad - k;
+    __device__ __forceinline__ void next_unit(const AttnDecodeLaunch& p) {
+        left -= T + kQ4Pad - k;
         k = 0;
         if (++u < units || left <= 0) return;
         u = 0;
@@ -212,12 +212,12 @@ struct Place {
         } while (T == 0);
     }
     __device__ __forceinline__ Place() {}
-    __device__ __forceinline__ Place(const AttnDecodeLaunch& p, const PieceStart& at, int64_t length, int units_, int pad) {
+    __device__ __forceinline__ Place(const AttnDecodeLaunch& p, const PieceStart& at, int64_t length, int units_) {
         left = length, s = at.s, units = units_, info = at.info;
         T = (int)seq_tiles(info, kKeys);
-        u = (int32_t)divide(at.rel, T + pad);
-        k = (int32_t)(at.rel - (int64_t)u * (T + pad));
-        if (k >= T) next_unit(p, pad);
+        u = (int32_t)divide(at.rel, T + kQ4Pad);
+        k = (int32_t)(at.rel - (int64_t)u * (T + kQ4Pad));
+        if (k >= T) next_unit(p);
     }
 };
 
@@ -237,13 +237,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, blocks = (G + kRows - 1) / kRows;
     __shared__ PieceStart at_[WARPS];
-    const int pad = q4_pad(a);
-    const Line line = find_pieces<32 * WARPS, WARPS>(p, a.n_kv_heads * blocks, kKeys, at_, pad);
+    const Line line = find_pieces<32 * WARPS, WARPS>(p, a.n_kv_heads * blocks, kKeys, at_, kQ4Pad);
     griddep_launch();
     const int64_t piece = (int64_t)blockIdx.x * WARPS + warp;
     Place first;
     first.left = 0;
-    if (piece < line.pieces) first = Place(p, at_[warp], line.begin(piece + 1) - line.begin(piece), a.n_kv_heads * blocks, pad);
+    if (piece < line.pieces) first = Place(p, at_[warp], line.begin(piece + 1) - line.begin(piece), a.n_kv_heads * blocks);
     if (first.left <= 0) {
         if (lane == 0) p.open[piece] = make_int4(-1, 0, 0, 0);
         finish_empty<T, D>(p, piece, lane);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
             f_key += kKeys;
             if (--f_run == 0) {
                 Place f = ahead[warp];
-                f.next_unit(p, pad);
+                f.next_unit(p);
                 __syncwarp();
                 ahead[warp] = f;
                 __syncwarp();
@@ -743,7 +742,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         const int64_t at = line.begin(piece + 1) - done.left;                // of tile done.k
         const bool goes_on = done.k == 0 && !whole;      // begins here and ends in a later piece: the join's
         const int4 note = goes_on ? make_int4(s, done.u, (int)line.piece_of(at + done.T - 1), prefix_parts(p, done.info.x)) : make_int4(-1, 0, 0, 0);
-        done.next_unit(p, pad);
+        done.next_unit(p);
         more = done.left > 0;
         if (lane == 0 && !more) p.open[piece] = note;
         __syncwarp();

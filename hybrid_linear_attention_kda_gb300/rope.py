@@ -46,10 +46,6 @@ def _rotation(turns, d, dev, index):
     return (_dev(turns, "turns", _I64, (n,), dev, index) if n else None), 2 * n
 
 
-def _weight(w, name, d, dev, index):
-    return None if w is None else _dev(w, name, _F32, (d,), dev, index)
-
-
 def kda_qk_norm_rope(args: QkRopeArgs, stream=None):
     _kda._check(_kda.load().kda_qk_norm_rope(_byref(args), _kda._stream_handle(stream)))
 
@@ -70,7 +66,8 @@ def qk_norm_rope(q, k, positions, turns=None, *, interleaved=False, q_weight=Non
     kp, ks = _tokens(k, "k", dtype, kv, dev, ix)
     pos = _dev(positions, "positions", _I32, (T,), dev, ix)
     tp, rot = _rotation(turns, d, dev, ix)
-    wq, wk = _weight(q_weight, "q_weight", d, dev, ix), _weight(k_weight, "k_weight", d, dev, ix)
+    wq = None if q_weight is None else _dev(q_weight, "q_weight", _F32, (d,), dev, ix)
+    wk = None if k_weight is None else _dev(k_weight, "k_weight", _F32, (d,), dev, ix)
     q_out = _empty(shape, dtype=dtype, device=dev) if q_out is None else q_out
     k_out = _empty(kv, dtype=dtype, device=dev) if k_out is None else k_out
     qo, qos = _tokens(q_out, "q_out", dtype, shape, dev, ix)
@@ -105,7 +102,8 @@ def cache_append_rope(k, v, positions, turns, slot_map, k_cache, v_cache, *, q=N
     slots = _dev(slot_map, "slot_map", _I32, (T,), dev, ix)
     kc, vc, n_blocks, bs = _cache(k_cache, v_cache, dtype, H_kv, d, dev, ix)
     tp, rot = _rotation(turns, d, dev, ix)
-    wq, wk = _weight(q_weight, "q_weight", d, dev, ix), _weight(k_weight, "k_weight", d, dev, ix)
+    wq = None if q_weight is None else _dev(q_weight, "q_weight", _F32, (d,), dev, ix)
+    wk = None if k_weight is None else _dev(k_weight, "k_weight", _F32, (d,), dev, ix)
     H, qp, qs, qo, qos = 0, None, 0, None, 0
     if q is not None:
         H = _shape(q, "q", 3)[1]

@@ -15,12 +15,29 @@
 // K: a code in an fp16 number's lowest bits is that number: the subnormals are n 2^-24, exact
 // operands like any other.  A word's eight codes take four masks and a shift: at bits 4..7
 // a code counts 16-fold, which q's side makes up for.  q is scaled by a power of two for the
-// range of fp16.  (fp32 takes centred codes here too, and q's sum times m + 8 s: what the tensor
-// cores cut off of larger sums would be more than fp32 loses.)  V: the products add up over keys, so that a byte of codes has to meet the
-// same byte of the next key: ldmatrix transposes bytes, a permutation puts 0x64 behind each,
-// which makes 1024 + byte of it, and one fp16 instruction n - 8 of each of its codes.  A
-// product's rows are the keys in the order in which that hands them out.  Weights times scales are rounded to fp16: 11 bits, counted from the largest so far
-// of each head and group (a power of two, moved like the weights' own maximum).
+// range of fp16.  (fp32 takes centred codes here too, and q's sum times m + 8 s: what the
+// tensor cores cut off of larger sums would be more than fp32 loses.)
+//
+// V: the products add up over keys, so that a byte of codes has to meet the same byte of the
+// next key: ldmatrix transposes bytes, a permutation puts 0x64 behind each, which makes 1024 +
+// byte of it, and one fp16 instruction n - 8 of each of its codes.  A product's rows are the
+// keys in the order in which that hands them out.  Weights times scales are rounded to fp16: 11
+// bits, counted from the largest so far of each head and group (a power of two, moved like the
+// weights' own maximum).
+//
+// Bound, on long sequences, by the cache's bytes and the instructions that take codes apart: 300
+// a warp for 16 keys of d = 128, 104 of them masks, permutations and conversions of codes; the
+// ALU and issue slots are 55% and 64% busy, DRAM 90% of the measured copy rate between the
+// beginning and the end.  One sequence of 2^20 tokens, 8 heads: 0.22 ms (5.5 TB/s), of which
+// some 15 us are the beginning and the end and 6 us the join; in bf16 it takes 0.64 ms.  512
+// sequences of up to 2048: 127 us (4.7 TB/s).  16 query heads a key/value head: 0.33 ms, where
+// twice the rows make arithmetic of it (0.41 ms in units of eight).  7 requests of up to 700
+// tokens: 15 us, a chain of about ten trips to memory in two kernels.
+//
+// Twelve warps a block, three a scheduler, have 168 registers (one sequence of 2^20 203 us
+// without the join; sixteen with 128, 209 us).  The copies are cp.async by each warp for itself:
+// a copy warp that served the others with bulk and tensor copies of 1 KB took 0.57 ms, since such
+// copies leave a warp one lane at a time.
 #include <cuda_fp16.h>
 #include <float.h>
 
@@ -754,9 +771,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 }
 
 // The join of units that several pieces share, as join_kernel does it: parts in the order of the
-// prefix's blocks and then the pieces.  A row is one warp's where units have few parts (narrow),
-// the warps of a row's block then share them where there are many: every thread block counts
-// the open units itself and takes its share of their rows.
+// prefix's blocks and then the pieces.  A row is one warp's where units have few parts (narrow).
+// Where they have many (16 pieces a unit on average), a thread block's warps share a row's: every
+// block counts the open units itself and takes its share of their rows.  One sequence of 2^20
+// tokens: 219 us, all narrow 262 us; 512 of up to 2048: 127 us, all wide 180 us.
 struct OpenRow {
     int4 open;            // sequence, unit, last piece, prefix parts
     int64_t c0;           // the piece in which the unit begins

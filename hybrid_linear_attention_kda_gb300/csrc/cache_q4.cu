@@ -1,4 +1,12 @@
 // The 4-bit paged cache: append and read-back (include/kda_cache_q4.h has the format).
+//
+// The append is bound by its arithmetic: 32768 tokens of 8 heads, d = 128, bf16, with the values
+// written too, take 73 us (4.2 TB/s) at 78% of the issue slots, 266 instructions a warp for 8
+// channels a lane, a quarter of them for lanes whose quotient lies in the middle of two codes.
+// In pairs of floats (fma.f32x2) they took 75 us.  512 tokens: 3.0 us.
+//
+// The read-back is bound by HBM, most of it writes: 24 sequences of up to 16384 tokens, 8 heads,
+// d = 128 to bf16 take 200 us (5.9 TB/s).
 #include <float.h>
 #include <math_constants.h>
 

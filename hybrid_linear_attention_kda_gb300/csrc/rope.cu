@@ -7,6 +7,11 @@
 // lane's four pairs are the same in all rows of a token, so that a warp forms the sines of
 // its token once, with the weights in them, and walks the token's rows, several at a time: loads
 // first, then each row's sum of squares over its lanes, its norm and its rotation.
+//
+// Bound by HBM: 32768 tokens, 32 + 8 heads, d = 128, bf16 take 111 us (6.1 TB/s), fp32 with d = 64
+// 7001 tokens, 16 + 2 + 2 heads 17 us (4.3 TB/s: a wave and a half of warps, each with a
+// beginning of its own).  512 tokens take 4.3 us: the launch and three trips to memory, the
+// position, the frequencies, the rows.
 #include "attn_common.cuh"
 #include "rope.cuh"
 
@@ -60,7 +65,7 @@ template <bool kHalves> __device__ __forceinline__ constexpr int first_of(int i)
 template <bool kHalves> __device__ __forceinline__ constexpr int second_of(int i) { return kHalves ? 4 + i : 2 * i + 1; }
 
 // Rows lo .. hi - 1 of one kind; from and to are the lane's places in row 0, kRows rows a warp.
-// Rows of a lane under way: 64 bytes.
+// Rows of a lane under way: 64 bytes (fp32 with 128: 19 us for the 7001 tokens, 92 registers).
 template <typename T> constexpr int kAtOnce = 8 / (int)sizeof(T);
 
 template <typename T, int D, bool kHalves>
@@ -189,7 +194,8 @@ template <typename T, int D, bool kAppend>
 cudaError_t launch_t(const RopeLaunch& p, cudaStream_t s) {
     constexpr int kBatch = kAtOnce<T> * (32 / (D / 8));
     const int n_rows = p.a.n_heads + (kAppend ? 2 : 1) * p.a.n_kv_heads, batches = (n_rows + kBatch - 1) / kBatch;
-    // a token's rows are spread over warps until the GPU has 32 of them an SM
+    // A token's rows are spread over warps until the GPU has 32 of them an SM (bf16, 40 rows, d =
+    // 128: 512 tokens 4.3 us, a warp each 6.6 us; 6000 tokens, a warp each, 25.1 us, three 28.4 us).
     int64_t parts = (152 * 32 + p.a.n_tokens - 1) / p.a.n_tokens;
     parts = parts < batches ? parts : batches;
     const int32_t part_rows = (int32_t)((batches + parts - 1) / parts) * kBatch;

@@ -102,9 +102,13 @@ kda_status_t kda_cache_unpack_q4(const kda_cache_unpack_q4_args *args, void *str
  *    bits.  Without groups the three are ignored.
  * q and o are of base.dtype.  The keys' scores are the exact products of the codes
  * with q, which bf16 q holds exactly and fp32 q in two 11-bit parts, accumulated
- * in fp32; a weight times its value's scale is rounded to bf16 (bf16), or held in
- * two bf16 parts (fp32), for the product with the codes.  Positions that a mask
- * hides never reach a result, whatever their codes and scales are.
+ * in fp32, for |q| up to 2^100 and scores up to 2^27 as there.  A weight times its
+ * value's scale is held in fp16 (fp32: in two such parts) for the product with the
+ * codes: 11 bits (22), counted from the largest one so far of its head and group,
+ * so that values of any size may stand beside each other.  The weights' sum is
+ * taken before that rounding.  Positions that a mask hides never reach a result,
+ * whatever their codes and scales are.  A position that is NaN makes its key
+ * group's heads NaN, or its value group's channels.
  */
 typedef struct kda_attn_decode_q4_args {
     kda_attn_decode_args base;

@@ -15,7 +15,8 @@
  *     (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = 2 pi frac(p F_i / 2^64)
  * for the pairs i < rot_dim / 2 of the first rot_dim channels: channels i and
  * i + rot_dim / 2, or 2 i and 2 i + 1 where interleaved is set; the others are y.
- * All of it in fp32, rounded once to the element type.  F_i = turns[i] is the
+ * All of it in fp32, rounded once to the element type; the squares are fp32's too,
+ * so that a norm is for |x| below 2^60 (and above 2^-60, where eps is 0).  F_i = turns[i] is the
  * frequency in turns a position, as a 64-bit fraction of one turn: p F_i wraps
  * around a turn exactly, so that far positions are as precise as near ones.  A
  * frequency of f radians a position is F = round(f / (2 pi) * 2^64) modulo 2^64.

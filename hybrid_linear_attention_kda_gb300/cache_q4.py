@@ -6,16 +6,18 @@ a fused projection's output.  All tensors are on the current device: the library
 """
 import collections
 import ctypes
+import struct
 
 import torch
 
 import hybrid_linear_attention_kda_gb300 as _kda
 from . import attention as _attention
 from .attention import (_cache, _current_stream, _dev, _elsewhere, _empty, _first, _FLOATS, _I32, _on, _outputs, _shape, _tokens,
-                        _U8, _workspace)
-from .attention_abi import AttnDecodeArgs, AttnDecodeQ4Args, CacheAppendQ4Args, CacheQ4, CacheUnpackQ4Args
+                        _U8)
+from .attention_abi import PACK, AttnDecodeQ4Args, CacheAppendQ4Args, CacheUnpackQ4Args
 
 _BF, _byref = torch.bfloat16, ctypes.byref
+_pack_append, _pack_unpack, _pack_decode = (struct.Struct(PACK[block]).pack for block in (CacheAppendQ4Args, CacheUnpackQ4Args, AttnDecodeQ4Args))
 GROUP = 64          # channels that share a scale
 
 #: The cache's tensors: codes uint8 [n_blocks, H_kv, block_size, d / 2], scales bf16 [n_blocks, H_kv, block_size, d / 64, 2].
@@ -33,14 +35,12 @@ def q4_cache(n_blocks, n_kv_heads, block_size, d, device=None):
 
 
 def _q4(cache, heads, d, dev, index):
-    """(the cache's argument block, n_blocks, block_size)."""
+    """The cache's argument block, as values to pack: four addresses, n_blocks, block_size, 0."""
     k_codes, k_scales, v_codes, v_scales = cache
-    shape = _shape(k_codes, "k_codes", 4)
-    n_blocks, bs = shape[0], shape[2]
+    n_blocks, _, bs, _ = _shape(k_codes, "k_codes", 4)
     codes, scales = (n_blocks, heads, bs, d // 2), (n_blocks, heads, bs, d // GROUP, 2)
-    return CacheQ4(_dev(k_codes, "k_codes", _U8, codes, dev, index), _dev(k_scales, "k_scales", _BF, scales, dev, index),
-                   _dev(v_codes, "v_codes", _U8, codes, dev, index), _dev(v_scales, "v_scales", _BF, scales, dev, index),
-                   n_blocks, bs, 0), n_blocks, bs
+    return (_dev(k_codes, "k_codes", _U8, codes, dev, index), _dev(k_scales, "k_scales", _BF, scales, dev, index),
+            _dev(v_codes, "v_codes", _U8, codes, dev, index), _dev(v_scales, "v_scales", _BF, scales, dev, index), n_blocks, bs, 0)
 
 
 def kda_cache_append_q4(args: CacheAppendQ4Args, stream=None):
@@ -59,14 +59,14 @@ def cache_append_q4(k, v, slot_map, cache, *, k_out=None, v_out=None, want_value
     T, H_kv, d = shape
     vp, vs = _tokens(v, "v", dtype, shape, dev, ix)
     slots = _dev(slot_map, "slot_map", _I32, (T,), dev, ix)
-    block, _, _ = _q4(cache, H_kv, d, dev, ix)
+    block = _q4(cache, H_kv, d, dev, ix)
     if want_values:
         k_out = _empty(shape, dtype=dtype, device=dev) if k_out is None else k_out
         v_out = _empty(shape, dtype=dtype, device=dev) if v_out is None else v_out
-    ko, kos = (None, 0) if k_out is None else _tokens(k_out, "k_out", dtype, shape, dev, ix)
-    vo, vos = (None, 0) if v_out is None else _tokens(v_out, "v_out", dtype, shape, dev, ix)
-    a = CacheAppendQ4Args(T, H_kv, d, code, 0, ks, vs, kos, vos, kp, vp, ko, vo, slots, block)
-    status = _kda.load().kda_cache_append_q4(_byref(a), _current_stream(ix))
+    ko, kos = (0, 0) if k_out is None else _tokens(k_out, "k_out", dtype, shape, dev, ix)
+    vo, vos = (0, 0) if v_out is None else _tokens(v_out, "v_out", dtype, shape, dev, ix)
+    a = _pack_append(T, H_kv, d, code, 0, ks, vs, kos, vos, kp, vp, ko, vo, slots, *block)
+    status = _kda.load().kda_cache_append_q4(a, _current_stream(ix))
     if status:
         _kda._check(status)
     return k_out, v_out
@@ -92,17 +92,17 @@ def cache_unpack_q4(cache, block_table, kv_lens, k_cache, v_cache, to_table, *, 
     if ix != _attention._current_device():
         _attention._not_current(ix, "k_cache")
     vc = _dev(v_cache, "v_cache", dtype, (wide, H_kv, bs, d), dev, ix)
-    block, _, cache_bs = _q4(cache, H_kv, d, dev, ix)
-    if cache_bs != bs:
-        raise ValueError(f"the caches' block sizes differ ({cache_bs} and {bs})")
+    block = _q4(cache, H_kv, d, dev, ix)
+    if block[5] != bs:
+        raise ValueError(f"the caches' block sizes differ ({block[5]} and {bs})")
     n, stride = _shape(block_table, "block_table", 2)
     to_stride = _shape(to_table, "to_table", 2)[1]
     table, to = _dev(block_table, "block_table", _I32, (n, stride), dev, ix), _dev(to_table, "to_table", _I32, (n, to_stride), dev, ix)
     kv = _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix)
-    at = None if first is None else _dev(first, "first", _I32, (n,), dev, ix)
-    a = CacheUnpackQ4Args(n, H_kv, d, _kda.KDA_BF16 if dtype == _BF else _kda.KDA_FP32, block, table, to, stride, to_stride, at,
-                          kv, kc, vc, wide)
-    status = _kda.load().kda_cache_unpack_q4(_byref(a), _current_stream(ix))
+    at = 0 if first is None else _dev(first, "first", _I32, (n,), dev, ix)
+    a = _pack_unpack(n, H_kv, d, _kda.KDA_BF16 if dtype == _BF else _kda.KDA_FP32, *block, table, to, stride, to_stride, at,
+                     kv, kc, vc, wide)
+    status = _kda.load().kda_cache_unpack_q4(a, _current_stream(ix))
     if status:
         _kda._check(status)
 
@@ -137,10 +137,11 @@ def attn_decode_q4(q, cache, block_table, kv_lens, *, k_prefix=None, v_prefix=No
     n, H, d = shape
     H_kv = _shape(cache[0], "k_codes", 4)[1]
     stride = _shape(block_table, "block_table", 2)[1]
-    block, _, bs = _q4(cache, H_kv, d, dev, ix)
+    block = _q4(cache, H_kv, d, dev, ix)
+    bs = block[5]
     table = _dev(block_table, "block_table", _I32, (n, stride), dev, ix)
     kv = _dev(kv_lens, "kv_lens", _I32, (n,), dev, ix)
-    groups, start, prefix, kc, vc, wide = 0, None, None, None, None, 0
+    groups = start = prefix = kc = vc = wide = 0
     if group_start is not None:
         groups, = _shape(prefix_lens, "prefix_lens", 1)
         start = _dev(group_start, "group_start", _I32, (groups + 1,), dev, ix)
@@ -149,14 +150,16 @@ def attn_decode_q4(q, cache, block_table, kv_lens, *, k_prefix=None, v_prefix=No
         if prefix_bs != bs:
             raise ValueError(f"the caches' block sizes differ ({prefix_bs} and {bs})")
     o, op, os_, lse, zp = _outputs(dtype, shape, dev, ix, o, lse, want_lse)
-    a = AttnDecodeQ4Args((n, H, H_kv, d, code, d ** -0.5 if scale is None else scale, qs, os_, qp, op, zp, kc, vc, table, kv,
-                          wide, bs, stride, groups, 0, start, prefix), block)
+    before = (n, H, H_kv, d, code, d ** -0.5 if scale is None else scale, qs, os_, qp, op, zp or 0, kc, vc, table, kv, wide, bs,
+              stride, groups, 0, start, prefix)
     lib = _kda.load()
-    need = lib.kda_attn_decode_q4_workspace_size(_byref(a))
-    if need:
-        base = a.base                                        # part of a, and keeps the workspace until the launch
-        _workspace(base, workspace, need, dev)
-    status = lib.kda_attn_decode_q4(_byref(a), _current_stream(ix))
+    need = lib.kda_attn_decode_q4_workspace_size(_pack_decode(*before, 0, 0, *block))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = _empty(need, dtype=_U8, device=dev)
+        at = workspace.data_ptr()
+    else:
+        at, need = _kda._dev(workspace, "workspace", device=dev), workspace.numel() * workspace.element_size()
+    status = lib.kda_attn_decode_q4(_pack_decode(*before, at, need, *block), _current_stream(ix))
     if status:
         _kda._check(status)
     return o, lse

@@ -5,15 +5,17 @@ Argument marshalling only, as in the package itself; the header states formulas,
 views of a fused projection's output.  All tensors are on the current device: the library launches there.
 """
 import ctypes
+import struct
 from decimal import Decimal, localcontext
 
 import torch
 
 import hybrid_linear_attention_kda_gb300 as _kda
 from .attention import _cache, _current_stream, _dev, _elsewhere, _empty, _F32, _first, _I32, _on, _shape, _tokens
-from .attention_abi import CacheAppendRopeArgs, QkRopeArgs
+from .attention_abi import PACK, CacheAppendRopeArgs, QkRopeArgs
 
 _I64, _byref = torch.int64, ctypes.byref
+_pack_rope, _pack_append = (struct.Struct(PACK[block]).pack for block in (QkRopeArgs, CacheAppendRopeArgs))
 _TWO_PI = Decimal("6.28318530717958647692528676655900576839433879875021164194989")
 
 
@@ -39,11 +41,11 @@ def rope_turns(inv_freq, device=None):
 def _rotation(turns, d, dev, index):
     """(address, rotated channels) of the frequencies."""
     if turns is None:
-        return None, 0
+        return 0, 0
     n, = _shape(turns, "turns", 1)
     if 2 * n > d:
         raise ValueError(f"turns holds {n} frequencies for {d // 2} pairs of channels")
-    return (_dev(turns, "turns", _I64, (n,), dev, index) if n else None), 2 * n
+    return (_dev(turns, "turns", _I64, (n,), dev, index) if n else 0), 2 * n
 
 
 def kda_qk_norm_rope(args: QkRopeArgs, stream=None):
@@ -66,14 +68,14 @@ def qk_norm_rope(q, k, positions, turns=None, *, interleaved=False, q_weight=Non
     kp, ks = _tokens(k, "k", dtype, kv, dev, ix)
     pos = _dev(positions, "positions", _I32, (T,), dev, ix)
     tp, rot = _rotation(turns, d, dev, ix)
-    wq = None if q_weight is None else _dev(q_weight, "q_weight", _F32, (d,), dev, ix)
-    wk = None if k_weight is None else _dev(k_weight, "k_weight", _F32, (d,), dev, ix)
+    wq = 0 if q_weight is None else _dev(q_weight, "q_weight", _F32, (d,), dev, ix)
+    wk = 0 if k_weight is None else _dev(k_weight, "k_weight", _F32, (d,), dev, ix)
     q_out = _empty(shape, dtype=dtype, device=dev) if q_out is None else q_out
     k_out = _empty(kv, dtype=dtype, device=dev) if k_out is None else k_out
     qo, qos = _tokens(q_out, "q_out", dtype, shape, dev, ix)
     ko, kos = _tokens(k_out, "k_out", dtype, kv, dev, ix)
-    a = QkRopeArgs(T, H, kv[1], d, code, rot, 1 if interleaved else 0, eps, 0, qs, ks, qos, kos, qp, kp, qo, ko, wq, wk, tp, pos)
-    status = _kda.load().kda_qk_norm_rope(_byref(a), _current_stream(ix))
+    a = _pack_rope(T, H, kv[1], d, code, rot, 1 if interleaved else 0, eps, 0, qs, ks, qos, kos, qp, kp, qo, ko, wq, wk, tp, pos)
+    status = _kda.load().kda_qk_norm_rope(a, _current_stream(ix))
     if status:
         _kda._check(status)
     return q_out, k_out
@@ -102,17 +104,17 @@ def cache_append_rope(k, v, positions, turns, slot_map, k_cache, v_cache, *, q=N
     slots = _dev(slot_map, "slot_map", _I32, (T,), dev, ix)
     kc, vc, n_blocks, bs = _cache(k_cache, v_cache, dtype, H_kv, d, dev, ix)
     tp, rot = _rotation(turns, d, dev, ix)
-    wq = None if q_weight is None else _dev(q_weight, "q_weight", _F32, (d,), dev, ix)
-    wk = None if k_weight is None else _dev(k_weight, "k_weight", _F32, (d,), dev, ix)
-    H, qp, qs, qo, qos = 0, None, 0, None, 0
+    wq = 0 if q_weight is None else _dev(q_weight, "q_weight", _F32, (d,), dev, ix)
+    wk = 0 if k_weight is None else _dev(k_weight, "k_weight", _F32, (d,), dev, ix)
+    H = qp = qs = qo = qos = 0
     if q is not None:
         H = _shape(q, "q", 3)[1]
         qp, qs = _tokens(q, "q", dtype, (T, H, d), dev, ix)
         q_out = _empty((T, H, d), dtype=dtype, device=dev) if q_out is None else q_out
         qo, qos = _tokens(q_out, "q_out", dtype, (T, H, d), dev, ix)
-    a = CacheAppendRopeArgs((T, H, H_kv, d, code, rot, 1 if interleaved else 0, eps, 0, qs, ks, qos, 0, qp, kp, qo, None, wq,
-                             wk, tp, pos), vp, vs, slots, kc, vc, n_blocks, bs, 0)
-    status = _kda.load().kda_cache_append_rope(_byref(a), _current_stream(ix))
+    a = _pack_append(T, H, H_kv, d, code, rot, 1 if interleaved else 0, eps, 0, qs, ks, qos, 0, qp, kp, qo, 0, wq, wk, tp, pos,
+                     vp, vs, slots, kc, vc, n_blocks, bs, 0)
+    status = _kda.load().kda_cache_append_rope(a, _current_stream(ix))
     if status:
         _kda._check(status)
     return q_out

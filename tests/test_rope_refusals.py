@@ -1,6 +1,7 @@
 """What the norm and rotation calls refuse, without a GPU, and their oracle and frequencies."""
 import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -8,6 +9,7 @@ import torch
 
 import hybrid_linear_attention_kda_gb300 as kda
 from hybrid_linear_attention_kda_gb300 import build as kbuild
+from hybrid_linear_attention_kda_gb300.attention_abi import PACK
 from oracle import rope as orope
 
 P = 0x10000000
@@ -45,6 +47,26 @@ def _append(qk=(), **over):
 def test_struct_sizes(lib):
     assert ctypes.sizeof(kda.QkRopeArgs) == 8 + 4 * 8 + 8 * 4 + 8 * 8
     assert ctypes.sizeof(kda.CacheAppendRopeArgs) == ctypes.sizeof(kda.QkRopeArgs) + 8 * 6 + 4 * 2
+
+
+def _leaves(block):
+    """(offset, ctypes type) of a block's fields, those of blocks within it too."""
+    out = []
+    for name, kind in block._fields_:
+        at = getattr(block, name).offset
+        out += [(at + o, k) for o, k in _leaves(kind)] if issubclass(kind, ctypes.Structure) else [(at, kind)]
+    return out
+
+
+@pytest.mark.parametrize("block", list(PACK), ids=lambda b: b.__name__)
+def test_packed_blocks_are_the_ctypes_blocks(block):
+    """The binding packs its argument blocks by format: field for field at the places of the ctypes mirror."""
+    pack = struct.Struct(PACK[block])
+    assert pack.size == ctypes.sizeof(block)
+    fields = _leaves(block)
+    data = pack.pack(*[float(i + 1) if kind is ctypes.c_float else i + 1 for i, (_, kind) in enumerate(fields)])
+    for i, (at, kind) in enumerate(fields):
+        assert kind.from_buffer_copy(data, at).value == i + 1, (i, kind)
 
 
 SHARED = [

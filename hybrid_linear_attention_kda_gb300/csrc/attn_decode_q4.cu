@@ -25,11 +25,12 @@
 // bits, counted from the largest so far of each head and group (a power of two, moved like the
 // weights' own maximum).
 //
-// Bound, on long sequences, by the cache's bytes and the instructions that take codes apart: 300
-// a warp for 16 keys of d = 128, 104 of them masks, permutations and conversions of codes; the
+// Bound, on long sequences, by the cache's bytes and the instructions that take codes apart: 315
+// a warp for 16 keys of d = 128, 104 of them (by the source) masks, permutations and conversions of
+// codes; the
 // ALU and issue slots are 55% and 64% busy, DRAM 90% of the measured copy rate between the
 // beginning and the end.  One sequence of 2^20 tokens, 8 heads: 0.22 ms (5.5 TB/s), of which
-// some 15 us are the beginning and the end and 6 us the join; in bf16 it takes 0.64 ms.  512
+// 23 us do not grow with the length; in bf16 it takes 0.69 ms.  512
 // sequences of up to 2048: 127 us (4.7 TB/s).  16 query heads a key/value head: 0.33 ms, where
 // twice the rows make arithmetic of it (0.41 ms in units of eight).  7 requests of up to 700
 // tokens: 15 us, a chain of about ten trips to memory in two kernels.

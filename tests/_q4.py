@@ -6,9 +6,11 @@ A = 15 s + |m| in magnitude.
   scores   sums of d products in fp32, each accumulation cut or rounded (2 u), and the parts' factors: off by at most
            (d + 16) 2 u sum |q_c| A_c; fp32 q is cut into two parts of 11 bits, 4 u more of the same sum.  e bounds this over
            a batch, times scale, and twice for the base-2 detour.
-  weights  are off by a factor 1 +- (2 e + 2^-20); times s they are rounded by w = 2^-8 (bf16) or 2^-16 (two bf16 parts).
+  weights  are off by a factor 1 +- (2 e + 2^-20); times s they are rounded to fp16: w = 2^-11 (bf16), or 2^-21
+           (two parts of 11 bits).  What falls under fp16's range is below K u of the sum, counted there.  A bf16 prefix has
+           weights in bf16, w = 2^-8; an fp32 one fp32 weights, within 2^-21.
   output   the sums over K positions, accumulated in fp32 (2 u each), are of p s (n - 8) and p (m + 8 s); spread is the sum
-           of their magnitudes:  |o - ref| <= (2 e + 2^-20 + 2 K u + w) spread + r |ref|.
+           of their magnitudes:  |o - ref| <= (2 e + 2^-20 + 2 K u) spread + sum of w spread + r |ref|.
   lse      |lse - ref| <= e + 2^-20 + K u + 4 u |ref|
 Positions of a shared prefix are full-width keys and values; their magnitudes take the places of A and of the spread.
 """
@@ -126,13 +128,16 @@ def check(o, lse, q, c, scale, dtype, only=None):
     for i in range(len(c.kv)) if only is None else only:
         keys, values, key_size, value_size = c.sequence(i)
         ref, ref_lse, spread = attention(qn[i], keys, values, value_size, scale)
+        before = c.before[i] if hasattr(c, "before") else 0
+        wide = attention(qn[i], keys, values, np.where(np.arange(len(keys))[:, None, None] < before, value_size, 0), scale)[2]
         K, r = keys.shape[0], A.half_step(dtype)
         if K == 0:
             assert (o[i] == 0).all() and (lse[i] == -np.inf).all()
             continue
         e = 2 * (d + 18) * 2 * A.U * abs(scale) * float(np.abs(qn[i]).max(0) @ key_size.max((0, 1)))
-        f = 2 * e + 2.0 ** -20 + 2 * K * A.U + (2.0 ** -8 if dtype == BF else 2.0 ** -16)
-        bound = f * spread + r * np.abs(ref) * (1 + f) + 1e-30
+        f = 2 * e + 2.0 ** -20 + 2 * K * A.U
+        rounded = 2.0 ** -11 * (spread - wide) + 2.0 ** -8 * wide if dtype == BF else 2.0 ** -21 * spread
+        bound = (f * spread + rounded) * (1 + r) + r * np.abs(ref) + 1e-30
         off = np.abs(o[i] - ref)
         assert np.isfinite(o[i]).all() and (off <= bound).all(), (i, K, float((off / bound).max()), np.argwhere(off > bound)[:4].tolist())
         assert (np.abs(lse[i] - ref_lse) <= e + 2.0 ** -20 + K * A.U + 4 * A.U * np.abs(ref_lse)).all(), (i, K, float(np.abs(lse[i] - ref_lse).max()))

@@ -9,8 +9,7 @@
 // first, then each row's sum of squares over its lanes, its norm and its rotation.
 //
 // Bound by HBM: 32768 tokens, 32 + 8 heads, d = 128, bf16 take 111 us (6.1 TB/s), fp32 with d = 64
-// 7001 tokens, 16 + 2 + 2 heads 17 us (4.3 TB/s: a wave and a half of warps, each with a
-// beginning of its own).  512 tokens take 4.3 us: the launch and three trips to memory, the
+// 7001 tokens, 16 + 2 + 2 heads 17 us (4.3 TB/s).  512 tokens take 4.3 us: the launch and three trips to memory, the
 // position, the frequencies, the rows.
 #include "attn_common.cuh"
 #include "rope.cuh"
@@ -53,7 +52,6 @@ __device__ __forceinline__ void turn(int32_t position, uint64_t turns, float& c,
     if (quarter == 1 || quarter == 2) c = -c;
     if (quarter >= 2) s = -s;
 }
-
 
 // What a lane makes of its pairs in all rows of one kind: with the weights w and its token's
 // angles, (x0, x1) -> ((w0 c) x0 - (w1 s) x1, (w0 s) x0 + (w1 c) x1), times the row's norm.

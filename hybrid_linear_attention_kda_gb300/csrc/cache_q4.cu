@@ -210,24 +210,29 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_consta
 constexpr int kWarps = kThreads / 32, kRows = 16;           // an item: 16 positions of one head
 
 // A lane's sixteen channels in stores of whole 32-byte sectors (two of 16 bytes each: 240 us for
-// 24 sequences of up to 16384 tokens, 8 heads, d = 128; so: 200 us).
-__device__ __forceinline__ void store32(void* to, uint4 a, uint4 b) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
-                 "r"(b.z), "r"(b.w)
-                 : "memory");
+// 24 sequences of up to 16384 tokens, 8 heads, d = 128; so: 200 us).  Such a store needs 32-byte
+// alignment: caches that are aligned to 16 bytes only (`sectors` false) take two of 16.
+__device__ __forceinline__ void store32(void* to, uint4 a, uint4 b, bool sectors) {
+    if (sectors) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                     "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(to)[0] = a, static_cast<uint4*>(to)[1] = b;
+    }
 }
-__device__ __forceinline__ void write_sixteen(__nv_bfloat16* to, uint2 codes, uint32_t scale) {
+__device__ __forceinline__ void write_sixteen(__nv_bfloat16* to, uint2 codes, uint32_t scale, bool sectors) {
     Eight<__nv_bfloat16> x, y;
     values_of(codes.x, scale, x);
     values_of(codes.y, scale, y);
-    store32(to, x.r, y.r);
+    store32(to, x.r, y.r, sectors);
 }
-__device__ __forceinline__ void write_sixteen(float* to, uint2 codes, uint32_t scale) {
+__device__ __forceinline__ void write_sixteen(float* to, uint2 codes, uint32_t scale, bool sectors) {
     Eight<float> x;
     values_of(codes.x, scale, x);
-    store32(to, reinterpret_cast<const uint4*>(x.r)[0], reinterpret_cast<const uint4*>(x.r)[1]);
+    store32(to, reinterpret_cast<const uint4*>(x.r)[0], reinterpret_cast<const uint4*>(x.r)[1], sectors);
     values_of(codes.y, scale, x);
-    store32(to + 8, reinterpret_cast<const uint4*>(x.r)[0], reinterpret_cast<const uint4*>(x.r)[1]);
+    store32(to + 8, reinterpret_cast<const uint4*>(x.r)[0], reinterpret_cast<const uint4*>(x.r)[1], sectors);
 }
 
 // Items in the order of sequences, positions, heads, dealt to the warps in turn, so that all
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(kThreads) unpack_q4_kernel(const __grid_consta
     constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes, kSteps = kRows / kAtOnce;    // lanes of a row, rows of a step
     const int own_row = lane / kLanes, own = lane % kLanes;
     const int64_t cap = (int64_t)min(a.table_stride, a.to_stride) * bs;
+    const bool sectors = ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & 31u) == 0;
     const int64_t workers = (int64_t)gridDim.x * kWarps, worker = (int64_t)blockIdx.x * kWarps + (tid >> 5);
     int64_t base = 0;                                        // items of the sequences before this chunk
     for (int32_t s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
@@ -299,7 +305,8 @@ __global__ void __launch_bounds__(kThreads) unpack_q4_kernel(const __grid_consta
                 for (int k = 0; k < kSteps; ++k) {
                     const int32_t pos = pos0 + own_row + k * kAtOnce;
                     if (pos < r.x || pos >= r.y) continue;
-                    write_sixteen(static_cast<T*>(v ? a.v_cache : a.k_cache) + (dst + k * kAtOnce) * D + own * 16, codes[v][k], scale[v][k]);
+                    write_sixteen(static_cast<T*>(v ? a.v_cache : a.k_cache) + (dst + k * kAtOnce) * D + own * 16, codes[v][k], scale[v][k],
+                                  sectors);
                 }
         }
         base += total;

@@ -52,6 +52,9 @@ using namespace decode;
 constexpr int kKeys = kQ4Keys;
 constexpr float kMaxGrowth = 8.f;        // log2 of how far weights may exceed 1 before their maximum moves
 constexpr float kMostWeight = 0x1p15f;   // times scale, in units: below fp16's largest
+// A weight (up to 2^8) times the unit stays finite, so that a weight of zero gives zeros whatever
+// its scale is.  (Scale times unit may not: a unit that was set by tiny scales meets a large one.)
+constexpr int kMostUnit = 118;           // log2
 
 // Per warp: a ring of tiles, each two halves of 16 keys, which may lie in two pages; codes
 // of K, codes of V, scales of K, scales of V.
@@ -204,7 +207,7 @@ __device__ __forceinline__ int unit_up(float most, float shrunk, float unit) {
     const int at = (int)(__float_as_uint(unit) >> 23) - 127;
     int up = 6 - 10 - ((int)(__float_as_uint(most) >> 23) - 127) - at;
     if (shrunk != 0.f) up = min(up, shrunk == 1.f ? 0 : 40 + 126 - (int)(__float_as_uint(shrunk) >> 23));
-    return max(-120 - at, min(120 - at, up));                        // the unit and its inverse stay normal
+    return max(-120 - at, min(kMostUnit - at, up));                  // the unit and its inverse stay normal
 }
 __device__ __forceinline__ float two_to(int i) { return __uint_as_float((uint32_t)(i + 127) << 23); }
 
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 float y[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    y[e] = x[nt][r][e] * (step * unit[nt][e][g]);
+                    y[e] = x[nt][r][e] * unit[nt][e][g] * step;      // in this order: see kMostUnit
                     if (kTwoParts) {
                         const float hi = __half2float(__float2half_rn(y[e]));
                         y[e] = t < 2 ? hi : y[e] - hi;

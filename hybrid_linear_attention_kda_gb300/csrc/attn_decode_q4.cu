@@ -201,7 +201,8 @@ __device__ __forceinline__ void write2(__nv_bfloat16* to, float x, float y) { *r
 // tile's largest weight, `most` * 2^10, lies at 2^6 .. 2^7 of it: then weights have 11 bits
 // down to 2^-20 of the largest and may grow by 2^8.  Upwards only where the sums so far have
 // shrunk (by `shrunk`; 0: there were none), and not by so much that they could leave fp32's
-// range.
+// range.  The unit starts at its largest, where hardly a weight fits: the first one that is not
+// zero (of a group whose first values have no width) moves it down.
 __device__ __forceinline__ int unit_up(float most, float shrunk, float unit) {
     if (!(most > 0.f)) return 0;
     const int at = (int)(__float_as_uint(unit) >> 23) - 127;
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
             for (int e = 0; e < 2; ++e) {
                 m[nt][e] = -FLT_MAX, l[nt][e] = 0.f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) low[nt][e][g] = 0.f, unit[nt][e][g] = 1.f;
+                for (int g = 0; g < NG; ++g) low[nt][e][g] = 0.f, unit[nt][e][g] = two_to(kMostUnit);
             }
         }
 

@@ -83,3 +83,36 @@ def _stairs(kda, dev, dtype, d, H, H_kv, scores, sizes):
     c.m[0] = np.where(np.isnan(c.m[0]), np.nan, _each(c, 0, 0, m))
     c.upload()
     return c
+
+
+@pytest.mark.parametrize("n", REQUESTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,H,H_kv", HEADS)
+@pytest.mark.parametrize("size", [0, -7, -14, -20, -27, -60])
+@pytest.mark.parametrize("empty", ["32", "64", "300", "each"])
+def test_value_groups_without_width(kda, cuda_device, dtype, n, d, H, H_kv, size, empty):
+    """Values of zero in the first positions, or in the first 96 of every 160 of many pieces; small ones behind them."""
+    K = 2500 if empty == "each" else 700
+    c = _q4.Paged(32, [K], H_kv, d, 32, dtype, cuda_device)
+    j = np.arange(K)
+    _scale_values(c, 0, np.where(j % 160 < 96 if empty == "each" else j < int(empty), 0.0, 2.0 ** size))
+    c.upload()
+    q = A.randn(33, (H, d), dtype, cuda_device)
+    _check(kda, q, c, dtype, n)
+
+
+@pytest.mark.parametrize("n", REQUESTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_group_without_width(kda, cuda_device, dtype, n):
+    """Only one of a head's two groups has no width at first; positions of one value, not of zero, among them."""
+    d, H, K = 128, 4, 200
+    c = _q4.Paged(34, [K], 1, d, 16, dtype, cuda_device)
+    for j in range(K):
+        at = (1, c.table_np[0, j // 16], 0, j % 16, 1)
+        if j < 40:
+            c.s[at], c.m[at] = 0, (0, 2.0 ** -18)[j % 2]
+        else:
+            c.s[at], c.m[at] = c.s[at] * np.float32(2.0 ** -18), c.m[at] * np.float32(2.0 ** -18)
+    c.upload()
+    q = A.randn(35, (H, d), dtype, cuda_device)
+    _check(kda, q, c, dtype, n)

@@ -200,16 +200,19 @@ __device__ __forceinline__ void write2(__nv_bfloat16* to, float x, float y) { *r
 // By how many powers of two the unit of a head's and group's weights is to move, so that the
 // tile's largest weight, `most` * 2^10, lies at 2^6 .. 2^7 of it: then weights have 11 bits
 // down to 2^-20 of the largest and may grow by 2^8.  Upwards only where the sums so far have
-// shrunk (by `shrunk`; 0: there were none), and not by so much that they could leave fp32's
-// range.  The unit starts at its largest, where hardly a weight fits: the first one that is not
-// zero (of a group whose first values have no width) moves it down.
+// shrunk (by `shrunk`; 0: there were none): then unit_room says how far.  The unit starts at its
+// largest, where hardly a weight fits: the first one that is not zero (of a group whose first
+// values have no width) moves it down.
 __device__ __forceinline__ int unit_up(float most, float shrunk, float unit) {
     if (!(most > 0.f)) return 0;
     const int at = (int)(__float_as_uint(unit) >> 23) - 127;
     int up = 6 - 10 - ((int)(__float_as_uint(most) >> 23) - 127) - at;
-    if (shrunk != 0.f) up = min(up, shrunk == 1.f ? 0 : 40 + 126 - (int)(__float_as_uint(shrunk) >> 23));
+    if (shrunk == 1.f) up = min(up, 0);
     return max(-120 - at, min(kMostUnit - at, up));                  // the unit and its inverse stay normal
 }
+// How far the unit may move up before a sum of magnitude `sum` is past 2^40 of it, where fp32 keeps
+// less of the sum than fp16 of the weights.  2^31 keys add 2^49 at most (2^15 times a code each).
+__device__ __forceinline__ int unit_room(float sum) { return max(0, 40 + 127 - (int)(__float_as_uint(sum) >> 23)); }
 __device__ __forceinline__ float two_to(int i) { return __uint_as_float((uint32_t)(i + 127) << 23); }
 
 // A worker's place on the line: unit u of sequence s at tile k of its T.  A unit takes some
@@ -632,7 +635,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                             for (int r = 0; r < 4; ++r) most = fmaxf(most, x[nt][r][e] * 0x1p-10f * step[r]);
 #pragma unroll
                             for (int off = 4; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-                            const int up = unit_up(most, grown ? shrunk[nt][e] : 1.f, unit[nt][e][g]);
+                            float sum = 0.f;             // the largest so far of the head's lanes, both parts'
+#pragma unroll
+                            for (int i = 4 * g; i < 4 * g + 4; ++i) sum = fmaxf(sum, fmaxf(fabsf(o[nt][i][e]), fabsf(o[nt][i][2 + e])));
+#pragma unroll
+                            for (int off = kTwoParts ? 2 : 4; off < 32; off <<= 1) sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, off));
+                            const int up = min(unit_room(sum), unit_up(most, grown ? shrunk[nt][e] : 1.f, unit[nt][e][g]));
                             const float by = two_to(up / 2), by2 = two_to(up - up / 2);
                             unit[nt][e][g] = unit[nt][e][g] * by * by2;
 #pragma unroll

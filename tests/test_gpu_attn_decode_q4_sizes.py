@@ -116,3 +116,36 @@ def test_one_group_without_width(kda, cuda_device, dtype, n):
     c.upload()
     q = A.randn(35, (H, d), dtype, cuda_device)
     _check(kda, q, c, dtype, n)
+
+
+@pytest.mark.parametrize("n", REQUESTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,H,H_kv", HEADS)
+@pytest.mark.parametrize("first,score,size", [(90, 9, -40), (110, 30, -50), (60, 9, -10), (-60, 9, 20), (60, -9, -20), (-90, -3, 30), (100, 12, -25)])
+def test_sizes_that_move_with_the_scores(kda, cuda_device, dtype, n, d, H, H_kv, first, score, size):
+    """Tile by tile the scores rise or fall by `score` (log2) and the values by `size`.  Heads of half the scores, of their
+    opposite and of none stand beside each other."""
+    tiles = range(min(6, 1 + (first + 116) // -size) if size < 0 else 6)       # down to 2^-116
+    c = _stairs(kda, cuda_device, dtype, d, H, H_kv, [score * i for i in tiles], [first + size * i for i in tiles])
+    q = torch.ones((H, d), dtype=dtype, device=cuda_device)
+    for h, x in enumerate((1, 0.5, -1, 0)):
+        q[h::4] = x
+    _check(kda, q, c, dtype, n)
+
+
+@pytest.mark.parametrize("n", REQUESTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_very_different_sizes(kda, cuda_device, dtype, n, d):
+    """Values in runs of 1 to 60 positions whose sizes are 2^-60 .. 2^60, in many orders, and scores of all kinds."""
+    rng = np.random.RandomState(36)
+    for std in (0.3, 3.0):
+        runs = []
+        while sum(n for n, _ in runs) < 900:
+            runs.append((rng.randint(1, 60), rng.randint(-60, 61)))
+        t = np.concatenate([np.full(n, 2.0 ** e) for n, e in runs])[:900]
+        c = _q4.Paged(37, [900], 1, d, 16, dtype, cuda_device)
+        _scale_values(c, 0, t)
+        c.upload()
+        q = A.randn(38, (8, d), dtype, cuda_device, std)
+        _check(kda, q, c, dtype, n)

@@ -14,8 +14,8 @@
 //
 // K: a code in an fp16 number's lowest bits is that number: the subnormals are n 2^-24, exact
 // operands like any other.  A word's eight codes take four masks and a shift: at bits 4..7
-// a code counts 16-fold, which q's side makes up for.  q is scaled by a power of two for the
-// range of fp16.  (fp32 takes centred codes here too, and q's sum times m + 8 s: what the
+// a code counts 16-fold, which q's side makes up for.  Each group of q is scaled by a power of two
+// for the range of fp16.  (fp32 takes centred codes here too, and q's sum times m + 8 s: what the
 // tensor cores cut off of larger sums would be more than fp32 loses.)
 //
 // V: the products add up over keys, so that a byte of codes has to meet the same byte of the
@@ -391,29 +391,27 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
         }
         uint32_t q[NT][NG][2][4];
         uint32_t qsum[NT];                               // of column n, part t of three, both groups, times scale log2 e
-        float unscale[NT][2], sums[NT][2][NG];           // of heads 2 t and 2 t + 1, times that too; sums: fp32 only
+        float unscale[NT][2][NG], sums[NT][2][NG];       // of heads 2 t and 2 t + 1, times that too; sums: fp32 only
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * kColumns + n % kColumns;
             const bool is_row = r < min(kRows, G - c.u % blocks * kRows);
-            float x[NG][16], most = 0.f;
+            float x[NG][16], undo[NG], sum[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
+                float most = 0.f;
                 raw[nt][g].open(x[g]);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     x[g][e] = is_row ? x[g][e] : 0.f;
                     most = fmaxf(most, fabsf(x[g][e]));
                 }
-            }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // a power of two that brings the largest to 2^14 .. 2^15; its inverse is normal
-            const int up = min(112, 14 - ((int)(__float_as_uint(most) >> 23) - 127));
-            const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-            float undo = __uint_as_float((uint32_t)(127 - up) << 23), sum[NG];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                // a power of two that brings the group's largest to 2^14 .. 2^15; its inverse is normal
+                const int up = min(112, 14 - ((int)(__float_as_uint(most) >> 23) - 127));
+                const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+                undo[g] = __uint_as_float((uint32_t)(127 - up) << 23);
                 sum[g] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sum[g] += x[g][e], x[g][e] *= by;
@@ -436,13 +434,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                unscale[nt][e] = __shfl_sync(0xffffffffu, undo, 4 * (2 * t + e)) * (kTwoParts ? 1.f : 0x1p24f) * sc;
-                if (kTwoParts) {
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) sums[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * t + e)) * sc;
+                for (int g = 0; g < NG; ++g) {
+                    unscale[nt][e][g] = __shfl_sync(0xffffffffu, undo[g], 4 * (2 * t + e)) * (kTwoParts ? 1.f : 0x1p24f) * sc;
+                    if (kTwoParts) sums[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * t + e)) * sc;
                 }
-            }
             const float lower = third(sum[0] * sc, t), upper = NG == 2 ? third(sum[NG - 1] * sc, t) : 0.f;
             qsum[nt] = __float_as_uint(lower) >> 16 | (__float_as_uint(upper) & 0xFFFF0000u);
         }
@@ -475,7 +472,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                 uint32_t scale[2][2];                    // (s, m) of both keys' groups
 #pragma unroll
                 for (int r = 0; r < 2; ++r) load_scales<NG>(scale[r], sb + hf * (S::kScales / 2) + r * (8 * NG));
-                float y[NT][4];                          // sum of s (q . n)
+                float y[NT][4] = {};                     // scores, as they grow; both parts' of a head, in fp32
+                if (!kTwoParts) {                        // sum of m (sum q)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_bf16_k8(y[nt], __byte_perm(scale[0][0], scale[0][NG - 1], 0x7632), __byte_perm(scale[1][0], scale[1][NG - 1], 0x7632), qsum[nt]);
+                }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     uint2 w[2];
@@ -511,28 +513,22 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float step = low_of(scale[k >> 1][g]);
-                            y[nt][k] = g == 0 ? acc[nt][k] * step : fmaf(acc[nt][k], step, y[nt][k]);
+                            y[nt][k] = fmaf(acc[nt][k] * low_of(scale[k >> 1][g]), unscale[nt][k & 1][g], y[nt][k]);
                         }
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float base[4] = {};                  // sum of m (sum q), or of (m + 8 s) (sum q) where the codes are centred
-                    if (kTwoParts) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                base[k] = fmaf(fmaf(8.f, low_of(scale[k >> 1][g]), high_of(scale[k >> 1][g])), sums[nt][k & 1][g], base[k]);
-                    } else {
-                        mma_bf16_k8(base, __byte_perm(scale[0][0], scale[0][NG - 1], 0x7632), __byte_perm(scale[1][0], scale[1][NG - 1], 0x7632), qsum[nt]);
-                    }
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (kTwoParts) y[nt][k] += __shfl_xor_sync(0xffffffffu, y[nt][k], 2);
-                        x[nt][2 * hf + (k >> 1)][k & 1] = fmaf(y[nt][k], unscale[nt][k & 1], base[k]);
+                        float& score = x[nt][2 * hf + (k >> 1)][k & 1];
+                        score = y[nt][k];
+                        if (kTwoParts) {                 // and the sum of (m + 8 s) (sum q), the codes being centred
+                            score += __shfl_xor_sync(0xffffffffu, y[nt][k], 2);
+#pragma unroll
+                            for (int g = 0; g < NG; ++g)
+                                score = fmaf(fmaf(8.f, low_of(scale[k >> 1][g]), high_of(scale[k >> 1][g])), sums[nt][k & 1][g], score);
+                        }
                     }
-                }
             }
             if (live < kKeys) {
 #pragma unroll

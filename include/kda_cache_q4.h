@@ -101,10 +101,12 @@ kda_status_t kda_cache_unpack_q4(const kda_cache_unpack_q4_args *args, void *str
  *    full width, and read once a group, while each request's own tokens are in 4
  *    bits.  Without groups the three are ignored.
  * q and o are of base.dtype.  The keys' scores are the exact products of the codes
- * with q, which bf16 q holds exactly and fp32 q in two 11-bit parts, accumulated
- * in fp32, for |q| up to 2^100 and scores up to 2^27 as there.  A weight times its
- * value's scale is held in fp16 (fp32: in two such parts) for the product with the
- * codes: 11 bits (22), counted from the largest one so far of its head and group,
+ * with q, accumulated in fp32, for |q| up to 2^100 and scores up to 2^27 as there.
+ * bf16 q is held exactly and fp32 q in two 11-bit parts: a channel to 2^-35 (fp32:
+ * 2^-39) of the largest of its 64, if that is coarser.  A weight times its value's
+ * scale is held in fp16 (fp32: in two such parts) for the product with the codes:
+ * 11 bits (22), or multiples of 2^-30 of the largest one so far of its head and
+ * group, if those are coarser,
  * so that values of any size may stand beside each other.  The weights' sum is
  * taken before that rounding.  Positions that a mask hides never reach a result,
  * whatever their codes and scales are.  A position that is NaN makes its key

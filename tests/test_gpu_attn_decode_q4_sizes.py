@@ -149,3 +149,19 @@ def test_values_of_very_different_sizes(kda, cuda_device, dtype, n, d):
         c.upload()
         q = A.randn(38, (8, d), dtype, cuda_device, std)
         _check(kda, q, c, dtype, n)
+
+
+@pytest.mark.parametrize("n", REQUESTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [4, 16])
+@pytest.mark.parametrize("size", [0, 15, 27, 30, 60])
+@pytest.mark.parametrize("group", [0, 1])
+def test_queries_of_different_sizes_in_the_two_groups(kda, cuda_device, dtype, n, H, size, group):
+    """One group's channels of the queries are 2^size times as large, and its keys are zeros: the scores are the other's."""
+    d, K = 128, 200
+    c = _q4.Paged(39, [K], 1, d, 16, dtype, cuda_device)
+    c.s[0][..., group], c.m[0][..., group] = c.s[0][..., group] * 0, c.m[0][..., group] * 0
+    c.upload()
+    q = A.randn(40, (H, d), dtype, cuda_device)
+    q[..., 64 * group:64 * group + 64] *= 2.0 ** size
+    _check(kda, q, c, dtype, n)                  # (the bound: keys of zero times any query are zero)

@@ -23,20 +23,19 @@
 // byte of it, and one fp16 instruction n - 8 of each of its codes.  A product's rows are the
 // keys in the order in which that hands them out.  Weights times scales are rounded to fp16: 11
 // bits, counted from the largest so far of each head and group (a power of two, moved like the
-// weights' own maximum).
+// weights' own maximum: unit_up).
 //
-// Bound, on long sequences, by the cache's bytes and the instructions that take codes apart: 315
+// Bound, on long sequences, by the cache's bytes and the instructions that take codes apart: 321
 // a warp for 16 keys of d = 128, 104 of them (by the source) masks, permutations and conversions of
-// codes; the
-// ALU and issue slots are 55% and 64% busy, DRAM 90% of the measured copy rate between the
-// beginning and the end.  One sequence of 2^20 tokens, 8 heads: 0.22 ms (5.5 TB/s), of which
-// 23 us do not grow with the length; in bf16 it takes 0.69 ms.  512
-// sequences of up to 2048: 127 us (4.7 TB/s).  16 query heads a key/value head: 0.33 ms, where
-// twice the rows make arithmetic of it (0.41 ms in units of eight).  7 requests of up to 700
+// codes; the ALU and issue slots are 54% and 64% busy, DRAM 89% of the measured copy rate between
+// the beginning and the end.  One sequence of 2^20 tokens, 8 key/value heads: 0.22 ms (5.4 TB/s), of
+// which 23 us do not grow with the length; in bf16 it takes 0.68 ms (32 query heads).  512
+// sequences of up to 2048: 128 us (4.7 TB/s).  16 query heads a key/value head: 0.34 ms, where
+// twice the rows make arithmetic of it (0.42 ms in units of eight).  7 requests of up to 700
 // tokens: 15 us, a chain of about ten trips to memory in two kernels.
 //
-// Twelve warps a block, three a scheduler, have 168 registers (one sequence of 2^20 203 us
-// without the join; sixteen with 128, 209 us).  The copies are cp.async by each warp for itself:
+// Twelve warps a block, three a scheduler, have 168 registers (one sequence of 2^20 223 us;
+// sixteen with 128, 237 us).  The copies are cp.async by each warp for itself:
 // a copy warp that served the others with bulk and tensor copies of 1 KB took 0.57 ms, since such
 // copies leave a warp one lane at a time.
 #include <cuda_fp16.h>
@@ -783,7 +782,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) decode_q4_kernel(const __grid_c
 // prefix's blocks and then the pieces.  A row is one warp's where units have few parts (narrow).
 // Where they have many (16 pieces a unit on average), a thread block's warps share a row's: every
 // block counts the open units itself and takes its share of their rows.  One sequence of 2^20
-// tokens: 219 us, all narrow 262 us; 512 of up to 2048: 127 us, all wide 180 us.
+// tokens: 223 us, all narrow 264 us; 512 of up to 2048: 128 us, all wide 173 us.
 struct OpenRow {
     int4 open;            // sequence, unit, last piece, prefix parts
     int64_t c0;           // the piece in which the unit begins

@@ -106,11 +106,10 @@ kda_status_t kda_cache_unpack_q4(const kda_cache_unpack_q4_args *args, void *str
  * 2^-39) of the largest of its 64, if that is coarser.  A weight times its value's
  * scale is held in fp16 (fp32: in two such parts) for the product with the codes:
  * 11 bits (22), or multiples of 2^-30 of the largest one so far of its head and
- * group, if those are coarser,
- * so that values of any size may stand beside each other.  The weights' sum is
- * taken before that rounding.  Positions that a mask hides never reach a result,
- * whatever their codes and scales are.  A position that is NaN makes its key
- * group's heads NaN, or its value group's channels.
+ * group, if those are coarser, so that values of any size may stand beside each
+ * other.  The weights' sum is taken before that rounding.  Positions that a mask
+ * hides never reach a result, whatever their codes and scales are.  A position
+ * that is NaN makes its key group's heads NaN, or its value group's channels.
  */
 typedef struct kda_attn_decode_q4_args {
     kda_attn_decode_args base;

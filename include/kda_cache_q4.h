@@ -19,9 +19,10 @@
  * otherwise:  m = min x, rounded down to bf16;  s = (max x - m) / 15, rounded up to
  * bf16;  code = (x - m) / s, rounded to the nearest integer, ties to even, and cut
  * to 0 .. 15 (0 where s is 0).  So x and its value are at most half a step of s
- * apart, and the roundings.  A group that holds an infinity or NaN, or whose width
- * or bounds leave the range of fp32 or bf16, gets s = 0 and m = NaN: all of it
- * reads as NaN.
+ * apart, and the roundings (m + 15 s, which can be above max x by these, is infinite
+ * where it passes the type's largest number).  A group that holds an infinity or
+ * NaN, or whose width or bounds leave the range of fp32 or bf16, gets s = 0 and m =
+ * NaN: all of it reads as NaN.
  *
  * Conventions: those of kda.h and kda_attention.h.  All four tensors are 16-byte
  * aligned, and n_blocks * block_size * H_kv <= 2^31 - 1.
